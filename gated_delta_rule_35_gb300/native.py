@@ -27,7 +27,8 @@ EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_stag
            "gdn_chunk_fwd_launches", "gdn_chunk_fwd_profiled", "gdn_check_device_status",
            "gdn_chunk_fwd_noalloc", "gdn_decode_step", "gdn_decode_step_launches",
            "gdn_chunk_fwd_ex", "gdn_decode_step_ex", "gdn_chunk_fwd_host_bytes",
-           "gdn_chunk_fwd_host", "gdn_debug_arm_stall", "gdn_status_string", "gdn_version")
+           "gdn_chunk_fwd_host", "gdn_conv_fwd", "gdn_scan_fwd", "gdn_scan_workspace_bytes",
+           "gdn_group_norm", "gdn_debug_arm_stall", "gdn_status_string", "gdn_version")
 
 
 class GdnError(RuntimeError):
@@ -96,6 +97,15 @@ def lib():
         L.gdn_decode_step_launches.restype = ctypes.c_int32
         L.gdn_decode_step_launches.argtypes = [pp, ctypes.POINTER(ctypes.c_char_p),
                                                ctypes.c_int32]
+        # the problems of these (mixer.py) are structures of their own
+        L.gdn_conv_fwd.restype = ctypes.c_int
+        L.gdn_conv_fwd.argtypes = [vp] * 9
+        L.gdn_scan_workspace_bytes.restype = sz
+        L.gdn_scan_workspace_bytes.argtypes = [vp]
+        L.gdn_scan_fwd.restype = ctypes.c_int
+        L.gdn_scan_fwd.argtypes = [vp] * 14 + [sz, vp]
+        L.gdn_group_norm.restype = ctypes.c_int
+        L.gdn_group_norm.argtypes = [vp] * 8
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_version.restype = ctypes.c_uint32

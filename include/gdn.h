@@ -345,6 +345,129 @@ GDN_API gdn_status gdn_decode_step_ex(const gdn_problem *p,
                                       const float *state_in, float *state_out,
                                       const gdn_output_norm *norm, void *o, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the recurrence in a mixing layer: the short causal
+ * convolution before it, the selective state space scan beside it and the
+ * group norm behind it.
+ *
+ * Conventions of these three, beyond those at the top of this file:
+ *  - Tensors of tokens are channels-last. The inputs marked "strided" may be a
+ *    slice of a wider tensor, such as one part of a fused projection: their
+ *    innermost axes are contiguous, the batch and token strides are given in
+ *    the problem (in elements, >= 0), and the pointer needs only the alignment
+ *    of its element. Where pointer and strides are multiples of 16 bytes and
+ *    the row is a whole number of 16-byte pieces the kernels load 16 bytes at a
+ *    time, else element by element, with the same results. Every other pointer
+ *    but lengths (4 bytes) is 16-byte aligned and its tensor contiguous.
+ *  - lengths (or NULL: T for every sequence): [B] int32 on the device, the valid
+ *    tokens of each sequence of a padded batch; values outside [0, T] are taken
+ *    as the nearest bound. Rows at or past the length are never used, whatever
+ *    they hold (NaN included), and the outputs' rows there are left as they
+ *    were. A sequence of length 0 passes its state through.
+ *  - A state may be updated in place (the two state pointers equal); a NULL
+ *    state_in is a zero state, a NULL state_out is not written. Other overlaps
+ *    of an output with an input or another output give GDN_ERR_INVALID_ARG
+ *    (gdn_group_norm documents its one exception).
+ *  - A call enqueues its kernels on `stream` and keeps nothing: it can be captured
+ *    into a CUDA graph, and calls on different streams are independent (with
+ *    separate workspaces where one is taken). Results do not depend on the
+ *    order in which blocks run: the same call gives the same bits.
+ *  - Arithmetic is fp32 whatever the dtype; each output is rounded once.
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+    GDN_ACT_NONE = 0,
+    GDN_ACT_SILU = 1,      /* v * sigmoid(v) */
+    GDN_ACT_SIGMOID = 2    /* sigmoid(v) = 1 / (1 + exp(-v)) */
+} gdn_act;
+
+/* Causal depthwise convolution over tokens ("WarpDrive" page, kernel 2,
+ * causal_conv1d; with its window state as in the "KdaSplit" decode kernel page):
+ *
+ *   y[b,t,c] = act(bias[c] + sum_{k < W} weight[c,k] x[b, t - W + 1 + k, c])
+ *
+ * where x at t < 0 is the window state: state_in[b, W - 1 + t, c], the last W - 1
+ * inputs before the first token. state_out receives the last W - 1 inputs up to
+ * the last valid token (with fewer than W - 1 new tokens the older ones move up).
+ *  - W in {2, 3, 4} (else GDN_ERR_UNSUPPORTED); any C.
+ *  - x [B,T,C] strided, y [B,T,C], state_in / state_out [B,W-1,C] in `dtype`;
+ *    weight [C,W], bias [C] (or NULL) fp32.
+ *  - One call serves prompts and single tokens (T = 1, state in place). T = 0
+ *    copies the state. */
+typedef struct {
+    int32_t B, T, C, W;
+    int32_t dtype;   /* gdn_dtype */
+    int32_t act;     /* gdn_act */
+    int64_t x_stride_b, x_stride_t;
+} gdn_conv_problem;
+
+GDN_API gdn_status gdn_conv_fwd(const gdn_conv_problem *p, const void *x, const float *weight,
+                                const float *bias, const void *state_in, const int32_t *lengths,
+                                void *y, void *state_out, void *stream);
+
+/* Selective state space scan: every channel d carries N states with a diagonal
+ * decay, the step Delta, the input row B and the output row C chosen per token:
+ *
+ *   Delta = dt[b,t,d] + dt_bias[d], through log(1 + exp(.)) with GDN_SCAN_SOFTPLUS
+ *   h[d,n] <- exp(Delta A[d,n]) h[d,n] + Delta x[b,t,d] B[b,t,g,n]
+ *   y[b,t,d] = (sum_n C[b,t,g,n] h[d,n] + D[d] x[b,t,d]) * silu(z[b,t,d])
+ *
+ * with g = d / (D / G) the channel's group of B and C rows.
+ *  - D a multiple of G, N in 1..128 (else GDN_ERR_INVALID_ARG / _UNSUPPORTED).
+ *  - x, dt, z [B,T,D] and Bm, Cm [B,T,G,N] in `dtype`, each strided; z may be NULL
+ *    (no gate). A [D,N], skip (the D of the formula) [D] or NULL, dt_bias [D] or
+ *    NULL: fp32 and finite. y [B,T,D] in `dtype`; h0, h_final [B,D,N] fp32.
+ *  - One call serves prompts and single tokens (T = 1, h0 and h_final equal). T
+ *    = 0 copies the state.
+ *  - workspace: gdn_scan_workspace_bytes(p) bytes of scratch, 0 for problems that
+ *    need none (then it may be NULL). Long sequences of few channels are cut
+ *    into segments whose states pass through it. Two calls that may overlap on
+ *    the GPU (two captured graphs among them) need one each. */
+enum { GDN_SCAN_SOFTPLUS = 1 };
+
+typedef struct {
+    int32_t B, T, D, N, G;
+    int32_t dtype;   /* gdn_dtype */
+    int32_t flags;   /* GDN_SCAN_* bits */
+    int32_t reserved;   /* 0 */
+    int64_t x_stride_b, x_stride_t, dt_stride_b, dt_stride_t, z_stride_b, z_stride_t;
+    int64_t b_stride_b, b_stride_t, c_stride_b, c_stride_t;
+} gdn_scan_problem;
+
+/* Depends on the sizes and the dtype alone; SIZE_MAX for an invalid problem. */
+GDN_API size_t gdn_scan_workspace_bytes(const gdn_scan_problem *p);
+
+GDN_API gdn_status gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const void *dt,
+                                const float *A, const void *Bm, const void *Cm, const float *skip,
+                                const void *z, const float *dt_bias, const float *h0,
+                                const int32_t *lengths, void *y, float *h_final, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* Group norm of channels-last rows with an activation: the C channels form G
+ * groups of C / G, and mean and variance (biased) are taken over the valid tokens
+ * of a sequence and the channels of a group. T = 1 with one token per "sequence"
+ * is the norm over heads of a mixer's output, T > 1 the norm over whole sequences.
+ *
+ *   v = (x - mean) / sqrt(var + eps) * weight[c] + bias[c]
+ *   y = act(v)            without a gate
+ *   y = v * act(gate)     with one
+ *
+ *  - C a multiple of G (else GDN_ERR_INVALID_ARG). x, gate (or NULL) [B,T,C] strided,
+ *    y [B,T,C] in `dtype`; weight, bias [C] fp32 or NULL (1 and 0); eps >= 0.
+ *  - y == x with x contiguous normalises in place. */
+typedef struct {
+    int32_t B, T, C, G;
+    int32_t dtype;   /* gdn_dtype */
+    int32_t act;     /* gdn_act */
+    float eps;
+    int32_t reserved;   /* 0 */
+    int64_t x_stride_b, x_stride_t, gate_stride_b, gate_stride_t;
+} gdn_group_norm_problem;
+
+GDN_API gdn_status gdn_group_norm(const gdn_group_norm_problem *p, const void *x,
+                                  const float *weight, const float *bias, const void *gate,
+                                  const int32_t *lengths, void *y, void *stream);
+
 /* Static description of a status code. Never NULL. */
 GDN_API const char *gdn_status_string(gdn_status s);
 

@@ -1,0 +1,52 @@
+"""Elementwise error bounds of the mixer operators' tests, from rounding analysis.
+
+u = 2^-24 is fp32's rounding. An output is rounded once to its type, off by at
+most eps(type) / 2 of its value. __expf(v) is within 2 + 1.173 |v| ulp (CUDA's
+stated bound) and __fdividef within 2 ulp, an ulp being 2u at most, so a
+sigmoid(v) is off by at most (6 + 1.2 |v|) 2u of itself, and so is v sigmoid(v)
+beside the error of v (slope of silu at most 1.1, of sigmoid 0.25)."""
+import numpy as np
+import torch
+
+U = 2.0 ** -24
+
+
+def act_error(v, ev, y, name):
+    """Error of act(v) where v is off by ev."""
+    if name == "none":
+        return ev
+    slope = 1.1 if name == "silu" else 0.25
+    return slope * ev + abs(y) * (6 + 1.2 * abs(v)) * 2 * U
+
+
+def conv_bound(y, v, S, W, name):
+    return act_error(v, (W + 1) * U * S, y, name)
+
+
+def norm_bound(y, v, xhat, size, weight, name, gate=None, act=None):
+    """Sums of a group add at most 256 terms in a row (threads, then trees): the mean
+    is off by 256 u mean|x|, the deviation by that relative error of 256 u and a
+    root within 2 ulp."""
+    w = 1.0 if weight is None else abs(weight)
+    ev = w * (256 * U * size + abs(xhat) * (256 * U + 4 * U) + 4 * U * abs(xhat)) + 2 * U * abs(v)
+    if gate is None:
+        return act_error(v, ev, y, name)
+    return abs(act) * ev + abs(y) * (6 + 1.2 * abs(gate)) * 2 * U
+
+
+def check(got, want, bound, dtype, what=""):
+    """got (a tensor) within the bound and one rounding of want, where want is a number;
+    tiny covers results below the normal range."""
+    got = got.detach().cpu().double().numpy()
+    at = ~np.isnan(want)
+    half = torch.finfo(dtype).eps / 2
+    lim = bound + half * (abs(want) + bound) + 1e-35
+    assert np.isfinite(got[at]).all(), what
+    off = abs(got - want)[at] / lim[at]
+    assert off.size == 0 or off.max() <= 1.0, f"{what}: {off.max():.3f} of the bound"
+
+
+def untouched(got, want, fill):
+    """The rows outside the sequences (NaN in want) still hold fill."""
+    at = np.isnan(want)
+    assert (got.detach().cpu().float().numpy()[at] == fill).all()
