@@ -1,16 +1,21 @@
 // Causal depthwise convolution over tokens with its window state: gdn_conv_fwd of
 // include/gdn.h.
 //
-// A thread owns one channel and a run of tokens and keeps the W - 1 previous
-// inputs in registers, so that each input is loaded once per run (plus the W - 1
-// before the run).
+// Bound by memory: one read of x and one write of y. A thread owns a piece of V
+// channels (16 bytes, or one channel where rows are not whole 16-byte pieces) over a
+// run of tokens, with its weights and the W - 1 previous inputs in registers, so x is
+// read once but for the W - 1 tokens before each run. Each turn of the loop
+// issues U tokens' loads before the first use.
 #include "mixer.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kRun = 16;        // tokens per thread
 constexpr int kThreads = 128;
+constexpr int kUnroll = 8;      // tokens whose loads are in flight together
+constexpr int kMaxRun = 32;     // tokens per thread at most; a call of several runs has kUnroll or more to
+                                // each, so that only the first run reads the window state
+static_assert(kUnroll >= 3, "W - 1");
 
 template <typename E>
 struct ConvParams {
@@ -20,51 +25,83 @@ struct ConvParams {
     const int32_t *lengths;
     E *y, *state_out;
     int64_t sb, st;
-    int T, C, act;
+    int T, C, act, run;
 };
 
-// Input at token t of sequence b, channel c; t >= -(W - 1), tokens before 0 come
+// Inputs at token t of sequence b, channels c..; t >= -(W - 1), tokens before 0 come
 // from the window state.
-template <typename E, int W>
-__device__ __forceinline__ E input_at(const ConvParams<E> &p, int b, int t, int c) {
-    if (t >= 0) return p.x[b * p.sb + t * p.st + c];
-    return p.state_in ? p.state_in[(static_cast<int64_t>(b) * (W - 1) + W - 1 + t) * p.C + c]
-                      : from_f32<E>(0.f);
+template <typename E, int W, int V>
+__device__ __forceinline__ void input_at(Piece<E, V> &q, const ConvParams<E> &p, int64_t b, int t,
+                                         int c) {
+    if (t >= 0)
+        q.load(p.x + b * p.sb + t * p.st + c);
+    else if (p.state_in)
+        q.load_rw(p.state_in + (b * (W - 1) + W - 1 + t) * p.C + c);
+    else
+        q.zero();
 }
 
-template <typename E, int W>
+template <typename E, int W, int V, int U>
 __global__ void __launch_bounds__(kThreads) gdn_conv_kernel(const ConvParams<E> p) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    const int b = blockIdx.z, t0 = blockIdx.y * kRun;
-    if (c >= p.C) return;
+    const int cv = p.C / V;                            // pieces of a row
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    const int c = i % cv * V, t0 = i / cv * p.run;     // runs of a piece lie cv threads apart
+    const int64_t b = blockIdx.y;
+    if (t0 >= max(p.T, 1)) return;
     const int n = valid_tokens(p.lengths, b, p.T);
     if (t0 < n) {
-        float w[W], win[W];
+        float w[V * W], bias[V], win[W - 1][V];
+        load_f32<V * W>(p.w + static_cast<int64_t>(c) * W, w);   // [V][W]
+        if (p.bias) {
+            load_f32<V>(p.bias + c, bias);
+        } else {
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k] = p.w[static_cast<int64_t>(c) * W + k];
-        const float bias = p.bias ? p.bias[c] : 0.f;
+            for (int j = 0; j < V; ++j) bias[j] = 0.f;
+        }
+        Piece<E, V> q[U];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) win[k + 1] = to_f32(input_at<E, W>(p, b, t0 - W + 1 + k, c));
-        const int t1 = min(t0 + kRun, n);
-        for (int t = t0; t < t1; ++t) {
+        for (int k = 0; k < W - 1; ++k) {
+            Piece<E, V> before;
+            input_at<E, W, V>(before, p, b, t0 - W + 1 + k, c);
+            before.widen(win[k]);
+        }
+        const int t1 = min(t0 + p.run, n);
+        const E *x = p.x + b * p.sb + c;
+        E *y = p.y + b * p.T * p.C + c;
+        for (int t = t0; t < t1; t += U) {
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) win[k] = win[k + 1];
-            win[W - 1] = to_f32(p.x[b * p.sb + t * p.st + c]);
-            float v = bias;
+            for (int u = 0; u < U; ++u)
+                if (t + u < t1) q[u].load(x + (t + u) * p.st);
 #pragma unroll
-            for (int k = 0; k < W; ++k) v = fmaf(w[k], win[k], v);
-            p.y[(static_cast<int64_t>(b) * p.T + t) * p.C + c] = from_f32<E>(activate(v, p.act));
+            for (int u = 0; u < U; ++u) {
+                if (t + u < t1) {
+                    float in[V], out[V];
+                    q[u].widen(in);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        float v = bias[j];
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k) v = fmaf(w[j * W + k], win[k][j], v);
+                        out[j] = activate(fmaf(w[j * W + W - 1], in[j], v), p.act);
+#pragma unroll
+                        for (int k = 0; k < W - 2; ++k) win[k][j] = win[k + 1][j];
+                        win[W - 2][j] = in[j];
+                    }
+                    Piece<E, V> r;
+                    r.round(out);
+                    r.store(y + static_cast<int64_t>(t + u) * p.C);
+                }
+            }
         }
     }
-    // The thread that read this channel's state_in writes its state_out, after
+    // The thread that read this piece of state_in writes its state_out, after
     // reading all of it: the two may be the same buffer.
     if (t0 == 0 && p.state_out) {
-        E last[W - 1];
+        Piece<E, V> last[W - 1];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) last[k] = input_at<E, W>(p, b, n - W + 1 + k, c);
+        for (int k = 0; k < W - 1; ++k) input_at<E, W, V>(last[k], p, b, n - W + 1 + k, c);
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-            p.state_out[(static_cast<int64_t>(b) * (W - 1) + k) * p.C + c] = last[k];
+        for (int k = 0; k < W - 1; ++k) last[k].store(p.state_out + (b * (W - 1) + k) * p.C + c);
     }
 }
 
@@ -76,15 +113,32 @@ gdn_status check(const gdn_conv_problem *p) {
     if (p->act != GDN_ACT_NONE && p->act != GDN_ACT_SILU && p->act != GDN_ACT_SIGMOID)
         return GDN_ERR_INVALID_ARG;
     if (p->W < 2 || p->W > 4) return GDN_ERR_UNSUPPORTED;
-    if (p->B > 65535 || p->T > 65535 * kRun) return GDN_ERR_UNSUPPORTED;
+    if (p->B > 65535 || static_cast<int64_t>(p->C) * p->T > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
-template <typename E, int W>
-cudaError_t launch(const gdn_conv_problem *pr, const ConvParams<E> &p, cudaStream_t s) {
-    const dim3 grid((pr->C + kThreads - 1) / kThreads, pr->T ? (pr->T + kRun - 1) / kRun : 1, pr->B);
-    gdn_conv_kernel<E, W><<<grid, kThreads, 0, s>>>(p);
+template <typename E, int W, int V>
+cudaError_t launch(const gdn_conv_problem *pr, ConvParams<E> &p, cudaStream_t s) {
+    // Runs of kMaxRun tokens re-read (W - 1) / 32 of x; shorter ones where those would
+    // leave SMs without their four blocks, a single one for a few tokens.
+    const int64_t cv = pr->C / V, T = pr->T > 0 ? pr->T : 1;
+    p.run = kMaxRun;
+    while (p.run > kUnroll && (T + p.run - 1) / p.run * cv * pr->B < 152LL * 4 * kThreads) p.run /= 2;
+    if (T <= kUnroll / 2) p.run = static_cast<int>(T);
+    const int64_t threads = (T + p.run - 1) / p.run * cv;
+    const dim3 grid(static_cast<unsigned>((threads + kThreads - 1) / kThreads), pr->B);
+    if (T <= kUnroll / 2)
+        gdn_conv_kernel<E, W, V, 1><<<grid, kThreads, 0, s>>>(p);
+    else
+        gdn_conv_kernel<E, W, V, kUnroll><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+template <typename E, int W>
+cudaError_t launch_pieces(const gdn_conv_problem *pr, ConvParams<E> &p, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(E);
+    return pieces16(p.x, pr->B, pr->T, pr->C, p.sb, p.st, sizeof(E)) ? launch<E, W, V>(pr, p, s)
+                                                                     : launch<E, W, 1>(pr, p, s);
 }
 
 template <typename E>
@@ -105,9 +159,9 @@ cudaError_t dispatch(const gdn_conv_problem *pr, const void *x, const float *w, 
     p.C = pr->C;
     p.act = pr->act;
     switch (pr->W) {
-        case 2: return launch<E, 2>(pr, p, s);
-        case 3: return launch<E, 3>(pr, p, s);
-        default: return launch<E, 4>(pr, p, s);
+        case 2: return launch_pieces<E, 2>(pr, p, s);
+        case 3: return launch_pieces<E, 3>(pr, p, s);
+        default: return launch_pieces<E, 4>(pr, p, s);
     }
 }
 

@@ -2,6 +2,9 @@
 // activations, 16-byte pieces, and the host's pointer checks.
 #pragma once
 
+#include <cstring>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "gdn_internal.h"
@@ -31,6 +34,66 @@ __device__ __forceinline__ float activate(float v, int act) {
 
 __device__ __forceinline__ int valid_tokens(const int32_t *lengths, int b, int T) {
     return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+// V elements moved as one piece (16 bytes, or a single element) and widened to fp32.
+template <typename E, int V>
+struct Piece {
+    static_assert(V == 1 || V * sizeof(E) == 16, "one element or 16 bytes");
+    using Raw = typename std::conditional<V == 1, E, uint4>::type;
+    Raw raw;
+    __device__ __forceinline__ void load(const E *p) { raw = __ldg(reinterpret_cast<const Raw *>(p)); }
+    // through the coherent path: for memory that this launch also writes
+    __device__ __forceinline__ void load_rw(const E *p) { raw = *reinterpret_cast<const Raw *>(p); }
+    __device__ __forceinline__ void store(E *p) const { *reinterpret_cast<Raw *>(p) = raw; }
+    __device__ __forceinline__ void zero() { memset(&raw, 0, sizeof(raw)); }
+    __device__ __forceinline__ void widen(float (&f)[V]) const {
+        if constexpr (V == 1) {
+            f[0] = to_f32(raw);
+        } else if constexpr (sizeof(E) == 4) {
+            f[0] = __uint_as_float(raw.x); f[1] = __uint_as_float(raw.y);
+            f[2] = __uint_as_float(raw.z); f[3] = __uint_as_float(raw.w);
+        } else {
+            // bf16's bits are the high half of the fp32's
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void round(const float (&f)[V]) {
+        if constexpr (V == 1) {
+            raw = from_f32<E>(f[0]);
+        } else if constexpr (sizeof(E) == 4) {
+            raw = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                             __float_as_uint(f[3]));
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            raw = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+};
+
+// Widened copies of V consecutive fp32 parameters (16-byte aligned when V is a multiple of 4).
+template <int V>
+__device__ __forceinline__ void load_f32(const float *p, float (&f)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 q = __ldg(reinterpret_cast<const float4 *>(p) + i);
+            f[4 * i] = q.x; f[4 * i + 1] = q.y; f[4 * i + 2] = q.z; f[4 * i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = __ldg(p + i);
+    }
 }
 
 // A byte range, for the overlap checks of the C entries.

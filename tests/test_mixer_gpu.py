@@ -431,7 +431,7 @@ def test_wrapper_refusals():
         (TypeError, lambda: gdn.conv_fwd(x, w.bfloat16())),
         (TypeError, lambda: gdn.conv_fwd(x.half(), w)),
         (ValueError, lambda: gdn.conv_fwd(x, w, state=st[:, :2])),
-        (ValueError, lambda: gdn.conv_fwd(x, w, state=st.bfloat16())),
+        (TypeError, lambda: gdn.conv_fwd(x, w, state=st.bfloat16())),
         (TypeError, lambda: gdn.conv_fwd(x, w, lengths=n.long())),
         (ValueError, lambda: gdn.conv_fwd(x, w, lengths=n[:1])),
         (ValueError, lambda: gdn.conv_fwd(x, w, lengths=n.cpu())),
