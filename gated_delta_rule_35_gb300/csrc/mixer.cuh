@@ -19,17 +19,65 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(v);
 }
 
-// 1 / (1 + exp(-v)), as e / (1 + e) with e = exp(-|v|) for v < 0: no overflow, and full
-// relative accuracy down to the smallest normal result.
-__device__ __forceinline__ float sigmoid(float v) {
-    const float e = __expf(-fabsf(v));
-    return __fdividef(v < 0.f ? e : 1.f, 1.f + e);
+// Two fp32 values in one 64-bit register pair: one instruction works on both.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
+__device__ __forceinline__ void unpack2(F2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^v and 1 / v of the special function unit, results below 2^-126 flushed to 0
+// (without the scaling instructions that keep them).
+__device__ __forceinline__ float exp2_ftz(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_ftz(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 1 / (1 + exp(-v)). Far below 0 the exponential is inf and the quotient 0: what is lost
+// there is below 2^-126.
+__device__ __forceinline__ float sigmoid(float v) { return rcp_ftz(1.f + exp2_ftz(-kLog2e * v)); }
 
 __device__ __forceinline__ float activate(float v, int act) {
     if (act == GDN_ACT_NONE) return v;
     const float s = sigmoid(v);
     return act == GDN_ACT_SILU ? v * s : s;
+}
+
+// activate() of two values.
+__device__ __forceinline__ F2 activate2(F2 v, int act) {
+    if (act == GDN_ACT_NONE) return v;
+    float a, b;
+    unpack2(mul2(v, pack2(-kLog2e, -kLog2e)), a, b);
+    unpack2(add2(pack2(exp2_ftz(a), exp2_ftz(b)), pack2(1.f, 1.f)), a, b);
+    const F2 s = pack2(rcp_ftz(a), rcp_ftz(b));
+    return act == GDN_ACT_SILU ? mul2(v, s) : s;
 }
 
 __device__ __forceinline__ int valid_tokens(const int32_t *lengths, int b, int T) {
@@ -94,6 +142,16 @@ __device__ __forceinline__ void load_f32(const float *p, float (&f)[V]) {
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = __ldg(p + i);
     }
+}
+
+// Asynchronous 16-byte copies from global to shared memory, in groups.
+__device__ __forceinline__ void copy16_async(void *smem, const void *g) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(g) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A byte range, for the overlap checks of the C entries.

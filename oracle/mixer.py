@@ -84,7 +84,8 @@ def scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=False, h0=N
             o = o + skip
             if z is not None:
                 g = act(z[b, t], "silu")
-                eo = abs(g) * (eo + abs(o) * (6 + 1.2 * abs(z[b, t])) * 2 * unit)
+                eo = abs(g) * (eo + abs(o) * (6 + 1.2 * abs(z[b, t])) * 2 * unit) \
+                    + abs(o * z[b, t]) * 2.0 ** -126   # a sigmoid below the normal range is 0
                 o = o * g
             y[b, t], Ey[b, t] = o, eo
     return y, h, Ey, E

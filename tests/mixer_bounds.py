@@ -4,11 +4,14 @@ u = 2^-24 is fp32's rounding. An output is rounded once to its type, off by at
 most eps(type) / 2 of its value. __expf(v) is within 2 + 1.173 |v| ulp (CUDA's
 stated bound) and __fdividef within 2 ulp, an ulp being 2u at most, so a
 sigmoid(v) is off by at most (6 + 1.2 |v|) 2u of itself, and so is v sigmoid(v)
-beside the error of v (slope of silu at most 1.1, of sigmoid 0.25)."""
+beside the error of v (slope of silu at most 1.1, of sigmoid 0.25). The quotient
+1 / (1 + exp(-v)) is flushed to 0 below fp32's normal range: what it multiplies is then
+off by that times 2^-126 at most (TINY)."""
 import numpy as np
 import torch
 
 U = 2.0 ** -24
+TINY = 2.0 ** -126
 
 
 def act_error(v, ev, y, name):
@@ -16,7 +19,7 @@ def act_error(v, ev, y, name):
     if name == "none":
         return ev
     slope = 1.1 if name == "silu" else 0.25
-    return slope * ev + abs(y) * (6 + 1.2 * abs(v)) * 2 * U
+    return slope * ev + abs(y) * (6 + 1.2 * abs(v)) * 2 * U + np.maximum(1, abs(v)) * TINY
 
 
 def conv_bound(y, v, S, W, name):
@@ -31,7 +34,7 @@ def norm_bound(y, v, xhat, size, weight, name, gate=None, act=None):
     ev = w * (256 * U * size + abs(xhat) * (256 * U + 4 * U) + 4 * U * abs(xhat)) + 2 * U * abs(v)
     if gate is None:
         return act_error(v, ev, y, name)
-    return abs(act) * ev + abs(y) * (6 + 1.2 * abs(gate)) * 2 * U
+    return abs(act) * ev + abs(y) * (6 + 1.2 * abs(gate)) * 2 * U + abs(v) * np.maximum(1, abs(gate)) * TINY
 
 
 def check(got, want, bound, dtype, what=""):
