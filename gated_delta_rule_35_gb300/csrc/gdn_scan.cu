@@ -1,13 +1,15 @@
 // Selective state space scan: gdn_scan_fwd of include/gdn.h.
 //
-// A thread owns one channel with all of its N states in registers and walks the
-// tokens in order.
+// Two kernels by length: gdn_scan_step_kernel for a few tokens (bound by the state's
+// traffic) and gdn_scan_kernel for prompts (bound by arithmetic: N exponentials and 5 N
+// multiply-adds per token and channel against 4 values moved).
 #include "mixer.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kStepTokens = 8;      // up to here the step kernel
 
 template <typename E>
 struct ScanParams {
@@ -17,48 +19,358 @@ struct ScanParams {
     E *y;
     float *h_final;
     int64_t x_sb, x_st, dt_sb, dt_st, z_sb, z_st, b_sb, b_st, c_sb, c_st;
-    int T, D, N, G, softplus;
+    int B, T, D, N, G, softplus;
+    int rows16;          // B and C rows are whole 16-byte pieces
+    // Segments of seg tokens each; with more than one, the state at the end of a
+    // segment that started from zero (the first one: from h0), h0 itself behind those,
+    // and each segment's sum of Delta.
+    int segs, seg;
+    float *seg_h, *seg_dt;      // [B][segs][D][N], [B][segs][D]
 };
 
-// log(1 + exp(v)) = max(v, 0) + log1p(exp(-|v|)).
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), with log1p(e) = 2 atanh(s),
+// s = e / (2 + e) <= 1/3, by the series s (1 + s^2/3 + s^4/5 + ...) through s^13: the rest
+// is below 2e-8 of it, so small Delta keep their relative accuracy.
 __device__ __forceinline__ float softplus(float v) {
-    return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
+    const float e = exp2_ftz(-kLog2e * fabsf(v));
+    const float s = e * rcp_ftz(2.f + e), q = s * s;
+    float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+    r = fmaf(q, r, 1.f / 9.f);
+    r = fmaf(q, r, 1.f / 7.f);
+    r = fmaf(q, r, 1.f / 5.f);
+    r = fmaf(q, r, 1.f / 3.f);
+    r = fmaf(q, r, 1.f);
+    return fmaf(2.f * s, r, fmaxf(v, 0.f));
 }
 
-template <typename E, int NP>
-__global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> p) {
-    const int d = blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y;
-    if (d >= p.D) return;
-    const int n = valid_tokens(p.lengths, b, p.T);
-    const int g = d / (p.D / p.G);
-    const int64_t row = (static_cast<int64_t>(b) * p.D + d) * p.N;
-    float h[NP];
+// ----------------------------------------------------------------- a few tokens
+//
+// L = NP / 4 lanes share a channel, four states to a lane, and each thread advances
+// kBatch sequences, so their states' loads are in flight together and A is read
+// once for all of them.
+constexpr int kBatch = 4;
+
+template <typename E, int NP, int NB>
+__global__ void __launch_bounds__(kThreads) gdn_scan_step_kernel(const ScanParams<E> p) {
+    constexpr int L = NP / 4;
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    const int d = i / L, n0 = i % L * 4;
+    const int b0 = blockIdx.y * NB;
+    const bool live = d < p.D;         // whole lane groups: L divides the block
+    const int dd = live ? d : 0, g = dd / (p.D / p.G);
+    const bool quads = p.N % 4 == 0;   // rows of states are whole 16-byte pieces
+    float A2[4], h[NB][4];
+    const float bias = p.dt_bias ? p.dt_bias[dd] : 0.f, skip = p.skip ? p.skip[dd] : 0.f;
+    auto quad = [&](const float *row, float (&f)[4]) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) h[i] = p.h0 && i < p.N ? p.h0[row + i] : 0.f;
-    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
-    for (int t = 0; t < n; ++t) {
-        const float x = to_f32(p.x[b * p.x_sb + t * p.x_st + d]);
-        float dt = to_f32(p.dt[b * p.dt_sb + t * p.dt_st + d]) + bias;
-        if (p.softplus) dt = softplus(dt);
-        const E *bm = p.Bm + b * p.b_sb + t * p.b_st + static_cast<int64_t>(g) * p.N;
-        const E *cm = p.Cm + b * p.c_sb + t * p.c_st + static_cast<int64_t>(g) * p.N;
-        float y = 0.f;
+        for (int k = 0; k < 4; ++k) f[k] = 0.f;
+        if (!live) return;
+        if (quads) {
+            if (n0 < p.N) {
+                const float4 q = *reinterpret_cast<const float4 *>(row + n0);
+                f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            if (i < p.N) {
-                const float a = expf(dt * p.A[static_cast<int64_t>(d) * p.N + i]);
-                h[i] = fmaf(a, h[i], dt * x * to_f32(bm[i]));
-                y = fmaf(to_f32(cm[i]), h[i], y);
+            for (int k = 0; k < 4; ++k)
+                if (n0 + k < p.N) f[k] = row[n0 + k];
+        }
+    };
+    auto state = [&](int b) { return (static_cast<int64_t>(b) * p.D + dd) * p.N; };
+#pragma unroll
+    for (int m = 0; m < NB; ++m) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[m][k] = 0.f;
+        if (p.h0 && b0 + m < p.B) quad(p.h0 + state(b0 + m), h[m]);
+    }
+    quad(p.A + static_cast<int64_t>(dd) * p.N, A2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
+
+    for (int t = 0; t < p.T; ++t) {
+#pragma unroll
+        for (int m = 0; m < NB; ++m) {
+            const int64_t b = b0 + m;
+            if (b >= p.B || t >= valid_tokens(p.lengths, b, p.T)) continue;   // the block's alike
+            const float x = to_f32(p.x[b * p.x_sb + t * p.x_st + dd]);
+            float dt = to_f32(p.dt[b * p.dt_sb + t * p.dt_st + dd]) + bias;
+            if (p.softplus) dt = softplus(dt);
+            const E *bm = p.Bm + b * p.b_sb + t * p.b_st + static_cast<int64_t>(g) * p.N + n0;
+            const E *cm = p.Cm + b * p.c_sb + t * p.c_st + static_cast<int64_t>(g) * p.N + n0;
+            float y = 0.f;
+            const float u = dt * x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool in = n0 + k < p.N;
+                h[m][k] = fmaf(exp2_ftz(dt * A2[k]), h[m][k], u * (in ? to_f32(bm[k]) : 0.f));
+                y = fmaf(in ? to_f32(cm[k]) : 0.f, h[m][k], y);
+            }
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            if (live && n0 == 0) {
+                y = fmaf(skip, x, y);
+                if (p.z) y *= activate(to_f32(p.z[b * p.z_sb + t * p.z_st + d]), GDN_ACT_SILU);
+                p.y[(b * p.T + t) * p.D + d] = from_f32<E>(y);
             }
         }
-        y = fmaf(skip, x, y);
-        if (p.z) y *= activate(to_f32(p.z[b * p.z_sb + t * p.z_st + d]), GDN_ACT_SILU);
-        p.y[(static_cast<int64_t>(b) * p.T + t) * p.D + d] = from_f32<E>(y);
     }
-    if (p.h_final) {
+    if (!p.h_final || !live) return;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-            if (i < p.N) p.h_final[row + i] = h[i];
+    for (int m = 0; m < NB; ++m) {
+        if (b0 + m >= p.B) break;
+        float *row = p.h_final + state(b0 + m) + n0;
+        if (quads) {
+            if (n0 < p.N) *reinterpret_cast<float4 *>(row) = make_float4(h[m][0], h[m][1], h[m][2], h[m][3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (n0 + k < p.N) row[k] = h[m][k];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------- prompts
+//
+// A block takes 32 channels of one group of one sequence, four lanes to a channel with
+// NP / 4 states each, and walks the tokens in tiles of TT:
+//   copy    the next tile's rows on their way to shared memory;
+//   widen   Delta and Delta x of every token and channel, B and C as fp32;
+//   scan    per token and state: ex2(Delta A), h = a h + (Delta x) B, y += C h, on pairs
+//           of states; after four tokens the four lanes add their shares of
+//           y so that each ends with one token's sum (3 shuffles for 4 tokens);
+//   finish  D x, the gate, and rows of y in 16-byte pieces.
+// The decay's exponentials dominate; Delta's and the gate's are taken once per token and
+// channel, not in the four lanes.
+constexpr int kChannels = 32;
+
+template <typename E, int NP, int TT>
+struct Tile {
+    static constexpr int row = kChannels * sizeof(E) + 16;   // bytes; 16 more: no bank conflicts
+    static constexpr int du_row = 2 * TT + 4;                // floats of a channel's (Delta, Delta x)
+    static constexpr int y_row = kChannels + 8;
+    static constexpr int bc = TT * NP * sizeof(E);
+    static constexpr int raw = 3 * TT * row + 2 * bc;        // x, dt, z, B, C
+    static constexpr int du = kChannels * du_row * 4;
+    static constexpr int wide = TT * NP * 4;
+    static constexpr int bytes = 2 * raw + du + 2 * wide + TT * y_row * 4;
+};
+
+// PARTIAL: only the state at the end of a segment that starts from zero.
+template <typename E, int NP, int TT, bool VEC, bool PARTIAL>
+__global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> p) {
+    using S = Tile<E, NP, TT>;
+    constexpr int SP = NP / 4, SP2 = SP / 2;
+    constexpr int V = VEC ? 16 / sizeof(E) : 1;      // channels per piece
+    constexpr int PR = kChannels / V;                // pieces per row
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *du = reinterpret_cast<float *>(smem + 2 * S::raw);
+    float *bw = du + S::du / 4, *cw = bw + TT * NP, *yb = cw + TT * NP;
+
+    const int per = p.D / p.G, blocks = (per + kChannels - 1) / kChannels;
+    const int g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * kChannels;
+    const int nc = min(kChannels, per - c0);         // channels of this block
+    const int d0 = g * per + c0;
+    const int64_t b = blockIdx.y;
+    const int s = blockIdx.z;
+    const int n = valid_tokens(p.lengths, b, p.T);
+    const int t_begin = s * p.seg, t_end = min(n, t_begin + p.seg);
+    if (s > 0 && t_begin >= n) return;
+
+    const int tid = threadIdx.x, c = tid / 4, j = tid % 4;
+    const bool live = c < nc;
+    const int d = d0 + (live ? c : 0);
+    const int64_t state = (b * p.D + d) * p.N;
+    auto seg_at = [&](int i) { return ((b * p.segs + i) * p.D + d); };
+
+    F2 A2[SP2], h[SP2];
+    auto load_states = [&](const float *row, F2 (&f)[SP2], float scale) {
+#pragma unroll
+        for (int q = 0; q < SP2; ++q) {
+            const int k = j * SP + 2 * q;
+            f[q] = pack2(live && k < p.N ? scale * row[k] : 0.f,
+                         live && k + 1 < p.N ? scale * row[k + 1] : 0.f);
+        }
+    };
+    auto store_states = [&](float *row) {
+        if (!live) return;
+#pragma unroll
+        for (int q = 0; q < SP2; ++q) {
+            const int k = j * SP + 2 * q;
+            float lo, hi;
+            unpack2(h[q], lo, hi);
+            if (k < p.N) row[k] = lo;
+            if (k + 1 < p.N) row[k + 1] = hi;
+        }
+    };
+    auto decay = [&](float step, F2 A2) {
+        float lo, hi;
+        unpack2(mul2(pack2(step, step), A2), lo, hi);
+        return pack2(exp2_ftz(lo), exp2_ftz(hi));
+    };
+    load_states(p.A + static_cast<int64_t>(d) * p.N, A2, kLog2e);
+#pragma unroll
+    for (int q = 0; q < SP2; ++q) h[q] = 0;
+    if (p.segs == 1) {
+        if (p.h0) load_states(p.h0 + state, h, 1.f);
+    } else if (PARTIAL) {
+        // h0 starts the first segment; a copy serves the second pass, which may write
+        // h_final in h0's place
+        if (s == 0) {
+            if (p.h0) load_states(p.h0 + state, h, 1.f);
+            store_states(p.seg_h + seg_at(p.segs - 1) * p.N);
+        }
+    } else if (s == 0) {
+        load_states(p.seg_h + seg_at(p.segs - 1) * p.N, h, 1.f);
+    } else {
+        for (int i = 0; i < s; ++i) {
+            F2 e[SP2];
+            load_states(p.seg_h + seg_at(i) * p.N, e, 1.f);
+            const float sum = p.seg_dt[seg_at(i)];
+#pragma unroll
+            for (int q = 0; q < SP2; ++q) h[q] = fma2(decay(sum, A2[q]), h[q], e[q]);
+        }
+    }
+
+    // A tile's rows into raw buffer k.
+    auto copy_rows = [&](unsigned char *dst, const E *src, int64_t sb, int64_t st, int t0, int rows) {
+        const E *from = src + b * sb + t0 * st + d0;
+        for (int i = tid; i < TT * PR; i += kThreads) {
+            const int t = i / PR, q = i % PR * V;
+            if (t >= rows || q >= nc) continue;
+            E *to = reinterpret_cast<E *>(dst + t * S::row) + q;
+            if constexpr (VEC)
+                copy16_async(to, from + t * st + q);
+            else
+                *to = from[t * st + q];
+        }
+    };
+    auto copy_bc = [&](unsigned char *dst, const E *src, int64_t sb, int64_t st, int t0, int rows) {
+        const E *from = src + b * sb + t0 * st + static_cast<int64_t>(g) * p.N;
+        E *to = reinterpret_cast<E *>(dst);
+        if (p.rows16) {
+            constexpr int W = 16 / sizeof(E);
+            const int pr = p.N / W;
+            for (int i = tid; i < rows * pr; i += kThreads) {
+                const int t = i / pr, q = i % pr * W;
+                copy16_async(to + t * NP + q, from + t * st + q);
+            }
+        } else {
+            for (int i = tid; i < rows * p.N; i += kThreads) {
+                const int t = i / p.N, q = i % p.N;
+                to[t * NP + q] = from[t * st + q];
+            }
+        }
+    };
+    auto fetch = [&](int k, int t0) {
+        unsigned char *raw = smem + k * S::raw;
+        const int rows = min(TT, t_end - t0);
+        if (rows > 0) {
+            copy_rows(raw, p.x, p.x_sb, p.x_st, t0, rows);
+            copy_rows(raw + TT * S::row, p.dt, p.dt_sb, p.dt_st, t0, rows);
+            copy_bc(raw + 3 * TT * S::row, p.Bm, p.b_sb, p.b_st, t0, rows);
+            if (!PARTIAL) {
+                if (p.z) copy_rows(raw + 2 * TT * S::row, p.z, p.z_sb, p.z_st, t0, rows);
+                copy_bc(raw + 3 * TT * S::row + S::bc, p.Cm, p.c_sb, p.c_st, t0, rows);
+            }
+        }
+        copy_commit();
+    };
+
+    float dt_sum = 0.f;
+    fetch(0, t_begin);
+    for (int t0 = t_begin, k = 0; t0 < t_end; t0 += TT, k ^= 1) {
+        const int rows = min(TT, t_end - t0);
+        copy_wait<0>();
+        __syncthreads();
+        fetch(k ^ 1, t0 + TT);
+        const unsigned char *raw = smem + k * S::raw;
+        // widen: tokens behind the segment get Delta = 0, B = C = 0 and change nothing
+        for (int i = tid; i < TT * PR; i += kThreads) {
+            const int t = i % TT, q = i / TT * V;
+            if (t >= (rows + 3) / 4 * 4 || q >= nc) continue;
+            float x[V], dt[V];
+            Piece<E, V> pc;
+            pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + q);
+            pc.widen(x);
+            pc.load_rw(reinterpret_cast<const E *>(raw + (TT + t) * S::row) + q);
+            pc.widen(dt);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float step = dt[v] + (p.dt_bias ? __ldg(p.dt_bias + d0 + q + v) : 0.f);
+                if (p.softplus) step = softplus(step);
+                *reinterpret_cast<float2 *>(du + (q + v) * S::du_row + 2 * t) =
+                    t < rows ? make_float2(step, step * x[v]) : make_float2(0.f, 0.f);
+            }
+        }
+        for (int i = tid; i < TT * NP; i += kThreads) {
+            const int t = i / NP;
+            const bool in = t < rows && i % NP < p.N;
+            const E *br = reinterpret_cast<const E *>(raw + 3 * TT * S::row);
+            bw[i] = in ? to_f32(br[i]) : 0.f;
+            if (!PARTIAL) cw[i] = in ? to_f32(br[TT * NP + i]) : 0.f;
+        }
+        __syncthreads();
+        // scan
+        const float *my = du + c * S::du_row;
+        for (int t = 0; t < rows; t += 4) {
+            float yt[4];
+            const float4 da = *reinterpret_cast<const float4 *>(my + 2 * t);
+            const float4 db = *reinterpret_cast<const float4 *>(my + 2 * t + 4);
+            const float step[4] = {da.x, da.z, db.x, db.z}, in[4] = {da.y, da.w, db.y, db.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const F2 uu = pack2(in[m], in[m]);
+                const F2 *br = reinterpret_cast<const F2 *>(bw + (t + m) * NP + j * SP);
+                const F2 *cr = reinterpret_cast<const F2 *>(cw + (t + m) * NP + j * SP);
+                F2 acc = 0;
+#pragma unroll
+                for (int q = 0; q < SP2; ++q) {
+                    h[q] = fma2(decay(step[m], A2[q]), h[q], mul2(uu, br[q]));
+                    if (!PARTIAL) acc = fma2(cr[q], h[q], acc);
+                }
+                float lo, hi;
+                unpack2(acc, lo, hi);
+                yt[m] = lo + hi;
+            }
+            if (PARTIAL) {
+                dt_sum += (step[0] + step[1]) + (step[2] + step[3]);
+            } else {
+                const bool up = j & 2, odd = j & 1;
+                const float r0 = __shfl_xor_sync(0xffffffffu, up ? yt[0] : yt[2], 2);
+                const float r1 = __shfl_xor_sync(0xffffffffu, up ? yt[1] : yt[3], 2);
+                const float k0 = (up ? yt[2] : yt[0]) + r0, k1 = (up ? yt[3] : yt[1]) + r1;
+                const float r2 = __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
+                yb[(t + j) * S::y_row + c] = (odd ? k1 : k0) + r2;
+            }
+        }
+        if (PARTIAL) continue;
+        __syncthreads();
+        // finish
+        for (int i = tid; i < TT * PR; i += kThreads) {
+            const int t = i / PR, q = i % PR * V;
+            if (t >= rows || q >= nc) continue;
+            float x[V], z[V], y[V];
+            Piece<E, V> pc;
+            pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + q);
+            pc.widen(x);
+            if (p.z) {
+                pc.load_rw(reinterpret_cast<const E *>(raw + (2 * TT + t) * S::row) + q);
+                pc.widen(z);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                y[v] = fmaf(p.skip ? __ldg(p.skip + d0 + q + v) : 0.f, x[v], yb[t * S::y_row + q + v]);
+                if (p.z) y[v] *= activate(z[v], GDN_ACT_SILU);
+            }
+            pc.round(y);
+            pc.store(p.y + (b * p.T + t0 + t) * p.D + d0 + q);
+        }
+    }
+    if (PARTIAL) {
+        store_states(p.seg_h + seg_at(s) * p.N);
+        if (live && j == 0) p.seg_dt[seg_at(s)] = dt_sum;
+    } else if (p.h_final && t_end == n) {
+        store_states(p.h_final + state);
     }
 }
 
@@ -71,33 +383,94 @@ gdn_status check(const gdn_scan_problem *p) {
     for (int64_t s : {p->x_stride_b, p->x_stride_t, p->dt_stride_b, p->dt_stride_t, p->z_stride_b,
                       p->z_stride_t, p->b_stride_b, p->b_stride_t, p->c_stride_b, p->c_stride_t})
         if (s < 0) return GDN_ERR_INVALID_ARG;
-    if (p->N > 128 || p->B > 65535) return GDN_ERR_UNSUPPORTED;
+    if (p->N > 128 || p->B > 65535 || p->D > (1 << 24)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
-size_t workspace_need(const gdn_scan_problem *) { return 0; }
+// Segments of a prompt: one for every 2 blocks that an SM could hold and the channels
+// do not fill, of 256 tokens at least. The first pass over a segment repeats most of the
+// arithmetic, so channels that fill half of the GPU are not cut.
+int segments(const gdn_scan_problem *p) {
+    const int per = p->D / p->G;
+    const int64_t blocks = static_cast<int64_t>(p->B) * p->G * ((per + kChannels - 1) / kChannels);
+    const int64_t want = 2 * 152 / blocks, most = p->T / 256;
+    const int64_t n = want < most ? want : most;
+    return n < 2 ? 1 : n > 64 ? 64 : static_cast<int>(n);
+}
 
-template <typename E, int NP>
-cudaError_t launch(const gdn_scan_problem *pr, const ScanParams<E> &p, cudaStream_t s) {
-    const dim3 grid((pr->D + kThreads - 1) / kThreads, pr->B);
-    gdn_scan_kernel<E, NP><<<grid, kThreads, 0, s>>>(p);
+size_t workspace_need(const gdn_scan_problem *p) {
+    const int n = segments(p);
+    const size_t rows = static_cast<size_t>(p->B) * n * p->D;
+    return n == 1 ? 0 : align_up(rows * p->N * 4) + align_up(rows * 4);
+}
+
+template <typename E, int NP, int TT, bool VEC>
+cudaError_t launch_prompt(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace, cudaStream_t s) {
+    const int per = pr->D / pr->G;
+    const int n = segments(pr);
+    p.seg = ((pr->T + n - 1) / n + TT - 1) / TT * TT;
+    p.segs = (pr->T + p.seg - 1) / p.seg;
+    const dim3 grid(pr->G * ((per + kChannels - 1) / kChannels), pr->B, p.segs);
+    constexpr int bytes = Tile<E, NP, TT>::bytes;
+    cudaError_t e;
+    if (p.segs > 1) {
+        p.seg_h = static_cast<float *>(workspace);
+        p.seg_dt = reinterpret_cast<float *>(
+            static_cast<char *>(workspace) +
+            align_up(static_cast<size_t>(pr->B) * p.segs * pr->D * pr->N * 4));
+        auto first = gdn_scan_kernel<E, NP, TT, VEC, true>;
+        e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        first<<<dim3(grid.x, grid.y, p.segs - 1), kThreads, bytes, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    auto kernel = gdn_scan_kernel<E, NP, TT, VEC, false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, bytes, s>>>(p);
     return cudaGetLastError();
 }
 
+template <typename E, int NP>
+cudaError_t launch(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace, cudaStream_t s) {
+    if (pr->T <= kStepTokens) {
+        // kBatch sequences to a thread where that still leaves two blocks to an SM
+        const int64_t blocks = (static_cast<int64_t>(pr->D) * (NP / 4) + kThreads - 1) / kThreads;
+        if (blocks * ((pr->B + kBatch - 1) / kBatch) >= 2 * 152)
+            gdn_scan_step_kernel<E, NP, kBatch>
+                <<<dim3(static_cast<unsigned>(blocks), (pr->B + kBatch - 1) / kBatch), kThreads, 0, s>>>(p);
+        else
+            gdn_scan_step_kernel<E, NP, 1><<<dim3(static_cast<unsigned>(blocks), pr->B), kThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    constexpr size_t e = sizeof(E);
+    constexpr int TT = NP <= 32 ? 64 : 32;
+    const bool vec = (pr->D / pr->G) * e % 16 == 0 &&
+                     pieces16(p.x, pr->B, pr->T, pr->D, p.x_sb, p.x_st, e) &&
+                     pieces16(p.dt, pr->B, pr->T, pr->D, p.dt_sb, p.dt_st, e) &&
+                     (!p.z || pieces16(p.z, pr->B, pr->T, pr->D, p.z_sb, p.z_st, e));
+    p.rows16 = pieces16(p.Bm, pr->B, pr->T, pr->N, p.b_sb, p.b_st, e) &&
+               pieces16(p.Cm, pr->B, pr->T, pr->N, p.c_sb, p.c_st, e);
+    return vec ? launch_prompt<E, NP, TT, true>(pr, p, workspace, s)
+               : launch_prompt<E, NP, TT, false>(pr, p, workspace, s);
+}
+
 template <typename E>
-cudaError_t dispatch(const gdn_scan_problem *pr, ScanParams<E> &p, cudaStream_t s) {
+cudaError_t dispatch(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace, cudaStream_t s) {
     p.x_sb = pr->x_stride_b; p.x_st = pr->x_stride_t;
     p.dt_sb = pr->dt_stride_b; p.dt_st = pr->dt_stride_t;
     p.z_sb = pr->z_stride_b; p.z_st = pr->z_stride_t;
     p.b_sb = pr->b_stride_b; p.b_st = pr->b_stride_t;
     p.c_sb = pr->c_stride_b; p.c_st = pr->c_stride_t;
-    p.T = pr->T; p.D = pr->D; p.N = pr->N; p.G = pr->G;
+    p.B = pr->B; p.T = pr->T; p.D = pr->D; p.N = pr->N; p.G = pr->G;
     p.softplus = (pr->flags & GDN_SCAN_SOFTPLUS) ? 1 : 0;
-    if (pr->N <= 8) return launch<E, 8>(pr, p, s);
-    if (pr->N <= 16) return launch<E, 16>(pr, p, s);
-    if (pr->N <= 32) return launch<E, 32>(pr, p, s);
-    if (pr->N <= 64) return launch<E, 64>(pr, p, s);
-    return launch<E, 128>(pr, p, s);
+    p.rows16 = 0; p.segs = 1; p.seg = pr->T; p.seg_h = p.seg_dt = nullptr;
+    if (pr->N <= 8) return launch<E, 8>(pr, p, workspace, s);
+    if (pr->N <= 16) return launch<E, 16>(pr, p, workspace, s);
+    if (pr->N <= 32) return launch<E, 32>(pr, p, workspace, s);
+    if (pr->N <= 64) return launch<E, 64>(pr, p, workspace, s);
+    return launch<E, 128>(pr, p, workspace, s);
 }
 
 }  // namespace
@@ -171,7 +544,7 @@ GDN_API gdn_status gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const 
         a.lengths = lengths;
         a.y = static_cast<E *>(y);
         a.h_final = h_final;
-        return gdn::dispatch<E>(p, a, s);
+        return gdn::dispatch<E>(p, a, workspace, s);
     };
     err = p->dtype == GDN_BF16 ? go(__nv_bfloat16()) : go(float());
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

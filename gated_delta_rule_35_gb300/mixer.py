@@ -206,7 +206,8 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = F
     need = lib().gdn_scan_workspace_bytes(pp)
     if need == _INVALID:
         raise GdnError(_refusal(p), "gdn_scan_fwd")
-    ws = _workspace(workspace, need, x.device).data_ptr() if need else None
+    if need:    # held until the call: freed before, out could be allocated in its place
+        workspace = _workspace(workspace, need, x.device)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
     if not output_final_state:
@@ -215,7 +216,7 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = F
         final_state = torch.empty(state, dtype=f32, device=x.device)
     _call(lib().gdn_scan_fwd, "gdn_scan_fwd", index, pp, x.data_ptr(), dt.data_ptr(), a, B.data_ptr(),
           C.data_ptr(), skip, _ptr(z), bias, hi, n, _dense(out, "out", shape, dtype, index),
-          _dense(final_state, "final_state", state, f32, index), ws, need)
+          _dense(final_state, "final_state", state, f32, index), _ptr(workspace) if need else None, need)
     return out, final_state
 
 
