@@ -30,17 +30,40 @@ struct ScanParams {
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), with log1p(e) = 2 atanh(s),
 // s = e / (2 + e) <= 1/3, by the series s (1 + s^2/3 + s^4/5 + ...) through s^13: the rest
-// is below 2e-8 of it, so small Delta keep their relative accuracy.
+// is below 2e-8 of it, so small Delta keep their relative accuracy. Of two values.
+__device__ __forceinline__ void softplus2(float &a, float &b) {
+    auto two = [](float v) { return pack2(v, v); };
+    const F2 e = pack2(exp2_ftz(-kLog2e * fabsf(a)), exp2_ftz(-kLog2e * fabsf(b)));
+    float p, q;
+    unpack2(add2(e, two(2.f)), p, q);
+    const F2 s = mul2(e, pack2(rcp_ftz(p), rcp_ftz(q))), s2 = mul2(s, s);
+    F2 r = fma2(s2, two(1.f / 13.f), two(1.f / 11.f));
+    r = fma2(s2, r, two(1.f / 9.f));
+    r = fma2(s2, r, two(1.f / 7.f));
+    r = fma2(s2, r, two(1.f / 5.f));
+    r = fma2(s2, r, two(1.f / 3.f));
+    r = fma2(s2, r, two(1.f));
+    unpack2(fma2(add2(s, s), r, pack2(fmaxf(a, 0.f), fmaxf(b, 0.f))), a, b);
+}
+
 __device__ __forceinline__ float softplus(float v) {
-    const float e = exp2_ftz(-kLog2e * fabsf(v));
-    const float s = e * rcp_ftz(2.f + e), q = s * s;
-    float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    r = fmaf(q, r, 1.f / 9.f);
-    r = fmaf(q, r, 1.f / 7.f);
-    r = fmaf(q, r, 1.f / 5.f);
-    r = fmaf(q, r, 1.f / 3.f);
-    r = fmaf(q, r, 1.f);
-    return fmaf(2.f * s, r, fmaxf(v, 0.f));
+    float unused = v;
+    softplus2(v, unused);
+    return v;
+}
+
+// Four consecutive elements of an aligned shared row, those from `left` on as 0.
+__device__ __forceinline__ float4 widen4(const float *p, int left) {
+    const float4 q = *reinterpret_cast<const float4 *>(p);
+    return make_float4(left > 0 ? q.x : 0.f, left > 1 ? q.y : 0.f, left > 2 ? q.z : 0.f,
+                       left > 3 ? q.w : 0.f);
+}
+__device__ __forceinline__ float4 widen4(const __nv_bfloat16 *p, int left) {
+    const uint2 q = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(left > 0 ? __uint_as_float(q.x << 16) : 0.f,
+                       left > 1 ? __uint_as_float(q.x & 0xffff0000u) : 0.f,
+                       left > 2 ? __uint_as_float(q.y << 16) : 0.f,
+                       left > 3 ? __uint_as_float(q.y & 0xffff0000u) : 0.f);
 }
 
 // ----------------------------------------------------------------- a few tokens
@@ -131,44 +154,47 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_step_kernel(const ScanParam
 
 // ---------------------------------------------------------------------- prompts
 //
-// A block takes 32 channels of one group of one sequence, four lanes to a channel with
-// NP / 4 states each, and walks the tokens in tiles of TT:
+// A block takes 128 / L channels of one group of one sequence, L lanes to a channel with
+// NP / L states each, and walks the tokens in tiles of 32:
 //   copy    the next tile's rows on their way to shared memory;
 //   widen   Delta and Delta x of every token and channel, B and C as fp32;
 //   scan    per token and state: ex2(Delta A), h = a h + (Delta x) B, y += C h, on pairs
-//           of states; after four tokens the four lanes add their shares of
-//           y so that each ends with one token's sum (3 shuffles for 4 tokens);
+//           of states; after four tokens the lanes of a channel add their shares of
+//           y so that the sums end spread over them;
 //   finish  D x, the gate, and rows of y in 16-byte pieces.
 // The decay's exponentials dominate; Delta's and the gate's are taken once per token and
-// channel, not in the four lanes.
-constexpr int kChannels = 32;
+// channel, not in every lane. Few lanes to a channel keep the exchange of y small, eight
+// or more states to a lane keep the arithmetic pipes fed from few warps.
+constexpr int kTile = 32;
 
-template <typename E, int NP, int TT>
+template <typename E, int NP>
 struct Tile {
-    static constexpr int row = kChannels * sizeof(E) + 16;   // bytes; 16 more: no bank conflicts
-    static constexpr int du_row = 2 * TT + 4;                // floats of a channel's (Delta, Delta x)
-    static constexpr int y_row = kChannels + 8;
-    static constexpr int bc = TT * NP * sizeof(E);
-    static constexpr int raw = 3 * TT * row + 2 * bc;        // x, dt, z, B, C
-    static constexpr int du = kChannels * du_row * 4;
-    static constexpr int wide = TT * NP * 4;
-    static constexpr int bytes = 2 * raw + du + 2 * wide + TT * y_row * 4;
+    static constexpr int L = NP <= 32 ? 2 : NP / 16;         // lanes to a channel
+    static constexpr int channels = kThreads / L;
+    static constexpr int row = channels * sizeof(E) + 16;    // bytes; 16 more: no bank conflicts
+    static constexpr int du_row = 2 * kTile + 4;             // floats of a channel's (Delta, Delta x)
+    static constexpr int y_row = channels + 32 / L;
+    static constexpr int bc = kTile * NP * sizeof(E);
+    static constexpr int raw = 3 * kTile * row + 2 * bc;     // x, dt, z, B, C
+    static constexpr int du = channels * du_row * 4;
+    static constexpr int wide = kTile * NP * 4;
+    static constexpr int bytes = 2 * raw + du + 2 * wide + kTile * y_row * 4;
 };
 
 // PARTIAL: only the state at the end of a segment that starts from zero.
-template <typename E, int NP, int TT, bool VEC, bool PARTIAL>
-__global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> p) {
-    using S = Tile<E, NP, TT>;
-    constexpr int SP = NP / 4, SP2 = SP / 2;
+template <typename E, int NP, bool VEC, bool PARTIAL>
+__global__ void __launch_bounds__(kThreads, 3) gdn_scan_kernel(const ScanParams<E> p) {
+    using S = Tile<E, NP>;
+    constexpr int L = S::L, SP = NP / L, SP2 = SP / 2, TT = kTile;
     constexpr int V = VEC ? 16 / sizeof(E) : 1;      // channels per piece
-    constexpr int PR = kChannels / V;                // pieces per row
+    constexpr int PR = S::channels / V;              // pieces per row
     extern __shared__ __align__(16) unsigned char smem[];
     float *du = reinterpret_cast<float *>(smem + 2 * S::raw);
     float *bw = du + S::du / 4, *cw = bw + TT * NP, *yb = cw + TT * NP;
 
-    const int per = p.D / p.G, blocks = (per + kChannels - 1) / kChannels;
-    const int g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * kChannels;
-    const int nc = min(kChannels, per - c0);         // channels of this block
+    const int per = p.D / p.G, blocks = (per + S::channels - 1) / S::channels;
+    const int g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * S::channels;
+    const int nc = min(S::channels, per - c0);       // channels of this block
     const int d0 = g * per + c0;
     const int64_t b = blockIdx.y;
     const int s = blockIdx.z;
@@ -176,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> 
     const int t_begin = s * p.seg, t_end = min(n, t_begin + p.seg);
     if (s > 0 && t_begin >= n) return;
 
-    const int tid = threadIdx.x, c = tid / 4, j = tid % 4;
+    const int tid = threadIdx.x, c = tid / L, j = tid % L;
     const bool live = c < nc;
     const int d = d0 + (live ? c : 0);
     const int64_t state = (b * p.D + d) * p.N;
@@ -202,9 +228,9 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> 
             if (k + 1 < p.N) row[k + 1] = hi;
         }
     };
-    auto decay = [&](float step, F2 A2) {
+    auto decay = [&](F2 step, F2 A2) {
         float lo, hi;
-        unpack2(mul2(pack2(step, step), A2), lo, hi);
+        unpack2(mul2(step, A2), lo, hi);
         return pack2(exp2_ftz(lo), exp2_ftz(hi));
     };
     load_states(p.A + static_cast<int64_t>(d) * p.N, A2, kLog2e);
@@ -227,37 +253,42 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> 
             load_states(p.seg_h + seg_at(i) * p.N, e, 1.f);
             const float sum = p.seg_dt[seg_at(i)];
 #pragma unroll
-            for (int q = 0; q < SP2; ++q) h[q] = fma2(decay(sum, A2[q]), h[q], e[q]);
+            for (int q = 0; q < SP2; ++q) h[q] = fma2(decay(pack2(sum, sum), A2[q]), h[q], e[q]);
         }
     }
 
-    // A tile's rows into raw buffer k.
+    // A tile's rows into a raw buffer: this thread's piece of every kThreads / PR-th row.
+    const int piece = tid % PR * V;
     auto copy_rows = [&](unsigned char *dst, const E *src, int64_t sb, int64_t st, int t0, int rows) {
-        const E *from = src + b * sb + t0 * st + d0;
-        for (int i = tid; i < TT * PR; i += kThreads) {
-            const int t = i / PR, q = i % PR * V;
-            if (t >= rows || q >= nc) continue;
-            E *to = reinterpret_cast<E *>(dst + t * S::row) + q;
-            if constexpr (VEC)
-                copy16_async(to, from + t * st + q);
-            else
-                *to = from[t * st + q];
+        if (piece >= nc) return;
+        const E *from = src + b * sb + (t0 + tid / PR) * st + d0 + piece;
+        E *to = reinterpret_cast<E *>(dst + tid / PR * S::row) + piece;
+        constexpr int step = kThreads / PR;
+#pragma unroll
+        for (int t = 0; t < TT; t += step) {
+            if (t + tid / PR < rows) {
+                if constexpr (VEC)
+                    copy16_async(to, from);
+                else
+                    *to = *from;
+            }
+            from += step * st;
+            to += step * S::row / sizeof(E);
         }
     };
     auto copy_bc = [&](unsigned char *dst, const E *src, int64_t sb, int64_t st, int t0, int rows) {
         const E *from = src + b * sb + t0 * st + static_cast<int64_t>(g) * p.N;
         E *to = reinterpret_cast<E *>(dst);
         if (p.rows16) {
-            constexpr int W = 16 / sizeof(E);
-            const int pr = p.N / W;
-            for (int i = tid; i < rows * pr; i += kThreads) {
-                const int t = i / pr, q = i % pr * W;
-                copy16_async(to + t * NP + q, from + t * st + q);
+            constexpr int W = 16 / sizeof(E), most = NP / W;
+            for (int i = tid; i < rows * most; i += kThreads) {
+                const int t = i / most, q = i % most * W;
+                if (q < p.N) copy16_async(to + t * NP + q, from + t * st + q);
             }
         } else {
-            for (int i = tid; i < rows * p.N; i += kThreads) {
-                const int t = i / p.N, q = i % p.N;
-                to[t * NP + q] = from[t * st + q];
+            for (int i = tid; i < rows * NP; i += kThreads) {
+                const int t = i / NP, q = i % NP;
+                if (q < p.N) to[i] = from[t * st + q];
             }
         }
     };
@@ -276,6 +307,11 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> 
         copy_commit();
     };
 
+    float skip[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) skip[v] = 0.f;
+    if (!PARTIAL && p.skip && piece < nc) load_f32<V>(p.skip + d0 + piece, skip);
+
     float dt_sum = 0.f;
     fetch(0, t_begin);
     for (int t0 = t_begin, k = 0; t0 < t_end; t0 += TT, k ^= 1) {
@@ -285,29 +321,39 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> 
         fetch(k ^ 1, t0 + TT);
         const unsigned char *raw = smem + k * S::raw;
         // widen: tokens behind the segment get Delta = 0, B = C = 0 and change nothing
-        for (int i = tid; i < TT * PR; i += kThreads) {
-            const int t = i % TT, q = i / TT * V;
-            if (t >= (rows + 3) / 4 * 4 || q >= nc) continue;
-            float x[V], dt[V];
-            Piece<E, V> pc;
-            pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + q);
-            pc.widen(x);
-            pc.load_rw(reinterpret_cast<const E *>(raw + (TT + t) * S::row) + q);
-            pc.widen(dt);
+        {
+            const int t = tid % TT;
+            const bool in = t < rows;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float step = dt[v] + (p.dt_bias ? __ldg(p.dt_bias + d0 + q + v) : 0.f);
-                if (p.softplus) step = softplus(step);
-                *reinterpret_cast<float2 *>(du + (q + v) * S::du_row + 2 * t) =
-                    t < rows ? make_float2(step, step * x[v]) : make_float2(0.f, 0.f);
+            for (int q = tid / TT * V; q < S::channels; q += kThreads / TT * V) {
+                if (q >= nc) break;
+                float x[V], dt[V + 1], bias[V];
+                Piece<E, V> pc;
+                pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + q);
+                pc.widen(x);
+                pc.load_rw(reinterpret_cast<const E *>(raw + (TT + t) * S::row) + q);
+                pc.widen(reinterpret_cast<float (&)[V]>(dt));
+                if (p.dt_bias) {
+                    load_f32<V>(p.dt_bias + d0 + q, bias);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) dt[v] += bias[v];
+                }
+                if (p.softplus) {
+                    if constexpr (V == 1) dt[1] = dt[0];
+#pragma unroll
+                    for (int v = 0; v < V; v += 2) softplus2(dt[v], dt[v + 1]);
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    *reinterpret_cast<float2 *>(du + (q + v) * S::du_row + 2 * t) =
+                        make_float2(in ? dt[v] : 0.f, in ? dt[v] * x[v] : 0.f);
             }
         }
-        for (int i = tid; i < TT * NP; i += kThreads) {
-            const int t = i / NP;
-            const bool in = t < rows && i % NP < p.N;
+        for (int i = tid * 4; i < TT * NP; i += kThreads * 4) {
             const E *br = reinterpret_cast<const E *>(raw + 3 * TT * S::row);
-            bw[i] = in ? to_f32(br[i]) : 0.f;
-            if (!PARTIAL) cw[i] = in ? to_f32(br[TT * NP + i]) : 0.f;
+            const int left = i / NP < rows ? p.N - i % NP : 0;
+            *reinterpret_cast<float4 *>(bw + i) = widen4(br + i, left);
+            if (!PARTIAL) *reinterpret_cast<float4 *>(cw + i) = widen4(br + TT * NP + i, left);
         }
         __syncthreads();
         // scan
@@ -319,14 +365,20 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> 
             const float step[4] = {da.x, da.z, db.x, db.z}, in[4] = {da.y, da.w, db.y, db.w};
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const F2 uu = pack2(in[m], in[m]);
-                const F2 *br = reinterpret_cast<const F2 *>(bw + (t + m) * NP + j * SP);
-                const F2 *cr = reinterpret_cast<const F2 *>(cw + (t + m) * NP + j * SP);
+                const F2 dd = pack2(step[m], step[m]), uu = pack2(in[m], in[m]);
+                const ulonglong2 *br = reinterpret_cast<const ulonglong2 *>(bw + (t + m) * NP + j * SP);
+                const ulonglong2 *cr = reinterpret_cast<const ulonglong2 *>(cw + (t + m) * NP + j * SP);
                 F2 acc = 0;
 #pragma unroll
-                for (int q = 0; q < SP2; ++q) {
-                    h[q] = fma2(decay(step[m], A2[q]), h[q], mul2(uu, br[q]));
-                    if (!PARTIAL) acc = fma2(cr[q], h[q], acc);
+                for (int q = 0; q < SP2; q += 2) {
+                    const ulonglong2 bq = br[q / 2];
+                    h[q] = fma2(decay(dd, A2[q]), h[q], mul2(uu, bq.x));
+                    h[q + 1] = fma2(decay(dd, A2[q + 1]), h[q + 1], mul2(uu, bq.y));
+                    if (!PARTIAL) {
+                        const ulonglong2 cq = cr[q / 2];
+                        acc = q == 0 ? mul2(cq.x, h[q]) : fma2(cq.x, h[q], acc);
+                        acc = fma2(cq.y, h[q + 1], acc);
+                    }
                 }
                 float lo, hi;
                 unpack2(acc, lo, hi);
@@ -334,36 +386,61 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_kernel(const ScanParams<E> 
             }
             if (PARTIAL) {
                 dt_sum += (step[0] + step[1]) + (step[2] + step[3]);
-            } else {
-                const bool up = j & 2, odd = j & 1;
+                continue;
+            }
+            const bool odd = j & 1;
+            float *y = yb + t * S::y_row + c;
+            if constexpr (L == 2) {     // lane j: tokens j and 2 + j
+                const float r0 = __shfl_xor_sync(0xffffffffu, odd ? yt[0] : yt[1], 1);
+                const float r1 = __shfl_xor_sync(0xffffffffu, odd ? yt[2] : yt[3], 1);
+                y[j * S::y_row] = (odd ? yt[1] : yt[0]) + r0;
+                y[(2 + j) * S::y_row] = (odd ? yt[3] : yt[2]) + r1;
+            } else {                    // lane j: token j of the first four lanes
+                const bool up = j & 2;
                 const float r0 = __shfl_xor_sync(0xffffffffu, up ? yt[0] : yt[2], 2);
                 const float r1 = __shfl_xor_sync(0xffffffffu, up ? yt[1] : yt[3], 2);
                 const float k0 = (up ? yt[2] : yt[0]) + r0, k1 = (up ? yt[3] : yt[1]) + r1;
-                const float r2 = __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
-                yb[(t + j) * S::y_row + c] = (odd ? k1 : k0) + r2;
+                float sum = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
+                if constexpr (L == 8) sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                if (j < 4) y[j * S::y_row] = sum;
             }
         }
         if (PARTIAL) continue;
         __syncthreads();
         // finish
-        for (int i = tid; i < TT * PR; i += kThreads) {
-            const int t = i / PR, q = i % PR * V;
-            if (t >= rows || q >= nc) continue;
-            float x[V], z[V], y[V];
-            Piece<E, V> pc;
-            pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + q);
-            pc.widen(x);
-            if (p.z) {
-                pc.load_rw(reinterpret_cast<const E *>(raw + (2 * TT + t) * S::row) + q);
-                pc.widen(z);
-            }
+        if (piece < nc) {
+            E *to = p.y + (b * p.T + t0) * p.D + d0 + piece;
+            for (int t = tid / PR; t < rows; t += kThreads / PR) {
+                float x[V], z[V];
+                alignas(16) float y[V + 1];
+                Piece<E, V> pc;
+                pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + piece);
+                pc.widen(x);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                y[v] = fmaf(p.skip ? __ldg(p.skip + d0 + q + v) : 0.f, x[v], yb[t * S::y_row + q + v]);
-                if (p.z) y[v] *= activate(z[v], GDN_ACT_SILU);
+                for (int v = 0; v < V; v += 4) {
+                    const float *from = yb + t * S::y_row + piece + v;
+                    if constexpr (V == 1)
+                        y[0] = *from;
+                    else
+                        *reinterpret_cast<float4 *>(y + v) = *reinterpret_cast<const float4 *>(from);
+                }
+                if (p.skip) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) y[v] = fmaf(skip[v], x[v], y[v]);
+                }
+                if (p.z) {
+                    pc.load_rw(reinterpret_cast<const E *>(raw + (2 * TT + t) * S::row) + piece);
+                    pc.widen(z);
+#pragma unroll
+                    for (int v = 0; v < V; v += 2) {
+                        const int w = V == 1 ? 0 : v + 1;
+                        const F2 gate = activate2(pack2(z[v], z[w]), GDN_ACT_SILU);
+                        unpack2(mul2(pack2(y[v], y[w]), gate), y[v], y[v + 1]);
+                    }
+                }
+                pc.round(reinterpret_cast<const float (&)[V]>(y));
+                pc.store(to + static_cast<int64_t>(t) * p.D);
             }
-            pc.round(y);
-            pc.store(p.y + (b * p.T + t0 + t) * p.D + d0 + q);
         }
     }
     if (PARTIAL) {
@@ -390,9 +467,15 @@ gdn_status check(const gdn_scan_problem *p) {
 // Segments of a prompt: one for every 2 blocks that an SM could hold and the channels
 // do not fill, of 256 tokens at least. The first pass over a segment repeats most of the
 // arithmetic, so channels that fill half of the GPU are not cut.
+int block_channels(int N) { return N <= 32 ? kThreads / 2 : N <= 64 ? kThreads / 4 : kThreads / 8; }
+
+int64_t row_blocks(const gdn_scan_problem *p) {
+    const int per = p->D / p->G, c = block_channels(p->N);
+    return static_cast<int64_t>(p->G) * ((per + c - 1) / c);
+}
+
 int segments(const gdn_scan_problem *p) {
-    const int per = p->D / p->G;
-    const int64_t blocks = static_cast<int64_t>(p->B) * p->G * ((per + kChannels - 1) / kChannels);
+    const int64_t blocks = p->B * row_blocks(p);
     const int64_t want = 2 * 152 / blocks, most = p->T / 256;
     const int64_t n = want < most ? want : most;
     return n < 2 ? 1 : n > 64 ? 64 : static_cast<int>(n);
@@ -404,28 +487,28 @@ size_t workspace_need(const gdn_scan_problem *p) {
     return n == 1 ? 0 : align_up(rows * p->N * 4) + align_up(rows * 4);
 }
 
-template <typename E, int NP, int TT, bool VEC>
+template <typename E, int NP, bool VEC>
 cudaError_t launch_prompt(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace, cudaStream_t s) {
-    const int per = pr->D / pr->G;
+    static_assert(Tile<E, NP>::channels == kThreads / (NP <= 32 ? 2 : NP / 16), "block_channels");
     const int n = segments(pr);
-    p.seg = ((pr->T + n - 1) / n + TT - 1) / TT * TT;
+    p.seg = ((pr->T + n - 1) / n + kTile - 1) / kTile * kTile;
     p.segs = (pr->T + p.seg - 1) / p.seg;
-    const dim3 grid(pr->G * ((per + kChannels - 1) / kChannels), pr->B, p.segs);
-    constexpr int bytes = Tile<E, NP, TT>::bytes;
+    const dim3 grid(static_cast<unsigned>(row_blocks(pr)), pr->B, p.segs);
+    constexpr int bytes = Tile<E, NP>::bytes;
     cudaError_t e;
     if (p.segs > 1) {
         p.seg_h = static_cast<float *>(workspace);
         p.seg_dt = reinterpret_cast<float *>(
             static_cast<char *>(workspace) +
             align_up(static_cast<size_t>(pr->B) * p.segs * pr->D * pr->N * 4));
-        auto first = gdn_scan_kernel<E, NP, TT, VEC, true>;
+        auto first = gdn_scan_kernel<E, NP, VEC, true>;
         e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         first<<<dim3(grid.x, grid.y, p.segs - 1), kThreads, bytes, s>>>(p);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    auto kernel = gdn_scan_kernel<E, NP, TT, VEC, false>;
+    auto kernel = gdn_scan_kernel<E, NP, VEC, false>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     kernel<<<grid, kThreads, bytes, s>>>(p);
@@ -445,15 +528,14 @@ cudaError_t launch(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace
         return cudaGetLastError();
     }
     constexpr size_t e = sizeof(E);
-    constexpr int TT = NP <= 32 ? 64 : 32;
     const bool vec = (pr->D / pr->G) * e % 16 == 0 &&
                      pieces16(p.x, pr->B, pr->T, pr->D, p.x_sb, p.x_st, e) &&
                      pieces16(p.dt, pr->B, pr->T, pr->D, p.dt_sb, p.dt_st, e) &&
                      (!p.z || pieces16(p.z, pr->B, pr->T, pr->D, p.z_sb, p.z_st, e));
     p.rows16 = pieces16(p.Bm, pr->B, pr->T, pr->N, p.b_sb, p.b_st, e) &&
                pieces16(p.Cm, pr->B, pr->T, pr->N, p.c_sb, p.c_st, e);
-    return vec ? launch_prompt<E, NP, TT, true>(pr, p, workspace, s)
-               : launch_prompt<E, NP, TT, false>(pr, p, workspace, s);
+    return vec ? launch_prompt<E, NP, true>(pr, p, workspace, s)
+               : launch_prompt<E, NP, false>(pr, p, workspace, s);
 }
 
 template <typename E>
