@@ -1,12 +1,19 @@
 // Group norm of channels-last rows with an activation or a gate: gdn_group_norm of
 // include/gdn.h.
 //
-// One CTA per (sequence, group): a pass for the mean, a pass for the variance about
-// it, a pass that normalises.
+// Bound by memory: one read of x (and of the gate) and one write of y. Two kernels, both
+// with the mean first and the variance about it:
+//   gdn_norm_rows_kernel   T = 1: a group is cg consecutive values, held in the registers of a
+//                          part of a warp between the statistics and the output;
+//   gdn_norm_tokens_kernel any T: a cluster of CTAs shares a sequence's tokens for a slice of
+//                          whole groups; its second reading comes from L2.
 #include "mixer.cuh"
+#include "sm100_ptx.cuh"
 
 namespace gdn {
 namespace {
+
+using namespace ptx;
 
 constexpr int kThreads = 256;
 
@@ -17,47 +24,381 @@ struct NormParams {
     const int32_t *lengths;
     E *y;
     int64_t x_sb, x_st, g_sb, g_st;
-    int T, C, G, act;
+    int B, T, C, G, act;
     float eps;
+    // rows kernel: lanes to a group, rows in flight; tokens kernel: groups to a slice,
+    // CTAs to a cluster
+    int lanes, flight, groups, cluster;
 };
 
-__device__ float block_sum(float v) {
-    __shared__ float part[kThreads / 32];
+// v (normalised) scaled and shifted, through the activation or the gate.
+template <int V>
+__device__ __forceinline__ void outputs(float (&v)[V], const float (&w)[V], const float (&bias)[V],
+                                        const float (&gate)[V], bool gated, int act) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-    return s;
+    for (int i = 0; i < V; i += 2) {
+        const int k = V == 1 ? 0 : i + 1;
+        F2 o = fma2(pack2(v[i], v[k]), pack2(w[i], w[k]), pack2(bias[i], bias[k]));
+        o = gated ? mul2(o, activate2(pack2(gate[i], gate[k]), act)) : activate2(o, act);
+        float lo, hi;
+        unpack2(o, lo, hi);
+        v[i] = lo;
+        if (V > 1) v[k] = hi;
+    }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kThreads) gdn_group_norm_kernel(const NormParams<E> p) {
-    const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
-    const int cg = p.C / p.G, n = valid_tokens(p.lengths, b, p.T);
-    if (n == 0) return;
-    const int64_t count = static_cast<int64_t>(n) * cg;
-    const E *x = p.x + b * p.x_sb + g * cg;
-    float s = 0.f;
-    for (int64_t i = threadIdx.x; i < count; i += kThreads) s += to_f32(x[i / cg * p.x_st + i % cg]);
-    const float mean = block_sum(s) / count;
-    s = 0.f;
-    for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-        const float d = to_f32(x[i / cg * p.x_st + i % cg]) - mean;
-        s = fmaf(d, d, s);
+template <int V>
+__device__ __forceinline__ void params(const float *p, int c, float other, float (&f)[V]) {
+    if (p) {
+        load_f32<V>(p + c, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = other;
     }
-    const float rstd = rsqrtf(block_sum(s) / count + p.eps);
-    for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-        const int64_t t = i / cg;
-        const int c = g * cg + static_cast<int>(i % cg);
-        float v = (to_f32(x[t * p.x_st + i % cg]) - mean) * rstd;
-        v = fmaf(v, p.w ? p.w[c] : 1.f, p.bias ? p.bias[c] : 0.f);
-        v = p.gate ? v * activate(to_f32(p.gate[b * p.g_sb + t * p.g_st + c]), p.act)
-                   : activate(v, p.act);
-        p.y[(static_cast<int64_t>(b) * p.T + t) * p.C + c] = from_f32<E>(v);
+}
+
+// ------------------------------------------------------------------ single rows
+//
+// `lanes` lanes (a power of two) hold a group, P pieces of V channels to a lane, R rows at a
+// time. A thread keeps its channels from row to row, so weight and bias stay in registers.
+template <typename E, int V, int P, int R>
+__global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p) {
+    const int L = p.lanes, cg = p.C / p.G, slots = p.G * L;
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    const int j = i % L;                               // slots and 32 are multiples of L
+    const int g = i % slots / L;
+    int row = i < slots * p.flight ? i / slots : p.B;
+    const float inv = 1.f / cg;
+    float w[P][V], bias[P][V];
+    bool in[P];
+    int c[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        const int at = (q * L + j) * V;
+        in[q] = at < cg;
+        c[q] = g * cg + (in[q] ? at : 0);
+        params<V>(p.w, c[q], 1.f, w[q]);
+        params<V>(p.bias, c[q], 0.f, bias[q]);
+    }
+    // every thread takes the same number of turns: the shuffles need whole warps
+    for (int done = 0; done < p.B; done += R * p.flight, row += R * p.flight) {
+        Piece<E, V> x[R][P], gate[R][P];
+        bool live[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t b = row + r * p.flight;
+            live[r] = b < p.B && (!p.lengths || p.lengths[b] > 0);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                x[r][q].zero();
+                gate[r][q].zero();
+                if (live[r] && in[q]) {
+                    x[r][q].load_rw(p.x + b * p.x_sb + c[q]);
+                    if (p.gate) gate[r][q].load(p.gate + b * p.g_sb + c[q]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float v[P][V], s = 0.f;
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                x[r][q].widen(v[q]);
+#pragma unroll
+                for (int k = 0; k < V; ++k) s += v[q][k];
+            }
+            for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            const float mean = s * inv;
+            s = 0.f;
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    v[q][k] -= mean;
+                    if (in[q]) s = fmaf(v[q][k], v[q][k], s);
+                }
+            for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            const float rstd = rsqrtf(fmaf(s, inv, p.eps));
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                if (!live[r] || !in[q]) continue;
+                float gv[V];
+                gate[r][q].widen(gv);
+#pragma unroll
+                for (int k = 0; k < V; ++k) v[q][k] *= rstd;
+                outputs<V>(v[q], w[q], bias[q], gv, p.gate != nullptr, p.act);
+                x[r][q].round(v[q]);
+                x[r][q].store(p.y + (row + static_cast<int64_t>(r) * p.flight) * p.C + c[q]);
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- whole sequences
+//
+// The CTAs of a cluster take equal shares of a sequence's valid tokens, for one slice of
+// `groups` groups. A thread keeps one piece of V channels and takes every RP-th
+// token, eight at a time: their mean and the squares about it, merged into the running
+// (count, mean, squares) of each channel by the exact update for two sets,
+//   mean += d nb / n,   M2 += M2b + d^2 na nb / n   with d = mean_b - mean,
+// which loses nothing where the mean is far from zero. Channels and threads then merge to
+// groups, and the CTAs' groups through distributed shared memory, in rank order.
+constexpr int kBlockTokens = 8;
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// (count, mean, squares) of each CTA's groups, all CTAs': mean and 1 / deviation.
+__device__ __forceinline__ void merge_cluster(float (&part)[3][kThreads], int groups, int K, float eps,
+                                              float *mean, float *rstd) {
+    __syncthreads();
+    if (K > 1) cluster_sync();
+    for (int g = threadIdx.x; g < groups; g += kThreads) {
+        float na = 0.f, m = 0.f, s = 0.f;
+        for (int r = 0; r < K; ++r) {
+            auto of_rank = [&](float *f) {
+                return K > 1 ? ld_cluster_f32(mapa_shared(smem_u32(f), r)) : *f;
+            };
+            const float nb = of_rank(&part[0][g]);
+            if (nb == 0.f) continue;
+            const float d = of_rank(&part[1][g]) - m, f = nb / (na + nb);
+            s += fmaf(d * d, na * f, of_rank(&part[2][g]));
+            m = fmaf(d, f, m);
+            na += nb;
+        }
+        mean[g] = m;
+        rstd[g] = rsqrtf(s / na + eps);
+    }
+    __syncthreads();
+    if (K > 1) cluster_sync();           // no CTA leaves while another may read its part
+}
+
+template <typename E, int V>
+__global__ void __launch_bounds__(kThreads) gdn_norm_tokens_kernel(NormParams<E> p) {
+    __shared__ float means[kThreads * V], squares[kThreads * V];   // [token row][channel of the slice]
+    __shared__ float part[3][kThreads];                            // count, mean, squares of a group
+    __shared__ float g_mean[kThreads], g_rstd[kThreads];
+    const int cg = p.C / p.G, K = p.cluster, rank = blockIdx.x % K;
+    const int g0 = blockIdx.y * p.groups, ng = min(p.groups, p.G - g0);
+    const int64_t b = blockIdx.x / K;
+    const int n = valid_tokens(p.lengths, b, p.T);
+    if (n == 0) return;                                            // the whole cluster
+    const int SC = ng * cg, PR = SC / V, RP = kThreads / PR;
+    const int row = threadIdx.x / PR, q = threadIdx.x % PR * V, c = g0 * cg + q;
+    const int share = (n + K - 1) / K, t_begin = min(n, rank * share), t_end = min(n, t_begin + share);
+    const bool mine = row < RP;
+    const E *x = p.x + b * p.x_sb + c;
+
+    float mean[V], m2[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) mean[k] = m2[k] = 0.f;
+    float count = 0.f;
+    if (mine) {
+        int t = t_begin + row;
+        for (; t + (kBlockTokens - 1) * RP < t_end; t += kBlockTokens * RP) {
+            Piece<E, V> r[kBlockTokens];
+#pragma unroll
+            for (int u = 0; u < kBlockTokens; ++u) r[u].load_rw(x + (t + static_cast<int64_t>(u) * RP) * p.x_st);
+            const float na = count;
+            count += kBlockTokens;
+            const float f = kBlockTokens / count;
+            float f0[V], s[V], s2[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) s[k] = s2[k] = 0.f;
+#pragma unroll
+            for (int u = 0; u < kBlockTokens; ++u) {
+                r[u].widen(f0);
+#pragma unroll
+                for (int k = 0; k < V; ++k) s[k] += f0[k];
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k) s[k] *= 1.f / kBlockTokens;
+#pragma unroll
+            for (int u = 0; u < kBlockTokens; ++u) {
+                r[u].widen(f0);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float d = f0[k] - s[k];
+                    s2[k] = fmaf(d, d, s2[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float d = s[k] - mean[k];
+                mean[k] = fmaf(d, f, mean[k]);
+                m2[k] += fmaf(d * d, na * f, s2[k]);
+            }
+        }
+        for (; t < t_end; t += RP) {
+            Piece<E, V> r;
+            float f0[V];
+            r.load_rw(x + t * p.x_st);
+            r.widen(f0);
+            count += 1.f;
+            const float f = 1.f / count;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float d = f0[k] - mean[k];
+                mean[k] = fmaf(d, f, mean[k]);
+                m2[k] = fmaf(d, f0[k] - mean[k], m2[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            means[row * SC + q + k] = mean[k];
+            squares[row * SC + q + k] = m2[k];
+        }
+    }
+    __syncthreads();
+    // a warp merges a group: its cg channels of RP token rows, each with the row's count
+    for (int g = threadIdx.x / 32; g < ng; g += kThreads / 32) {
+        auto rows_of = [&](int r) {      // tokens of row r
+            const int left = t_end - t_begin - r;
+            return left > 0 ? static_cast<float>((left + RP - 1) / RP) : 0.f;
+        };
+        const int entries = RP * cg;
+        float s = 0.f;
+        for (int i = threadIdx.x % 32; i < entries; i += 32)
+            s = fmaf(rows_of(i / cg), means[i / cg * SC + g * cg + i % cg], s);
+        const float total = static_cast<float>(t_end - t_begin) * cg;
+        const float m = total > 0.f ? warp_sum(s) / total : 0.f;
+        s = 0.f;
+        for (int i = threadIdx.x % 32; i < entries; i += 32) {
+            const int at = i / cg * SC + g * cg + i % cg;
+            const float d = means[at] - m;
+            s += fmaf(rows_of(i / cg) * d, d, squares[at]);
+        }
+        s = warp_sum(s);
+        if (threadIdx.x % 32 == 0) {
+            part[0][g] = total;
+            part[1][g] = m;
+            part[2][g] = s;
+        }
+    }
+    merge_cluster(part, ng, K, p.eps, g_mean, g_rstd);
+    if (!mine) return;
+    float w[V], bias[V];
+    params<V>(p.w, c, 1.f, w);
+    params<V>(p.bias, c, 0.f, bias);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        mean[k] = g_mean[(q + k) / cg];
+        w[k] *= g_rstd[(q + k) / cg];
+    }
+    const E *gate = p.gate ? p.gate + b * p.g_sb + c : nullptr;
+    E *y = p.y + b * p.T * p.C + c;
+    auto finish = [&](Piece<E, V> &r, const Piece<E, V> &z, int64_t t) {
+        float v[V], gv[V];
+        r.widen(v);
+        z.widen(gv);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] -= mean[k];
+        outputs<V>(v, w, bias, gv, gate != nullptr, p.act);
+        r.round(v);
+        r.store(y + t * p.C);
+    };
+    constexpr int U = 4;
+    for (int t = t_begin + row; t < t_end; t += U * RP) {
+        Piece<E, V> r[U], z[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            z[u].zero();
+            if (t + u * RP < t_end) {
+                r[u].load_rw(x + (t + static_cast<int64_t>(u) * RP) * p.x_st);
+                if (gate) z[u].load(gate + (t + static_cast<int64_t>(u) * RP) * p.g_st);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u * RP < t_end) finish(r[u], z[u], t + static_cast<int64_t>(u) * RP);
+    }
+}
+
+// The same for a group of more pieces than a block has threads: a cluster to a group, each
+// thread taking every kThreads-th piece of a token and merging all its values.
+template <typename E, int V>
+__global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p) {
+    __shared__ float part[3][kThreads];
+    __shared__ float g_mean[1], g_rstd[1];
+    const int cg = p.C / p.G, K = p.cluster, rank = blockIdx.x % K, c0 = blockIdx.y * cg;
+    const int64_t b = blockIdx.x / K;
+    const int n = valid_tokens(p.lengths, b, p.T);
+    if (n == 0) return;                                            // the whole cluster
+    const int share = (n + K - 1) / K, t_begin = min(n, rank * share), t_end = min(n, t_begin + share);
+    const E *x = p.x + b * p.x_sb + c0;
+    float count = 0.f, mean = 0.f, m2 = 0.f;
+    for (int64_t t = t_begin; t < t_end; ++t) {
+        for (int q = threadIdx.x * V; q < cg; q += kThreads * V) {
+            Piece<E, V> r;
+            float f[V], s = 0.f, s2 = 0.f;
+            r.load_rw(x + t * p.x_st + q);
+            r.widen(f);
+#pragma unroll
+            for (int k = 0; k < V; ++k) s += f[k];
+            s *= 1.f / V;
+#pragma unroll
+            for (int k = 0; k < V; ++k) s2 = fmaf(f[k] - s, f[k] - s, s2);
+            const float na = count;
+            count += V;
+            const float d = s - mean, w = V / count;
+            mean = fmaf(d, w, mean);
+            m2 += fmaf(d * d, na * w, s2);
+        }
+    }
+    part[0][threadIdx.x] = count;
+    part[1][threadIdx.x] = mean;
+    part[2][threadIdx.x] = m2;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        float na = 0.f, m = 0.f, s = 0.f;
+        for (int i = threadIdx.x; i < kThreads; i += 32) {
+            na += part[0][i];
+            m = fmaf(part[0][i], part[1][i], m);
+        }
+        na = warp_sum(na);
+        m = na > 0.f ? warp_sum(m) / na : 0.f;
+        for (int i = threadIdx.x; i < kThreads; i += 32) {
+            const float d = part[1][i] - m;
+            s += fmaf(part[0][i] * d, d, part[2][i]);
+        }
+        s = warp_sum(s);
+        __syncwarp();
+        if (threadIdx.x == 0) {
+            part[0][0] = na;
+            part[1][0] = m;
+            part[2][0] = s;
+        }
+    }
+    merge_cluster(part, 1, K, p.eps, g_mean, g_rstd);
+    const E *gate = p.gate ? p.gate + b * p.g_sb + c0 : nullptr;
+    E *y = p.y + b * p.T * p.C + c0;
+    for (int64_t t = t_begin; t < t_end; ++t) {
+        for (int q = threadIdx.x * V; q < cg; q += kThreads * V) {
+            Piece<E, V> r, z;
+            float v[V], gv[V], w[V], bias[V];
+            r.load_rw(x + t * p.x_st + q);
+            z.zero();
+            if (gate) z.load(gate + t * p.g_st + q);
+            params<V>(p.w, c0 + q, 1.f, w);
+            params<V>(p.bias, c0 + q, 0.f, bias);
+            r.widen(v);
+            z.widen(gv);
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = (v[k] - g_mean[0]) * g_rstd[0];
+            outputs<V>(v, w, bias, gv, gate != nullptr, p.act);
+            r.round(v);
+            r.store(y + t * p.C + q);
+        }
     }
 }
 
@@ -70,8 +411,85 @@ gdn_status check(const gdn_group_norm_problem *p) {
     if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
     if (p->act != GDN_ACT_NONE && p->act != GDN_ACT_SILU && p->act != GDN_ACT_SIGMOID)
         return GDN_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(p->B) * p->G > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (p->B > (1 << 26) || p->G > 65535) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
+}
+
+template <typename E, int V, int P>
+cudaError_t launch_rows(NormParams<E> &p, cudaStream_t s) {
+    constexpr int R = P == 1 ? 4 : P == 2 ? 2 : 1;
+    const int64_t slots = static_cast<int64_t>(p.G) * p.lanes;
+    // rows in flight: 8 blocks to an SM, or all rows
+    const int64_t most = 152LL * 8 * kThreads / slots;
+    const int64_t flight = most < 1 ? 1 : most < p.B ? most : p.B;
+    p.flight = static_cast<int>(flight);
+    const int64_t blocks = (slots * flight + kThreads - 1) / kThreads;
+    gdn_norm_rows_kernel<E, V, P, R><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename E>
+cudaError_t launch_cluster(void (*kernel)(NormParams<E>), int K, int slices, NormParams<E> &p,
+                           cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(K) * p.B, slices);
+    p.cluster = K;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = K;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = K > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename E, int V>
+cudaError_t launch_tokens(NormParams<E> &p, cudaStream_t s) {
+    const int cg = p.C / p.G;
+    // Slices start at whole pieces; at least 128 bytes of a row, more where that alone gives
+    // every SM its blocks.
+    int unit = 1;
+    while (unit * cg % V != 0) ++unit;
+    auto slices = [&](int groups) { return (p.G + groups - 1) / groups; };
+    if (unit <= p.G && unit * static_cast<int64_t>(cg) / V > kThreads) {
+        if (cg % V != 0) return launch_tokens<E, 1>(p, s);
+        int K = 1;
+        while (K < kMaxCluster && static_cast<int64_t>(p.B) * p.G * K < 4 * 152 && p.T > 2 * K) K *= 2;
+        return launch_cluster(gdn_norm_wide_kernel<E, V>, K, p.G, p, s);
+    }
+    int groups = unit;
+    while (groups < p.G && (groups + unit) * cg / V <= kThreads && groups + unit <= kThreads &&
+           (groups * cg * static_cast<int>(sizeof(E)) < 128 ||
+            static_cast<int64_t>(p.B) * slices(groups + unit) >= 4 * 152))
+        groups += unit;
+    if (groups > p.G) groups = p.G;
+    p.groups = groups;
+    // CTAs to a sequence: 4 blocks to an SM, but 8 turns of each thread at least
+    const int rows = kThreads / (groups * cg / V > 0 ? groups * cg / V : 1);
+    int K = 1;
+    while (K < kMaxCluster && static_cast<int64_t>(p.B) * slices(groups) * K < 4 * 152 &&
+           p.T > 2 * K * rows * 4)
+        K *= 2;
+    return launch_cluster(gdn_norm_tokens_kernel<E, V>, K, slices(groups), p, s);
+}
+
+template <typename E, int V>
+cudaError_t launch_pieces(NormParams<E> &p, cudaStream_t s) {
+    const int cg = p.C / p.G;
+    if (V > 1 && p.T == 1 && cg % V != 0) return launch_pieces<E, 1>(p, s);
+    if (p.T == 1) {
+        const int pieces = cg / V;
+        p.lanes = 1;
+        while (p.lanes < 32 && p.lanes < pieces) p.lanes *= 2;
+        const int per = (pieces + p.lanes - 1) / p.lanes;
+        if (per <= 1) return launch_rows<E, V, 1>(p, s);
+        if (per <= 2) return launch_rows<E, V, 2>(p, s);
+        if (per <= 4) return launch_rows<E, V, 4>(p, s);
+        if (per <= 8) return launch_rows<E, V, 8>(p, s);
+    }
+    return launch_tokens<E, V>(p, s);
 }
 
 template <typename E>
@@ -89,13 +507,17 @@ cudaError_t launch(const gdn_group_norm_problem *pr, const void *x, const float 
     p.x_st = pr->x_stride_t;
     p.g_sb = pr->gate_stride_b;
     p.g_st = pr->gate_stride_t;
+    p.B = pr->B;
     p.T = pr->T;
     p.C = pr->C;
     p.G = pr->G;
     p.act = pr->act;
     p.eps = pr->eps;
-    gdn_group_norm_kernel<E><<<pr->B * pr->G, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    p.lanes = p.flight = p.groups = p.cluster = 1;
+    constexpr int V = 16 / sizeof(E);
+    const bool pieces = pieces16(x, p.B, p.T, p.C, p.x_sb, p.x_st, sizeof(E)) &&
+                        (!gate || pieces16(gate, p.B, p.T, p.C, p.g_sb, p.g_st, sizeof(E)));
+    return pieces ? launch_pieces<E, V>(p, s) : launch_pieces<E, 1>(p, s);
 }
 
 }  // namespace

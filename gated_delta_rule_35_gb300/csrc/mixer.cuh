@@ -144,9 +144,13 @@ __device__ __forceinline__ void load_f32(const float *p, float (&f)[V]) {
     }
 }
 
-// Asynchronous 16-byte copies from global to shared memory, in groups.
+// Asynchronous copies of 16 or 4 bytes from global to shared memory, in groups.
 __device__ __forceinline__ void copy16_async(void *smem, const void *g) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(g) : "memory");
+}
+__device__ __forceinline__ void copy4_async(void *smem, const void *g) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
                      static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(g) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
