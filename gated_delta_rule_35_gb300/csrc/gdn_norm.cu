@@ -31,36 +31,55 @@ struct NormParams {
     int lanes, flight, groups, cluster;
 };
 
-// v (normalised) scaled and shifted, through the activation or the gate.
-template <int V>
-__device__ __forceinline__ void outputs(float (&v)[V], const float (&w)[V], const float (&bias)[V],
-                                        const float (&gate)[V], bool gated, int act) {
+__device__ __forceinline__ F2 both(float v) { return pack2(v, v); }
+__device__ __forceinline__ float halves(F2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    return a + b;
+}
+
+// v (scaled and shifted) through the activation or the gate; one branch for all of a piece.
+template <int N>
+__device__ __forceinline__ void outputs(F2 (&v)[N], const F2 (&gate)[N], bool gated, int act) {
+    if (gated) {
+        if (act == GDN_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-        const int k = V == 1 ? 0 : i + 1;
-        F2 o = fma2(pack2(v[i], v[k]), pack2(w[i], w[k]), pack2(bias[i], bias[k]));
-        o = gated ? mul2(o, activate2(pack2(gate[i], gate[k]), act)) : activate2(o, act);
-        float lo, hi;
-        unpack2(o, lo, hi);
-        v[i] = lo;
-        if (V > 1) v[k] = hi;
+            for (int i = 0; i < N; ++i) v[i] = mul2(v[i], mul2(gate[i], sigmoid2(gate[i])));
+        } else if (act == GDN_ACT_SIGMOID) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = mul2(v[i], sigmoid2(gate[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = mul2(v[i], gate[i]);
+        }
+    } else if (act == GDN_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = mul2(v[i], sigmoid2(v[i]));
+    } else if (act == GDN_ACT_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = sigmoid2(v[i]);
     }
 }
 
+// Parameters of channels c.., `other` without any.
 template <int V>
-__device__ __forceinline__ void params(const float *p, int c, float other, float (&f)[V]) {
+__device__ __forceinline__ void params(const float *p, int c, float other, F2 (&f)[(V + 1) / 2]) {
+    float v[V];
     if (p) {
-        load_f32<V>(p + c, f);
+        load_f32<V>(p + c, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = other;
+        for (int i = 0; i < V; ++i) v[i] = other;
     }
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) f[i] = pack2(v[2 * i], v[V == 1 ? 0 : 2 * i + 1]);
 }
 
 // ------------------------------------------------------------------ single rows
 //
 // `lanes` lanes (a power of two) hold a group, P pieces of V channels to a lane, R rows at a
-// time. A thread keeps its channels from row to row, so weight and bias stay in registers.
+// time, so their sums' shuffles overlap. A thread keeps its channels from row to row: with
+// few pieces weight and bias stay in registers.
 template <typename E, int V, int P, int R>
 __global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p) {
     const int L = p.lanes, cg = p.C / p.G, slots = p.G * L;
@@ -69,7 +88,9 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p
     const int g = i % slots / L;
     int row = i < slots * p.flight ? i / slots : p.B;
     const float inv = 1.f / cg;
-    float w[P][V], bias[P][V];
+    constexpr bool KEEP = P <= 2;                      // weight and bias in registers
+    constexpr int PK = KEEP ? P : 1, N = (V + 1) / 2;
+    F2 w[PK][N], bias[PK][N];
     bool in[P];
     int c[P];
 #pragma unroll
@@ -77,16 +98,27 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p
         const int at = (q * L + j) * V;
         in[q] = at < cg;
         c[q] = g * cg + (in[q] ? at : 0);
-        params<V>(p.w, c[q], 1.f, w[q]);
-        params<V>(p.bias, c[q], 0.f, bias[q]);
+        if constexpr (KEEP) {
+            params<V>(p.w, c[q], 1.f, w[q]);
+            params<V>(p.bias, c[q], 0.f, bias[q]);
+        }
     }
+    // sums over the group's lanes, of R rows at once
+    auto group_sums = [&](float (&s)[R]) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            if (o >= L) continue;                      // alike for all threads
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+        }
+    };
     // every thread takes the same number of turns: the shuffles need whole warps
     for (int done = 0; done < p.B; done += R * p.flight, row += R * p.flight) {
         Piece<E, V> x[R][P], gate[R][P];
         bool live[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t b = row + r * p.flight;
+            const int64_t b = row + static_cast<int64_t>(r) * p.flight;
             live[r] = b < p.B && (!p.lengths || p.lengths[b] > 0);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
@@ -98,36 +130,58 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p
                 }
             }
         }
+        float mean[R], s[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float v[P][V], s = 0.f;
+            F2 sum = 0;
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-                x[r][q].widen(v[q]);
+                F2 v[N];
+                x[r][q].widen(v);
 #pragma unroll
-                for (int k = 0; k < V; ++k) s += v[q][k];
+                for (int k = 0; k < N; ++k) sum = add2(sum, v[k]);
             }
-            for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const float mean = s * inv;
-            s = 0.f;
+            mean[r] = V == 1 ? 0.5f * halves(sum) : halves(sum);
+        }
+        group_sums(mean);
 #pragma unroll
-            for (int q = 0; q < P; ++q)
+        for (int r = 0; r < R; ++r) {
+            mean[r] *= inv;
+            F2 sum = 0;
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    v[q][k] -= mean;
-                    if (in[q]) s = fmaf(v[q][k], v[q][k], s);
+            for (int q = 0; q < P; ++q) {
+                if (P > 1 && !in[q]) continue;
+                F2 v[N];
+                x[r][q].widen(v);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    v[k] = add2(v[k], both(-mean[r]));
+                    sum = fma2(v[k], v[k], sum);
                 }
-            for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const float rstd = rsqrtf(fmaf(s, inv, p.eps));
+            }
+            s[r] = V == 1 ? 0.5f * halves(sum) : halves(sum);
+            if (P == 1 && !in[0]) s[r] = 0.f;
+        }
+        group_sums(s);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const F2 rstd = both(rsqrtf(fmaf(s[r], inv, p.eps)));
 #pragma unroll
             for (int q = 0; q < P; ++q) {
                 if (!live[r] || !in[q]) continue;
-                float gv[V];
-                gate[r][q].widen(gv);
+                F2 v[N], z[N];
+                if constexpr (!KEEP) {
+                    params<V>(p.w, c[q], 1.f, w[0]);
+                    params<V>(p.bias, c[q], 0.f, bias[0]);
+                }
+                x[r][q].widen(v);
+                gate[r][q].widen(z);
 #pragma unroll
-                for (int k = 0; k < V; ++k) v[q][k] *= rstd;
-                outputs<V>(v[q], w[q], bias[q], gv, p.gate != nullptr, p.act);
-                x[r][q].round(v[q]);
+                for (int k = 0; k < N; ++k)
+                    v[k] = fma2(add2(v[k], both(-mean[r])), mul2(w[KEEP ? q : 0][k], rstd),
+                                bias[KEEP ? q : 0][k]);
+                outputs(v, z, p.gate != nullptr, p.act);
+                x[r][q].round(v);
                 x[r][q].store(p.y + (row + static_cast<int64_t>(r) * p.flight) * p.C + c[q]);
             }
         }
@@ -138,12 +192,14 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p
 //
 // The CTAs of a cluster take equal shares of a sequence's valid tokens, for one slice of
 // `groups` groups. A thread keeps one piece of V channels and takes every RP-th
-// token, eight at a time: their mean and the squares about it, merged into the running
-// (count, mean, squares) of each channel by the exact update for two sets,
-//   mean += d nb / n,   M2 += M2b + d^2 na nb / n   with d = mean_b - mean,
-// which loses nothing where the mean is far from zero. Channels and threads then merge to
-// groups, and the CTAs' groups through distributed shared memory, in rank order.
+// token. It sums x - k and (x - k)^2, k the channel's mean over its first 8 tokens, over up
+// to 16 blocks of 8 tokens, and merges these sets by the exact update for two,
+//   mean += d nb / n,   M2 += M2b + d^2 na nb / n   with d = mean_b - mean.
+// The mean of a set lies at most sqrt(16) of its deviations from k, so at most 17 times the
+// variance's rounding is lost, however far the mean is from zero. Channels and threads then
+// merge to groups, and the CTAs' groups through distributed shared memory, in rank order.
 constexpr int kBlockTokens = 8;
+constexpr int kSetBlocks = 16;
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -184,7 +240,7 @@ __device__ __forceinline__ void merge_cluster(float (&part)[3][kThreads], int gr
 }
 
 template <typename E, int V>
-__global__ void __launch_bounds__(kThreads) gdn_norm_tokens_kernel(NormParams<E> p) {
+__global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kernel(NormParams<E> p) {
     __shared__ float means[kThreads * V], squares[kThreads * V];   // [token row][channel of the slice]
     __shared__ float part[3][kThreads];                            // count, mean, squares of a group
     __shared__ float g_mean[kThreads], g_rstd[kThreads];
@@ -199,64 +255,93 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_tokens_kernel(NormParams<E>
     const bool mine = row < RP;
     const E *x = p.x + b * p.x_sb + c;
 
-    float mean[V], m2[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) mean[k] = m2[k] = 0.f;
-    float count = 0.f;
+    constexpr int N = (V + 1) / 2;
+    const int64_t step = RP * p.x_st;
     if (mine) {
-        int t = t_begin + row;
-        for (; t + (kBlockTokens - 1) * RP < t_end; t += kBlockTokens * RP) {
-            Piece<E, V> r[kBlockTokens];
+        F2 mean[N], m2[N];
 #pragma unroll
-            for (int u = 0; u < kBlockTokens; ++u) r[u].load_rw(x + (t + static_cast<int64_t>(u) * RP) * p.x_st);
-            const float na = count;
-            count += kBlockTokens;
-            const float f = kBlockTokens / count;
-            float f0[V], s[V], s2[V];
+        for (int k = 0; k < N; ++k) mean[k] = m2[k] = 0;
+        float count = 0.f;
+        const E *from = x + (t_begin + row) * p.x_st;
+        int left = (t_end - t_begin - row + RP - 1) / RP;      // tokens of this thread
+        while (left > 0) {
+            const int set = min(left, kSetBlocks * kBlockTokens);
+            left -= set;
+            F2 shift[N], s1[N], s2[N];
 #pragma unroll
-            for (int k = 0; k < V; ++k) s[k] = s2[k] = 0.f;
+            for (int k = 0; k < N; ++k) s1[k] = s2[k] = 0;
+            // the next block's loads are in flight while one is summed
+            Piece<E, V> next[kBlockTokens];
+            auto fetch = [&](int tokens) {
 #pragma unroll
-            for (int u = 0; u < kBlockTokens; ++u) {
-                r[u].widen(f0);
+                for (int u = 0; u < kBlockTokens; ++u)
+                    if (u < tokens) next[u].load_rw(from + u * step);
+                from += min(max(tokens, 0), kBlockTokens) * step;
+            };
+            fetch(set);
+            for (int done = 0; done < set; done += kBlockTokens) {
+                Piece<E, V> now[kBlockTokens];
+                const int here = min(set - done, kBlockTokens);
 #pragma unroll
-                for (int k = 0; k < V; ++k) s[k] += f0[k];
-            }
+                for (int u = 0; u < kBlockTokens; ++u) now[u] = next[u];
+                fetch(set - done - kBlockTokens);
+                F2 v[N], b1[N], b2[N];
 #pragma unroll
-            for (int k = 0; k < V; ++k) s[k] *= 1.f / kBlockTokens;
+                for (int k = 0; k < N; ++k) b1[k] = b2[k] = 0;
+                if (done == 0) {
 #pragma unroll
-            for (int u = 0; u < kBlockTokens; ++u) {
-                r[u].widen(f0);
+                    for (int u = 0; u < kBlockTokens; ++u) {
+                        if (u >= here) break;
+                        now[u].widen(v);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const float d = f0[k] - s[k];
-                    s2[k] = fmaf(d, d, s2[k]);
+                        for (int k = 0; k < N; ++k) b1[k] = add2(b1[k], v[k]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        shift[k] = mul2(b1[k], both(-1.f / here));
+                        b1[k] = 0;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kBlockTokens; ++u) {
+                    if (u >= here) break;
+                    now[u].widen(v);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        v[k] = add2(v[k], shift[k]);
+                        b1[k] = add2(b1[k], v[k]);
+                        b2[k] = fma2(v[k], v[k], b2[k]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    s1[k] = add2(s1[k], b1[k]);
+                    s2[k] = add2(s2[k], b2[k]);
                 }
             }
+            const float nb = static_cast<float>(set), na = count;
+            count += nb;
+            const float f = nb / count;
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float d = s[k] - mean[k];
-                mean[k] = fmaf(d, f, mean[k]);
-                m2[k] += fmaf(d * d, na * f, s2[k]);
-            }
-        }
-        for (; t < t_end; t += RP) {
-            Piece<E, V> r;
-            float f0[V];
-            r.load_rw(x + t * p.x_st);
-            r.widen(f0);
-            count += 1.f;
-            const float f = 1.f / count;
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float d = f0[k] - mean[k];
-                mean[k] = fmaf(d, f, mean[k]);
-                m2[k] = fmaf(d, f0[k] - mean[k], m2[k]);
+            for (int k = 0; k < N; ++k) {
+                const F2 off = mul2(s1[k], both(1.f / nb));             // the set's mean - k
+                const F2 set2 = fma2(mul2(off, s1[k]), both(-1.f), s2[k]);
+                const F2 set1 = fma2(shift[k], both(-1.f), off);        // the set's mean
+                const F2 d = fma2(mean[k], both(-1.f), set1);
+                mean[k] = fma2(d, both(f), mean[k]);
+                m2[k] = add2(m2[k], fma2(mul2(d, d), both(na * f), set2));
             }
         }
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            means[row * SC + q + k] = mean[k];
-            squares[row * SC + q + k] = m2[k];
+        for (int k = 0; k < N; ++k) {
+            float a, b;
+            float *to = means + row * SC + q + 2 * k, *to2 = squares + row * SC + q + 2 * k;
+            unpack2(mean[k], a, b);
+            to[0] = a;
+            if (V > 1) to[1] = b;
+            unpack2(m2[k], a, b);
+            to2[0] = a;
+            if (V > 1) to2[1] = b;
         }
     }
     __syncthreads();
@@ -287,40 +372,57 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_tokens_kernel(NormParams<E>
     }
     merge_cluster(part, ng, K, p.eps, g_mean, g_rstd);
     if (!mine) return;
-    float w[V], bias[V];
+    F2 w[N], bias[N], mean[N];
     params<V>(p.w, c, 1.f, w);
     params<V>(p.bias, c, 0.f, bias);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        mean[k] = g_mean[(q + k) / cg];
-        w[k] *= g_rstd[(q + k) / cg];
+    for (int k = 0; k < N; ++k) {
+        const int ga = (q + 2 * k) / cg, gb = V == 1 ? ga : (q + 2 * k + 1) / cg;
+        mean[k] = pack2(-g_mean[ga], -g_mean[gb]);
+        w[k] = mul2(w[k], pack2(g_rstd[ga], g_rstd[gb]));
     }
-    const E *gate = p.gate ? p.gate + b * p.g_sb + c : nullptr;
-    E *y = p.y + b * p.T * p.C + c;
-    auto finish = [&](Piece<E, V> &r, const Piece<E, V> &z, int64_t t) {
-        float v[V], gv[V];
-        r.widen(v);
-        z.widen(gv);
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] -= mean[k];
-        outputs<V>(v, w, bias, gv, gate != nullptr, p.act);
-        r.round(v);
-        r.store(y + t * p.C);
-    };
     constexpr int U = 4;
-    for (int t = t_begin + row; t < t_end; t += U * RP) {
-        Piece<E, V> r[U], z[U];
+    const int64_t g_step = RP * p.g_st, y_step = static_cast<int64_t>(RP) * p.C;
+    const E *from = x + (t_begin + row) * p.x_st;
+    const E *gate = p.gate ? p.gate + b * p.g_sb + c + (t_begin + row) * p.g_st : nullptr;
+    E *to = p.y + (b * p.T + t_begin + row) * p.C + c;
+    Piece<E, V> r[U], z[U];
+    auto fetch = [&](int tokens) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            z[u].zero();
-            if (t + u * RP < t_end) {
-                r[u].load_rw(x + (t + static_cast<int64_t>(u) * RP) * p.x_st);
-                if (gate) z[u].load(gate + (t + static_cast<int64_t>(u) * RP) * p.g_st);
-            }
+            if (u >= tokens) break;
+            r[u].load_rw(from + u * step);
+            if (gate) z[u].load(gate + u * g_step);
         }
+        from += U * step;
+        if (gate) gate += U * g_step;
+    };
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u * RP < t_end) finish(r[u], z[u], t + static_cast<int64_t>(u) * RP);
+    for (int u = 0; u < U; ++u) z[u].zero();
+    int left = (t_end - t_begin - row + RP - 1) / RP;
+    const bool gated = gate != nullptr;
+    fetch(left);
+    for (; left > 0; left -= U) {
+        Piece<E, V> nr[U], nz[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            nr[u] = r[u];
+            nz[u] = z[u];
+        }
+        fetch(left - U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u >= left) break;
+            F2 v[N], gv[N];
+            nr[u].widen(v);
+            nz[u].widen(gv);
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = fma2(add2(v[k], mean[k]), w[k], bias[k]);
+            outputs(v, gv, gated, p.act);
+            nr[u].round(v);
+            nr[u].store(to + u * y_step);
+        }
+        to += U * y_step;
     }
 }
 
@@ -384,8 +486,9 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
     E *y = p.y + b * p.T * p.C + c0;
     for (int64_t t = t_begin; t < t_end; ++t) {
         for (int q = threadIdx.x * V; q < cg; q += kThreads * V) {
+            constexpr int N = (V + 1) / 2;
             Piece<E, V> r, z;
-            float v[V], gv[V], w[V], bias[V];
+            F2 v[N], gv[N], w[N], bias[N];
             r.load_rw(x + t * p.x_st + q);
             z.zero();
             if (gate) z.load(gate + t * p.g_st + q);
@@ -394,8 +497,9 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
             r.widen(v);
             z.widen(gv);
 #pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = (v[k] - g_mean[0]) * g_rstd[0];
-            outputs<V>(v, w, bias, gv, gate != nullptr, p.act);
+            for (int k = 0; k < N; ++k)
+                v[k] = fma2(add2(v[k], both(-g_mean[0])), mul2(w[k], both(g_rstd[0])), bias[k]);
+            outputs(v, gv, gate != nullptr, p.act);
             r.round(v);
             r.store(y + t * p.C + q);
         }
@@ -448,30 +552,38 @@ cudaError_t launch_cluster(void (*kernel)(NormParams<E>), int K, int slices, Nor
 template <typename E, int V>
 cudaError_t launch_tokens(NormParams<E> &p, cudaStream_t s) {
     const int cg = p.C / p.G;
-    // Slices start at whole pieces; at least 128 bytes of a row, more where that alone gives
-    // every SM its blocks.
+    // Slices start at whole pieces.
     int unit = 1;
     while (unit * cg % V != 0) ++unit;
-    auto slices = [&](int groups) { return (p.G + groups - 1) / groups; };
     if (unit <= p.G && unit * static_cast<int64_t>(cg) / V > kThreads) {
         if (cg % V != 0) return launch_tokens<E, 1>(p, s);
         int K = 1;
         while (K < kMaxCluster && static_cast<int64_t>(p.B) * p.G * K < 4 * 152 && p.T > 2 * K) K *= 2;
         return launch_cluster(gdn_norm_wide_kernel<E, V>, K, p.G, p, s);
     }
-    int groups = unit;
-    while (groups < p.G && (groups + unit) * cg / V <= kThreads && groups + unit <= kThreads &&
-           (groups * cg * static_cast<int>(sizeof(E)) < 128 ||
-            static_cast<int64_t>(p.B) * slices(groups + unit) >= 4 * 152))
-        groups += unit;
-    if (groups > p.G) groups = p.G;
+    // Slice and cluster by the turns that a thread takes: its tokens, and about 8 for the
+    // merges, for every wave of blocks (2 or 4 to an SM by registers), and the sectors that
+    // the ends of a row's slice waste.
+    auto slices = [&](int groups) { return (p.G + groups - 1) / groups; };
+    constexpr int64_t wave = 152 * (V > 1 ? 2 : 4);
+    int groups = unit, K = 1;
+    float best = 0.f;
+    for (int n = unit; n == unit || (n / 2 < p.G && n * cg / V <= kThreads && n <= kThreads); n *= 2) {
+        const int m = n < p.G ? n : p.G, rows = kThreads / (m * cg / V);
+        for (int k = 1; k <= kMaxCluster; k *= 2) {
+            const int64_t blocks = static_cast<int64_t>(p.B) * slices(m) * k;
+            const int share = (p.T + k - 1) / k;
+            const float turns = static_cast<float>((share + rows - 1) / rows + 8) *
+                                (1.f + 16.f / (m * cg * sizeof(E)));
+            const float cost = turns * ((blocks + wave - 1) / wave);
+            if (best == 0.f || cost < best) {
+                best = cost;
+                groups = m;
+                K = k;
+            }
+        }
+    }
     p.groups = groups;
-    // CTAs to a sequence: 4 blocks to an SM, but 8 turns of each thread at least
-    const int rows = kThreads / (groups * cg / V > 0 ? groups * cg / V : 1);
-    int K = 1;
-    while (K < kMaxCluster && static_cast<int64_t>(p.B) * slices(groups) * K < 4 * 152 &&
-           p.T > 2 * K * rows * 4)
-        K *= 2;
     return launch_cluster(gdn_norm_tokens_kernel<E, V>, K, slices(groups), p, s);
 }
 
@@ -488,6 +600,7 @@ cudaError_t launch_pieces(NormParams<E> &p, cudaStream_t s) {
         if (per <= 2) return launch_rows<E, V, 2>(p, s);
         if (per <= 4) return launch_rows<E, V, 4>(p, s);
         if (per <= 8) return launch_rows<E, V, 8>(p, s);
+        if (V <= 4 && per <= 16) return launch_rows<E, V, V <= 4 ? 16 : 8>(p, s);
     }
     return launch_tokens<E, V>(p, s);
 }

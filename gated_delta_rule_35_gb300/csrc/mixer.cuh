@@ -70,13 +70,16 @@ __device__ __forceinline__ float activate(float v, int act) {
     return act == GDN_ACT_SILU ? v * s : s;
 }
 
-// activate() of two values.
-__device__ __forceinline__ F2 activate2(F2 v, int act) {
-    if (act == GDN_ACT_NONE) return v;
+// Of two values: sigmoid, activate.
+__device__ __forceinline__ F2 sigmoid2(F2 v) {
     float a, b;
     unpack2(mul2(v, pack2(-kLog2e, -kLog2e)), a, b);
     unpack2(add2(pack2(exp2_ftz(a), exp2_ftz(b)), pack2(1.f, 1.f)), a, b);
-    const F2 s = pack2(rcp_ftz(a), rcp_ftz(b));
+    return pack2(rcp_ftz(a), rcp_ftz(b));
+}
+__device__ __forceinline__ F2 activate2(F2 v, int act) {
+    if (act == GDN_ACT_NONE) return v;
+    const F2 s = sigmoid2(v);
     return act == GDN_ACT_SILU ? mul2(v, s) : s;
 }
 
@@ -110,6 +113,20 @@ struct Piece {
                 f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
             }
         }
+    }
+    // the same in pairs (a single element in both halves)
+    static constexpr int pairs = (V + 1) / 2;
+    __device__ __forceinline__ void widen(F2 (&f)[pairs]) const {
+        float v[V];
+        widen(v);
+#pragma unroll
+        for (int i = 0; i < pairs; ++i) f[i] = pack2(v[2 * i], v[V == 1 ? 0 : 2 * i + 1]);
+    }
+    __device__ __forceinline__ void round(const F2 (&f)[pairs]) {
+        float v[V + 1];
+#pragma unroll
+        for (int i = 0; i < pairs; ++i) unpack2(f[i], v[2 * i], v[2 * i + 1]);
+        round(reinterpret_cast<const float (&)[V]>(v));
     }
     __device__ __forceinline__ void round(const float (&f)[V]) {
         if constexpr (V == 1) {
