@@ -242,6 +242,7 @@ __device__ __forceinline__ void merge_cluster(float (&part)[3][kThreads], int gr
 template <typename E, int V>
 __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kernel(NormParams<E> p) {
     __shared__ float means[kThreads * V], squares[kThreads * V];   // [token row][channel of the slice]
+    __shared__ float columns[kThreads * V];                        // sums over token rows
     __shared__ float part[3][kThreads];                            // count, mean, squares of a group
     __shared__ float g_mean[kThreads], g_rstd[kThreads];
     const int cg = p.C / p.G, K = p.cluster, rank = blockIdx.x % K;
@@ -345,31 +346,41 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
         }
     }
     __syncthreads();
-    // a warp merges a group: its cg channels of RP token rows, each with the row's count
-    for (int g = threadIdx.x / 32; g < ng; g += kThreads / 32) {
-        auto rows_of = [&](int r) {      // tokens of row r
-            const int left = t_end - t_begin - r;
-            return left > 0 ? static_cast<float>((left + RP - 1) / RP) : 0.f;
-        };
-        const int entries = RP * cg;
-        float s = 0.f;
-        for (int i = threadIdx.x % 32; i < entries; i += 32)
-            s = fmaf(rows_of(i / cg), means[i / cg * SC + g * cg + i % cg], s);
-        const float total = static_cast<float>(t_end - t_begin) * cg;
-        const float m = total > 0.f ? warp_sum(s) / total : 0.f;
-        s = 0.f;
-        for (int i = threadIdx.x % 32; i < entries; i += 32) {
-            const int at = i / cg * SC + g * cg + i % cg;
-            const float d = means[at] - m;
-            s += fmaf(rows_of(i / cg) * d, d, squares[at]);
+    // Merge the token rows, then the channels, to groups: the weighted means first, then the
+    // squares about the group's mean. Threads take a channel's rows (several threads to
+    // a channel where they suffice), warps the groups.
+    const int tokens = t_end - t_begin, full = tokens / RP, more = tokens % RP;
+    const float total = static_cast<float>(tokens) * cg;
+    const int CT = min(SC, kThreads), RL = kThreads / CT, rl = threadIdx.x / CT;
+    auto over_rows = [&](auto term) {
+        for (int col = threadIdx.x % CT; rl < RL && col < SC; col += CT) {
+            float sum = 0.f;
+            for (int r = rl; r < RP; r += RL)
+                sum += term(static_cast<float>(full + (r < more)), r * SC + col, col);
+            columns[rl * SC + col] = sum;
         }
-        s = warp_sum(s);
-        if (threadIdx.x % 32 == 0) {
-            part[0][g] = total;
-            part[1][g] = m;
-            part[2][g] = s;
+        __syncthreads();
+    };
+    auto over_channels = [&](auto keep) {
+        for (int g = threadIdx.x / 32; g < ng; g += kThreads / 32) {
+            float sum = 0.f;
+            for (int r = 0; r < RL; ++r)
+                for (int i = threadIdx.x % 32; i < cg; i += 32) sum += columns[r * SC + g * cg + i];
+            sum = warp_sum(sum);
+            if (threadIdx.x % 32 == 0) keep(g, sum);
         }
-    }
+        __syncthreads();
+    };
+    over_rows([&](float count, int at, int) { return count * means[at]; });
+    over_channels([&](int g, float sum) {
+        part[0][g] = total;
+        part[1][g] = total > 0.f ? sum / total : 0.f;
+    });
+    over_rows([&](float count, int at, int col) {
+        const float d = means[at] - part[1][col / cg];
+        return fmaf(count * d, d, squares[at]);
+    });
+    over_channels([&](int g, float sum) { part[2][g] = sum; });
     merge_cluster(part, ng, K, p.eps, g_mean, g_rstd);
     if (!mine) return;
     F2 w[N], bias[N], mean[N];
