@@ -68,26 +68,26 @@ __device__ __forceinline__ float4 widen4(const __nv_bfloat16 *p, int left) {
 
 // ----------------------------------------------------------------- a few tokens
 //
-// L = NP / 4 lanes share a channel, four states to a lane, and each thread advances
-// kBatch sequences, so their states' loads are in flight together and A is read
-// once for all of them.
+// Bound by the states' traffic: each is read and written once. L = NP / 4 lanes share a
+// channel, four states to a lane, and a thread advances NB sequences, so that their
+// states' loads are in flight together and A is read once for all of them. Of a channel's
+// L lanes, lane m % L takes Delta, the gate and the output of sequence m.
 constexpr int kBatch = 4;
 
 template <typename E, int NP, int NB>
 __global__ void __launch_bounds__(kThreads) gdn_scan_step_kernel(const ScanParams<E> p) {
-    constexpr int L = NP / 4;
-    const int i = blockIdx.x * kThreads + threadIdx.x;
-    const int d = i / L, n0 = i % L * 4;
+    constexpr int L = NP / 4, channels = kThreads / L, OWN = (NB + L - 1) / L;
+    __shared__ __align__(16) float bc[NB][2][NP];      // a token's B and C rows
+    const int per = p.D / p.G, blocks = (per + channels - 1) / channels;
+    const int g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * channels;
+    const int tid = threadIdx.x, c = tid / L, j = tid % L, n0 = j * 4;
+    const bool live = c0 + c < per;
+    const int d = g * per + c0 + (live ? c : 0);
     const int b0 = blockIdx.y * NB;
-    const bool live = d < p.D;         // whole lane groups: L divides the block
-    const int dd = live ? d : 0, g = dd / (p.D / p.G);
     const bool quads = p.N % 4 == 0;   // rows of states are whole 16-byte pieces
-    float A2[4], h[NB][4];
-    const float bias = p.dt_bias ? p.dt_bias[dd] : 0.f, skip = p.skip ? p.skip[dd] : 0.f;
     auto quad = [&](const float *row, float (&f)[4]) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) f[k] = 0.f;
-        if (!live) return;
         if (quads) {
             if (n0 < p.N) {
                 const float4 q = *reinterpret_cast<const float4 *>(row + n0);
@@ -99,49 +99,78 @@ __global__ void __launch_bounds__(kThreads) gdn_scan_step_kernel(const ScanParam
                 if (n0 + k < p.N) f[k] = row[n0 + k];
         }
     };
-    auto state = [&](int b) { return (static_cast<int64_t>(b) * p.D + dd) * p.N; };
+    auto state = [&](int m) { return (static_cast<int64_t>(b0 + m) * p.D + d) * p.N; };
+    float A2[4], h[NB][4];
 #pragma unroll
     for (int m = 0; m < NB; ++m) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[m][k] = 0.f;
-        if (p.h0 && b0 + m < p.B) quad(p.h0 + state(b0 + m), h[m]);
+        if (p.h0 && b0 + m < p.B) quad(p.h0 + state(m), h[m]);
     }
-    quad(p.A + static_cast<int64_t>(dd) * p.N, A2);
+    quad(p.A + static_cast<int64_t>(d) * p.N, A2);
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
 
     for (int t = 0; t < p.T; ++t) {
+        if (t > 0) __syncthreads();
+        // behind a sequence's end: B = C = 0, Delta = 0
+        for (int i = tid; i < NB * 2 * NP; i += kThreads) {
+            const int q = i % NP;
+            const int64_t b = b0 + i / (2 * NP);
+            float v = 0.f;
+            if (b < p.B && q < p.N && t < valid_tokens(p.lengths, b, p.T))
+                v = to_f32(i / NP % 2 ? p.Cm[b * p.c_sb + t * p.c_st + static_cast<int64_t>(g) * p.N + q]
+                                      : p.Bm[b * p.b_sb + t * p.b_st + static_cast<int64_t>(g) * p.N + q]);
+            (&bc[0][0][0])[i] = v;
+        }
+        float x[OWN], z[OWN], step[OWN], u[OWN], y[OWN];
+        bool mine[OWN];
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            const int64_t b = b0 + o * L + j;
+            mine[o] = o * L + j < NB && b < p.B && t < valid_tokens(p.lengths, b < p.B ? b : 0, p.T);
+            x[o] = z[o] = step[o] = y[o] = 0.f;
+            if (mine[o]) {
+                x[o] = to_f32(p.x[b * p.x_sb + t * p.x_st + d]);
+                step[o] = to_f32(p.dt[b * p.dt_sb + t * p.dt_st + d]) + bias;
+                if (p.z) z[o] = to_f32(p.z[b * p.z_sb + t * p.z_st + d]);
+                if (p.softplus) step[o] = softplus(step[o]);
+            }
+            u[o] = step[o] * x[o];
+        }
+        __syncthreads();
 #pragma unroll
         for (int m = 0; m < NB; ++m) {
-            const int64_t b = b0 + m;
-            if (b >= p.B || t >= valid_tokens(p.lengths, b, p.T)) continue;   // the block's alike
-            const float x = to_f32(p.x[b * p.x_sb + t * p.x_st + dd]);
-            float dt = to_f32(p.dt[b * p.dt_sb + t * p.dt_st + dd]) + bias;
-            if (p.softplus) dt = softplus(dt);
-            const E *bm = p.Bm + b * p.b_sb + t * p.b_st + static_cast<int64_t>(g) * p.N + n0;
-            const E *cm = p.Cm + b * p.c_sb + t * p.c_st + static_cast<int64_t>(g) * p.N + n0;
-            float y = 0.f;
-            const float u = dt * x;
+            const int from = (tid & 31 & ~(L - 1)) | m % L;
+            const float dt = __shfl_sync(0xffffffffu, step[m / L], from);
+            const float du = __shfl_sync(0xffffffffu, u[m / L], from);
+            const float4 bq = *reinterpret_cast<const float4 *>(&bc[m][0][n0]);
+            const float4 cq = *reinterpret_cast<const float4 *>(&bc[m][1][n0]);
+            const float bv[4] = {bq.x, bq.y, bq.z, bq.w}, cv[4] = {cq.x, cq.y, cq.z, cq.w};
+            float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const bool in = n0 + k < p.N;
-                h[m][k] = fmaf(exp2_ftz(dt * A2[k]), h[m][k], u * (in ? to_f32(bm[k]) : 0.f));
-                y = fmaf(in ? to_f32(cm[k]) : 0.f, h[m][k], y);
+                h[m][k] = fmaf(exp2_ftz(dt * A2[k]), h[m][k], du * bv[k]);
+                sum = fmaf(cv[k], h[m][k], sum);
             }
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            if (live && n0 == 0) {
-                y = fmaf(skip, x, y);
-                if (p.z) y *= activate(to_f32(p.z[b * p.z_sb + t * p.z_st + d]), GDN_ACT_SILU);
-                p.y[(b * p.T + t) * p.D + d] = from_f32<E>(y);
-            }
+            for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (m % L == j) y[m / L] = sum;
+        }
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            if (!mine[o] || !live) continue;
+            if (p.skip) y[o] = fmaf(skip, x[o], y[o]);
+            if (p.z) y[o] *= activate(z[o], GDN_ACT_SILU);
+            p.y[(static_cast<int64_t>(b0 + o * L + j) * p.T + t) * p.D + d] = from_f32<E>(y[o]);
         }
     }
     if (!p.h_final || !live) return;
 #pragma unroll
     for (int m = 0; m < NB; ++m) {
         if (b0 + m >= p.B) break;
-        float *row = p.h_final + state(b0 + m) + n0;
+        float *row = p.h_final + state(m) + n0;
         if (quads) {
             if (n0 < p.N) *reinterpret_cast<float4 *>(row) = make_float4(h[m][0], h[m][1], h[m][2], h[m][3]);
         } else {
@@ -519,12 +548,13 @@ template <typename E, int NP>
 cudaError_t launch(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace, cudaStream_t s) {
     if (pr->T <= kStepTokens) {
         // kBatch sequences to a thread where that still leaves two blocks to an SM
-        const int64_t blocks = (static_cast<int64_t>(pr->D) * (NP / 4) + kThreads - 1) / kThreads;
-        if (blocks * ((pr->B + kBatch - 1) / kBatch) >= 2 * 152)
+        constexpr int channels = kThreads / (NP / 4);
+        const unsigned blocks = pr->G * ((pr->D / pr->G + channels - 1) / channels);
+        if (static_cast<int64_t>(blocks) * ((pr->B + kBatch - 1) / kBatch) >= 2 * 152)
             gdn_scan_step_kernel<E, NP, kBatch>
-                <<<dim3(static_cast<unsigned>(blocks), (pr->B + kBatch - 1) / kBatch), kThreads, 0, s>>>(p);
+                <<<dim3(blocks, (pr->B + kBatch - 1) / kBatch), kThreads, 0, s>>>(p);
         else
-            gdn_scan_step_kernel<E, NP, 1><<<dim3(static_cast<unsigned>(blocks), pr->B), kThreads, 0, s>>>(p);
+            gdn_scan_step_kernel<E, NP, 1><<<dim3(blocks, pr->B), kThreads, 0, s>>>(p);
         return cudaGetLastError();
     }
     constexpr size_t e = sizeof(E);
