@@ -21,7 +21,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kUnroll = 4;      // tokens per turn
 constexpr int kStages = 4;      // turns in the ring, all but one of them in flight
-constexpr int kStepTokens = 4;  // up to here one thread takes all tokens, one at a time
+constexpr int kStepTokens = 4;  // up to here the step kernel
 constexpr int kMaxRun = 64;     // tokens per thread at most; a call of several runs has kUnroll or more to
                                 // each, so that only the first run reads the window state
 static_assert(kUnroll >= 3, "W - 1");
@@ -34,7 +34,7 @@ struct ConvParams {
     const int32_t *lengths;
     E *y, *state_out;
     int64_t sb, st;
-    int T, C, act, run;
+    int B, T, C, act, run;
 };
 
 // Inputs at token t of sequence b, channels c..; t >= -(W - 1), tokens before 0 come
@@ -52,8 +52,9 @@ __device__ __forceinline__ void input_at(Piece<E, V> &q, const ConvParams<E> &p,
 
 // SILU: its activation without a branch per value, the others by p.act.
 // RING: 16-byte pieces reach the thread through its ring of slots in shared memory.
-template <typename E, int W, int V, int U, bool SILU, bool RING = (V > 1 && U > 1)>
+template <typename E, int W, int V, bool SILU, bool RING = (V > 1)>
 __global__ void __launch_bounds__(kThreads) gdn_conv_kernel(const ConvParams<E> p) {
+    constexpr int U = kUnroll;
     const int cv = p.C / V;                            // pieces of a row
     const int i = blockIdx.x * kThreads + threadIdx.x;
     const int c = i % cv * V, t0 = i / cv * p.run;     // runs of a piece lie cv threads apart
@@ -187,6 +188,77 @@ __global__ void __launch_bounds__(kThreads) gdn_conv_kernel(const ConvParams<E> 
     }
 }
 
+// A few tokens: a thread takes a piece of NB sequences, whose windows' and tokens' loads
+// are in flight together, and reads the weights once for all of them.
+constexpr int kStepBatch = 4;
+
+template <typename E, int W, int V, int NB, bool SILU>
+__global__ void __launch_bounds__(kThreads) gdn_conv_step_kernel(const ConvParams<E> p) {
+    constexpr int P = (V + 1) / 2;
+    const int c = (blockIdx.x * kThreads + threadIdx.x) * V;
+    const int b0 = blockIdx.y * NB;
+    if (c >= p.C) return;
+    Piece<E, V> win[NB][W - 1], x[NB];
+    int n[NB];
+#pragma unroll
+    for (int m = 0; m < NB; ++m) {
+        const int64_t b = b0 + m;
+        n[m] = b < p.B ? valid_tokens(p.lengths, b, p.T) : 0;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            win[m][k].zero();
+            if (b < p.B && p.state_in) win[m][k].load_rw(p.state_in + (b * (W - 1) + k) * p.C + c);
+        }
+        if (n[m] > 0) x[m].load(p.x + b * p.sb + c);
+    }
+    F2 w2[P][W], bias2[P];
+    {
+        float w[V * W], bias[V];
+        load_f32<V * W>(p.w + static_cast<int64_t>(c) * W, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) bias[j] = 0.f;
+        if (p.bias) load_f32<V>(p.bias + c, bias);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const int o = V == 1 ? 0 : 2 * j + 1;
+            bias2[j] = pack2(bias[2 * j], bias[o]);
+#pragma unroll
+            for (int k = 0; k < W; ++k) w2[j][k] = pack2(w[2 * j * W + k], w[o * W + k]);
+        }
+    }
+    for (int t = 0; t < p.T; ++t) {
+#pragma unroll
+        for (int m = 0; m < NB; ++m) {
+            if (t >= n[m]) continue;
+            const int64_t b = b0 + m;
+            F2 v[P], in[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] = bias2[j];
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                if (k < W - 1) win[m][k].widen(in); else x[m].widen(in);
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[j] = fma2(w2[j][k], in[j], v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] = activate2(v[j], SILU ? GDN_ACT_SILU : p.act);
+            Piece<E, V> r;
+            r.round(v);
+            r.store(p.y + (b * p.T + t) * p.C + c);
+#pragma unroll
+            for (int k = 0; k < W - 2; ++k) win[m][k] = win[m][k + 1];
+            win[m][W - 2] = x[m];
+            if (t + 1 < n[m]) x[m].load(p.x + b * p.sb + (t + 1) * p.st + c);
+        }
+    }
+    if (!p.state_out) return;
+#pragma unroll
+    for (int m = 0; m < NB; ++m)
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            if (b0 + m < p.B) win[m][k].store(p.state_out + (static_cast<int64_t>(b0 + m) * (W - 1) + k) * p.C + c);
+}
+
 gdn_status check(const gdn_conv_problem *p) {
     if (!p) return GDN_ERR_INVALID_ARG;
     if (p->B <= 0 || p->C <= 0 || p->T < 0 || p->x_stride_b < 0 || p->x_stride_t < 0)
@@ -201,22 +273,36 @@ gdn_status check(const gdn_conv_problem *p) {
 
 template <typename E, int W, int V>
 cudaError_t launch(const gdn_conv_problem *pr, ConvParams<E> &p, cudaStream_t s) {
+    const int64_t cv = pr->C / V;
+    if (pr->T <= kStepTokens) {
+        // kStepBatch sequences to a thread where that still leaves each SM its four blocks
+        const unsigned blocks = static_cast<unsigned>((cv + kThreads - 1) / kThreads);
+        const unsigned batches = (pr->B + kStepBatch - 1) / kStepBatch;
+        const bool silu = pr->act == GDN_ACT_SILU;
+        if (static_cast<int64_t>(blocks) * batches >= 2 * 152) {
+            if (silu)
+                gdn_conv_step_kernel<E, W, V, kStepBatch, true><<<dim3(blocks, batches), kThreads, 0, s>>>(p);
+            else
+                gdn_conv_step_kernel<E, W, V, kStepBatch, false><<<dim3(blocks, batches), kThreads, 0, s>>>(p);
+        } else if (silu) {
+            gdn_conv_step_kernel<E, W, V, 1, true><<<dim3(blocks, pr->B), kThreads, 0, s>>>(p);
+        } else {
+            gdn_conv_step_kernel<E, W, V, 1, false><<<dim3(blocks, pr->B), kThreads, 0, s>>>(p);
+        }
+        return cudaGetLastError();
+    }
     // Runs of kMaxRun tokens re-read (W - 1) / kMaxRun of x; shorter ones where those would
-    // leave SMs without their four blocks, a single one for a few tokens.
-    const int64_t cv = pr->C / V, T = pr->T > 0 ? pr->T : 1;
+    // leave SMs without their four blocks.
+    const int64_t T = pr->T;
     p.run = kMaxRun;
     while (p.run > 2 * kUnroll && (T + p.run - 1) / p.run * cv * pr->B < 152LL * 4 * kThreads) p.run /= 2;
-    if (T <= kStepTokens) p.run = static_cast<int>(T);
     const int64_t threads = (T + p.run - 1) / p.run * cv;
     const dim3 grid(static_cast<unsigned>((threads + kThreads - 1) / kThreads), pr->B);
-    constexpr int U = kUnroll;
-    constexpr size_t ring = V > 1 ? kStages * U * kThreads * 16 : 0;
-    if (T <= kStepTokens)
-        gdn_conv_kernel<E, W, V, 1, false><<<grid, kThreads, 0, s>>>(p);
-    else if (p.act == GDN_ACT_SILU)
-        gdn_conv_kernel<E, W, V, U, true><<<grid, kThreads, ring, s>>>(p);
+    constexpr size_t ring = V > 1 ? kStages * kUnroll * kThreads * 16 : 0;
+    if (pr->act == GDN_ACT_SILU)
+        gdn_conv_kernel<E, W, V, true><<<grid, kThreads, ring, s>>>(p);
     else
-        gdn_conv_kernel<E, W, V, U, false><<<grid, kThreads, ring, s>>>(p);
+        gdn_conv_kernel<E, W, V, false><<<grid, kThreads, ring, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -241,6 +327,7 @@ cudaError_t dispatch(const gdn_conv_problem *pr, const void *x, const float *w, 
     p.state_out = static_cast<E *>(state_out);
     p.sb = pr->x_stride_b;
     p.st = pr->x_stride_t;
+    p.B = pr->B;
     p.T = pr->T;
     p.C = pr->C;
     p.act = pr->act;
