@@ -214,29 +214,38 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// (count, mean, squares) of each CTA's groups, all CTAs': mean and 1 / deviation.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// From each CTA's (count, mean, squares) of the groups: their mean and 1 / deviation over all
+// K CTAs, a lane to a CTA. Ends with an arrival at the cluster's barrier: a CTA waits
+// there before it leaves, since others may still read its part.
 __device__ __forceinline__ void merge_cluster(float (&part)[3][kThreads], int groups, int K, float eps,
                                               float *mean, float *rstd) {
     __syncthreads();
     if (K > 1) cluster_sync();
-    for (int g = threadIdx.x; g < groups; g += kThreads) {
-        float na = 0.f, m = 0.f, s = 0.f;
-        for (int r = 0; r < K; ++r) {
+    const int lane = threadIdx.x % 32;
+    for (int g = threadIdx.x / 32; g < groups; g += kThreads / 32) {
+        float n = 0.f, m = 0.f, s = 0.f;
+        if (lane < K) {
             auto of_rank = [&](float *f) {
-                return K > 1 ? ld_cluster_f32(mapa_shared(smem_u32(f), r)) : *f;
+                return K > 1 ? ld_cluster_f32(mapa_shared(smem_u32(f), lane)) : *f;
             };
-            const float nb = of_rank(&part[0][g]);
-            if (nb == 0.f) continue;
-            const float d = of_rank(&part[1][g]) - m, f = nb / (na + nb);
-            s += fmaf(d * d, na * f, of_rank(&part[2][g]));
-            m = fmaf(d, f, m);
-            na += nb;
+            n = of_rank(&part[0][g]);
+            m = of_rank(&part[1][g]);
+            s = of_rank(&part[2][g]);
         }
-        mean[g] = m;
-        rstd[g] = rsqrtf(s / na + eps);
+        const float total = warp_sum(n), all = warp_sum(n * m) / total, d = m - all;
+        s = warp_sum(fmaf(n * d, d, s));
+        if (lane == 0) {
+            mean[g] = all;
+            rstd[g] = rsqrtf(s / total + eps);
+        }
     }
     __syncthreads();
-    if (K > 1) cluster_sync();           // no CTA leaves while another may read its part
+    if (K > 1) cluster_arrive();
 }
 
 template <typename E, int V>
@@ -349,92 +358,98 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
     // Merge the token rows, then the channels, to groups: the weighted means first, then the
     // squares about the group's mean. Threads take a channel's rows (several threads to
     // a channel where they suffice), warps the groups.
-    const int tokens = t_end - t_begin, full = tokens / RP, more = tokens % RP;
-    const float total = static_cast<float>(tokens) * cg;
+    const int tokens = t_end - t_begin, more = tokens % RP;
+    const float total = static_cast<float>(tokens) * cg, low = static_cast<float>(tokens / RP), high = low + 1.f;
     const int CT = min(SC, kThreads), RL = kThreads / CT, rl = threadIdx.x / CT;
-    auto over_rows = [&](auto term) {
-        for (int col = threadIdx.x % CT; rl < RL && col < SC; col += CT) {
-            float sum = 0.f;
-            for (int r = rl; r < RP; r += RL)
-                sum += term(static_cast<float>(full + (r < more)), r * SC + col, col);
-            columns[rl * SC + col] = sum;
-        }
-        __syncthreads();
-    };
     auto over_channels = [&](auto keep) {
+        __syncthreads();
         for (int g = threadIdx.x / 32; g < ng; g += kThreads / 32) {
             float sum = 0.f;
             for (int r = 0; r < RL; ++r)
+#pragma unroll 4
                 for (int i = threadIdx.x % 32; i < cg; i += 32) sum += columns[r * SC + g * cg + i];
             sum = warp_sum(sum);
             if (threadIdx.x % 32 == 0) keep(g, sum);
         }
         __syncthreads();
     };
-    over_rows([&](float count, int at, int) { return count * means[at]; });
+    for (int col = threadIdx.x % CT; rl < RL && col < SC; col += CT) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int r = rl; r < RP; r += RL) sum = fmaf(r < more ? high : low, means[r * SC + col], sum);
+        columns[rl * SC + col] = sum;
+    }
     over_channels([&](int g, float sum) {
         part[0][g] = total;
         part[1][g] = total > 0.f ? sum / total : 0.f;
     });
-    over_rows([&](float count, int at, int col) {
-        const float d = means[at] - part[1][col / cg];
-        return fmaf(count * d, d, squares[at]);
-    });
+    for (int col = threadIdx.x % CT; rl < RL && col < SC; col += CT) {
+        const float m = part[1][col / cg];
+        float sum = 0.f;
+#pragma unroll 8
+        for (int r = rl; r < RP; r += RL) {
+            const float d = means[r * SC + col] - m;
+            sum += fmaf((r < more ? high : low) * d, d, squares[r * SC + col]);
+        }
+        columns[rl * SC + col] = sum;
+    }
     over_channels([&](int g, float sum) { part[2][g] = sum; });
     merge_cluster(part, ng, K, p.eps, g_mean, g_rstd);
-    if (!mine) return;
-    F2 w[N], bias[N], mean[N];
-    params<V>(p.w, c, 1.f, w);
-    params<V>(p.bias, c, 0.f, bias);
+    if (mine) {
+        F2 w[N], bias[N], mean[N];
+        params<V>(p.w, c, 1.f, w);
+        params<V>(p.bias, c, 0.f, bias);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int ga = (q + 2 * k) / cg, gb = V == 1 ? ga : (q + 2 * k + 1) / cg;
-        mean[k] = pack2(-g_mean[ga], -g_mean[gb]);
-        w[k] = mul2(w[k], pack2(g_rstd[ga], g_rstd[gb]));
+        for (int k = 0; k < N; ++k) {
+            const int ga = (q + 2 * k) / cg, gb = V == 1 ? ga : (q + 2 * k + 1) / cg;
+            mean[k] = pack2(-g_mean[ga], -g_mean[gb]);
+            w[k] = mul2(w[k], pack2(g_rstd[ga], g_rstd[gb]));
+        }
+        constexpr int U = 4;
+        const int64_t g_step = RP * p.g_st, y_step = static_cast<int64_t>(RP) * p.C;
+        const E *from = x + (t_begin + row) * p.x_st;
+        const E *gate = p.gate ? p.gate + b * p.g_sb + c + (t_begin + row) * p.g_st : nullptr;
+        E *to = p.y + (b * p.T + t_begin + row) * p.C + c;
+        Piece<E, V> r[U], z[U];
+        auto fetch = [&](int tokens) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u >= tokens) break;
+                r[u].load_rw(from + u * step);
+                if (gate) z[u].load(gate + u * g_step);
+            }
+            from += U * step;
+            if (gate) gate += U * g_step;
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) z[u].zero();
+        int left = (t_end - t_begin - row + RP - 1) / RP;
+        const bool gated = gate != nullptr;
+        fetch(left);
+        for (; left > 0; left -= U) {
+            Piece<E, V> nr[U], nz[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                nr[u] = r[u];
+                nz[u] = z[u];
+            }
+            fetch(left - U);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u >= left) break;
+                F2 v[N], gv[N];
+                nr[u].widen(v);
+                nz[u].widen(gv);
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] = fma2(add2(v[k], mean[k]), w[k], bias[k]);
+                outputs(v, gv, gated, p.act);
+                nr[u].round(v);
+                nr[u].store(to + u * y_step);
+            }
+            to += U * y_step;
+        }
     }
-    constexpr int U = 4;
-    const int64_t g_step = RP * p.g_st, y_step = static_cast<int64_t>(RP) * p.C;
-    const E *from = x + (t_begin + row) * p.x_st;
-    const E *gate = p.gate ? p.gate + b * p.g_sb + c + (t_begin + row) * p.g_st : nullptr;
-    E *to = p.y + (b * p.T + t_begin + row) * p.C + c;
-    Piece<E, V> r[U], z[U];
-    auto fetch = [&](int tokens) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (u >= tokens) break;
-            r[u].load_rw(from + u * step);
-            if (gate) z[u].load(gate + u * g_step);
-        }
-        from += U * step;
-        if (gate) gate += U * g_step;
-    };
-#pragma unroll
-    for (int u = 0; u < U; ++u) z[u].zero();
-    int left = (t_end - t_begin - row + RP - 1) / RP;
-    const bool gated = gate != nullptr;
-    fetch(left);
-    for (; left > 0; left -= U) {
-        Piece<E, V> nr[U], nz[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            nr[u] = r[u];
-            nz[u] = z[u];
-        }
-        fetch(left - U);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (u >= left) break;
-            F2 v[N], gv[N];
-            nr[u].widen(v);
-            nz[u].widen(gv);
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = fma2(add2(v[k], mean[k]), w[k], bias[k]);
-            outputs(v, gv, gated, p.act);
-            nr[u].round(v);
-            nr[u].store(to + u * y_step);
-        }
-        to += U * y_step;
-    }
+    if (K > 1) cluster_wait();
 }
 
 // The same for a group of more pieces than a block has threads: a cluster to a group, each
@@ -515,6 +530,7 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
             r.store(y + t * p.C + q);
         }
     }
+    if (K > 1) cluster_wait();
 }
 
 gdn_status check(const gdn_group_norm_problem *p) {
