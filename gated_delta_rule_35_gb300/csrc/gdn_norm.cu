@@ -6,7 +6,8 @@
 //   gdn_norm_rows_kernel   T = 1: a group is cg consecutive values, held in the registers of a
 //                          part of a warp between the statistics and the output;
 //   gdn_norm_tokens_kernel any T: a cluster of CTAs shares a sequence's tokens for a slice of
-//                          whole groups; its second reading comes from L2.
+//                          whole groups; what shared memory does not keep is read from
+//                          L2 the second time.
 #include "mixer.cuh"
 #include "sm100_ptx.cuh"
 
@@ -192,14 +193,18 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p
 //
 // The CTAs of a cluster take equal shares of a sequence's valid tokens, for one slice of
 // `groups` groups. A thread keeps one piece of V channels and takes every RP-th
-// token. It sums x - k and (x - k)^2, k the channel's mean over its first 8 tokens, over up
-// to 16 blocks of 8 tokens, and merges these sets by the exact update for two,
+// token. It sums x - k and (x - k)^2, k the channel's mean over its first 4 tokens, over up
+// to 32 blocks of 4, and merges these sets by the exact update for two,
 //   mean += d nb / n,   M2 += M2b + d^2 na nb / n   with d = mean_b - mean.
-// The mean of a set lies at most sqrt(16) of its deviations from k, so at most 17 times the
+// The mean of a set lies at most sqrt(32) of its deviations from k, so at most 33 times the
 // variance's rounding is lost, however far the mean is from zero. Channels and threads then
 // merge to groups, and the CTAs' groups through distributed shared memory, in rank order.
-constexpr int kBlockTokens = 8;
-constexpr int kSetBlocks = 16;
+constexpr int kBlockTokens = 4;
+constexpr int kSetBlocks = 32;
+// Of a thread's blocks the first kKept stay in shared memory between the statistics and the
+// output; the others pass through kRing places there, twice.
+constexpr int kKept = 3;
+constexpr int kRing = 2;
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -266,61 +271,78 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
     const E *x = p.x + b * p.x_sb + c;
 
     constexpr int N = (V + 1) / 2;
+    constexpr int BT = kBlockTokens;
+    using Raw = typename Piece<E, V>::Raw;
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    Raw *const slots = reinterpret_cast<Raw *>(dynamic) + threadIdx.x;     // this thread's alone
     const int64_t step = RP * p.x_st;
+    const E *const first = x + (t_begin + row) * p.x_st;
+    const int own = mine ? max(0, (t_end - t_begin - row + RP - 1) / RP) : 0;    // tokens of this thread
+    const int blocks = (own + BT - 1) / BT;
+    auto place = [](int block) { return (block < kKept ? block : kKept + (block - kKept) % kRing) * BT; };
+    // A block's pieces on their way to its place; one group of copies whether or not it exists.
+    auto fetch = [&](int block) {
+        if (block < blocks) {
+            Raw *to = slots + place(block) * kThreads;
+            const E *from = first + static_cast<int64_t>(block) * BT * step;
+#pragma unroll
+            for (int u = 0; u < BT; ++u) {
+                if (block * BT + u < own) {
+                    if constexpr (sizeof(Raw) == 16)
+                        copy16_async(to + u * kThreads, from + u * step);
+                    else if constexpr (sizeof(Raw) == 4)
+                        copy4_async(to + u * kThreads, from + u * step);
+                    else
+                        to[u * kThreads] = from[u * step];
+                }
+            }
+        }
+        copy_commit();
+    };
+    auto block_piece = [&](int block, int u) {
+        Piece<E, V> q;
+        q.raw = slots[(place(block) + u) * kThreads];
+        return q;
+    };
+    for (int i = 0; i < kKept + kRing; ++i) fetch(i);
     if (mine) {
         F2 mean[N], m2[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) mean[k] = m2[k] = 0;
         float count = 0.f;
-        const E *from = x + (t_begin + row) * p.x_st;
-        int left = (t_end - t_begin - row + RP - 1) / RP;      // tokens of this thread
-        while (left > 0) {
-            const int set = min(left, kSetBlocks * kBlockTokens);
-            left -= set;
+        for (int set = 0; set < blocks; set += kSetBlocks) {
             F2 shift[N], s1[N], s2[N];
 #pragma unroll
             for (int k = 0; k < N; ++k) s1[k] = s2[k] = 0;
-            // the next block's loads are in flight while one is summed
-            Piece<E, V> next[kBlockTokens];
-            auto fetch = [&](int tokens) {
+            const int end = min(blocks, set + kSetBlocks);
+            for (int i = set; i < end; ++i) {
+                if (i < kKept + kRing)
+                    copy_wait<kKept + kRing - 1>();
+                else
+                    copy_wait<kRing - 1>();
+                const int here = min(BT, own - i * BT);
+                F2 v[BT][N], b1[N], b2[N];
 #pragma unroll
-                for (int u = 0; u < kBlockTokens; ++u)
-                    if (u < tokens) next[u].load_rw(from + u * step);
-                from += min(max(tokens, 0), kBlockTokens) * step;
-            };
-            fetch(set);
-            for (int done = 0; done < set; done += kBlockTokens) {
-                Piece<E, V> now[kBlockTokens];
-                const int here = min(set - done, kBlockTokens);
+                for (int u = 0; u < BT; ++u) {
+                    Piece<E, V> q = block_piece(i, u);
+                    if (u >= here) q.zero();
+                    q.widen(v[u]);
+                }
+                if (i >= kKept) fetch(i + kRing); else copy_commit();
 #pragma unroll
-                for (int u = 0; u < kBlockTokens; ++u) now[u] = next[u];
-                fetch(set - done - kBlockTokens);
-                F2 v[N], b1[N], b2[N];
-#pragma unroll
-                for (int k = 0; k < N; ++k) b1[k] = b2[k] = 0;
-                if (done == 0) {
-#pragma unroll
-                    for (int u = 0; u < kBlockTokens; ++u) {
-                        if (u >= here) break;
-                        now[u].widen(v);
-#pragma unroll
-                        for (int k = 0; k < N; ++k) b1[k] = add2(b1[k], v[k]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        shift[k] = mul2(b1[k], both(-1.f / here));
-                        b1[k] = 0;
-                    }
+                for (int k = 0; k < N; ++k) {
+                    if (i == set)
+                        shift[k] = mul2(add2(add2(v[0][k], v[1][k]), add2(v[2][k], v[3][k])), both(-1.f / here));
+                    b1[k] = b2[k] = 0;
                 }
 #pragma unroll
-                for (int u = 0; u < kBlockTokens; ++u) {
+                for (int u = 0; u < BT; ++u) {
                     if (u >= here) break;
-                    now[u].widen(v);
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
-                        v[k] = add2(v[k], shift[k]);
-                        b1[k] = add2(b1[k], v[k]);
-                        b2[k] = fma2(v[k], v[k], b2[k]);
+                        const F2 d = add2(v[u][k], shift[k]);
+                        b1[k] = add2(b1[k], d);
+                        b2[k] = fma2(d, d, b2[k]);
                     }
                 }
 #pragma unroll
@@ -329,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
                     s2[k] = add2(s2[k], b2[k]);
                 }
             }
-            const float nb = static_cast<float>(set), na = count;
+            const float nb = static_cast<float>(min(own - set * BT, kSetBlocks * BT)), na = count;
             count += nb;
             const float f = nb / count;
 #pragma unroll
@@ -342,6 +364,9 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
                 m2[k] = add2(m2[k], fma2(mul2(d, d), both(na * f), set2));
             }
         }
+        // the second reading begins during the merges
+        copy_wait<0>();
+        for (int i = kKept; i < kKept + kRing; ++i) fetch(i);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             float a, b;
@@ -405,49 +430,50 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
             mean[k] = pack2(-g_mean[ga], -g_mean[gb]);
             w[k] = mul2(w[k], pack2(g_rstd[ga], g_rstd[gb]));
         }
-        constexpr int U = 4;
         const int64_t g_step = RP * p.g_st, y_step = static_cast<int64_t>(RP) * p.C;
-        const E *from = x + (t_begin + row) * p.x_st;
         const E *gate = p.gate ? p.gate + b * p.g_sb + c + (t_begin + row) * p.g_st : nullptr;
-        E *to = p.y + (b * p.T + t_begin + row) * p.C + c;
-        Piece<E, V> r[U], z[U];
-        auto fetch = [&](int tokens) {
+        E *y = p.y + (b * p.T + t_begin + row) * p.C + c;
+        // kept blocks between those that still arrive
+        const int kept = min(blocks, kKept), other = blocks - kept, mixed = 2 * min(kept, other);
+        auto order = [&](int i) {
+            if (i < mixed) return i & 1 ? i / 2 : kKept + i / 2;
+            return other > kept ? kKept + i - kept : i - other;
+        };
+        Piece<E, V> z[BT];
+        auto fetch_gate = [&](int block) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u >= tokens) break;
-                r[u].load_rw(from + u * step);
-                if (gate) z[u].load(gate + u * g_step);
-            }
-            from += U * step;
-            if (gate) gate += U * g_step;
+            for (int u = 0; u < BT; ++u)
+                if (block * BT + u < own) z[u].load(gate + (static_cast<int64_t>(block) * BT + u) * g_step);
         };
 #pragma unroll
-        for (int u = 0; u < U; ++u) z[u].zero();
-        int left = (t_end - t_begin - row + RP - 1) / RP;
-        const bool gated = gate != nullptr;
-        fetch(left);
-        for (; left > 0; left -= U) {
-            Piece<E, V> nr[U], nz[U];
+        for (int u = 0; u < BT; ++u) z[u].zero();
+        if (gate && blocks > 0) fetch_gate(order(0));
+        for (int i = 0; i < blocks; ++i) {
+            const int block = order(i);
+            if (block >= kKept) copy_wait<kRing - 1>();
+            Piece<E, V> r[BT], zn[BT];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                nr[u] = r[u];
-                nz[u] = z[u];
+            for (int u = 0; u < BT; ++u) {
+                r[u] = block_piece(block, u);
+                zn[u] = z[u];
             }
-            fetch(left - U);
+            if (block >= kKept) fetch(block + kRing);
+            if (gate && i + 1 < blocks) fetch_gate(order(i + 1));
+            E *to = y + static_cast<int64_t>(block) * BT * y_step;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u >= left) break;
+            for (int u = 0; u < BT; ++u) {
+                if (block * BT + u >= own) break;
                 F2 v[N], gv[N];
-                nr[u].widen(v);
-                nz[u].widen(gv);
+                r[u].widen(v);
+                zn[u].widen(gv);
 #pragma unroll
                 for (int k = 0; k < N; ++k) v[k] = fma2(add2(v[k], mean[k]), w[k], bias[k]);
-                outputs(v, gv, gated, p.act);
-                nr[u].round(v);
-                nr[u].store(to + u * y_step);
+                outputs(v, gv, gate != nullptr, p.act);
+                r[u].round(v);
+                r[u].store(to + u * y_step);
             }
-            to += U * y_step;
         }
+        copy_wait<0>();
     }
     if (K > 1) cluster_wait();
 }
@@ -560,12 +586,16 @@ cudaError_t launch_rows(NormParams<E> &p, cudaStream_t s) {
 }
 
 template <typename E>
-cudaError_t launch_cluster(void (*kernel)(NormParams<E>), int K, int slices, NormParams<E> &p,
-                           cudaStream_t s) {
+cudaError_t launch_cluster(void (*kernel)(NormParams<E>), int K, int slices, int bytes,
+                           NormParams<E> &p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(K) * p.B, slices);
     p.cluster = K;
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -586,7 +616,7 @@ cudaError_t launch_tokens(NormParams<E> &p, cudaStream_t s) {
         if (cg % V != 0) return launch_tokens<E, 1>(p, s);
         int K = 1;
         while (K < kMaxCluster && static_cast<int64_t>(p.B) * p.G * K < 4 * 152 && p.T > 2 * K) K *= 2;
-        return launch_cluster(gdn_norm_wide_kernel<E, V>, K, p.G, p, s);
+        return launch_cluster(gdn_norm_wide_kernel<E, V>, K, p.G, 0, p, s);
     }
     // Slice and cluster by the turns that a thread takes: its tokens, and about 8 for the
     // merges, for every wave of blocks (2 or 4 to an SM by registers), and the sectors that
@@ -611,7 +641,8 @@ cudaError_t launch_tokens(NormParams<E> &p, cudaStream_t s) {
         }
     }
     p.groups = groups;
-    return launch_cluster(gdn_norm_tokens_kernel<E, V>, K, slices(groups), p, s);
+    constexpr int bytes = (kKept + kRing) * kBlockTokens * kThreads * sizeof(typename Piece<E, V>::Raw);
+    return launch_cluster(gdn_norm_tokens_kernel<E, V>, K, slices(groups), bytes, p, s);
 }
 
 template <typename E, int V>
