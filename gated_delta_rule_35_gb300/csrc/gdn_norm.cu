@@ -574,7 +574,8 @@ gdn_status check(const gdn_group_norm_problem *p) {
 
 template <typename E, int V, int P>
 cudaError_t launch_rows(NormParams<E> &p, cudaStream_t s) {
-    constexpr int R = P == 1 ? 4 : P == 2 ? 2 : 1;
+    // two rows at a time: 254 us for 65536 gated rows of 4096 (6.3 TB/s); one 304, four 293
+    constexpr int R = P <= 2 ? 2 : 1;
     const int64_t slots = static_cast<int64_t>(p.G) * p.lanes;
     // rows in flight: 8 blocks to an SM, or all rows
     const int64_t most = 152LL * 8 * kThreads / slots;

@@ -171,6 +171,38 @@ def _refusal(p) -> int:
     return lib().gdn_scan_fwd(ctypes.byref(p), *[None] * 13, 0, None)
 
 
+def _form(t):
+    """What a call checks of a tensor: two tensors of one form pass or fail alike."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+# The checked problem of each form of call (as the host entry keeps its plans): its many
+# tensors cost 6 us to check again for a single token.
+_scan_plans: dict = {}
+
+
+def _scan_plan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, lengths, out, final_state):
+    """(problem, workspace bytes, shape of the state, device index), or the refusal."""
+    shape, dtype, index = _x(x, "[B,T,D]")
+    nb, T, nd = shape
+    if B.dim() != 4:
+        raise ValueError("B and C must be [B,T,G,N]")
+    G, N = B.shape[2:]
+    rows, state, f32 = (nb, T, G, N), (nb, nd, N), torch.float32
+    p = ScanProblem(nb, T, nd, N, G, DTYPES[dtype], GDN_SCAN_SOFTPLUS if dt_softplus else 0, 0,
+                    *_tokens(x, "x", shape, dtype, index), *_tokens(dt, "dt", shape, dtype, index),
+                    *((0, 0) if z is None else _tokens(z, "z", shape, dtype, index)),
+                    *_tokens(B, "B", rows, dtype, index), *_tokens(C, "C", rows, dtype, index))
+    for t, name, form, kind in ((A, "A", (nd, N), f32), (D, "D", (nd,), f32), (dt_bias, "dt_bias", (nd,), f32),
+                                (h0, "h0", state, f32), (lengths, "lengths", (nb,), torch.int32),
+                                (out, "out", shape, dtype), (final_state, "final_state", state, f32)):
+        _dense(t, name, form, kind, index)
+    need = lib().gdn_scan_workspace_bytes(ctypes.byref(p))
+    if need == _INVALID:
+        raise GdnError(_refusal(p), "gdn_scan_fwd")
+    return ctypes.byref(p), need, state, index
+
+
 @_on_stream
 def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = False, h0=None,
              lengths=None, output_final_state: bool = True, workspace=None, out=None,
@@ -186,37 +218,28 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = F
     [B,D,N] float32; N in 1..128. ``final_state=h0`` updates the state in place.
     ``workspace`` (scan_workspace_bytes) and ``out`` may be passed to reuse
     buffers."""
-    shape, dtype, index = _x(x, "[B,T,D]")
-    nb, T, nd = shape
-    if B.dim() != 4:
-        raise ValueError("B and C must be [B,T,G,N]")
-    G, N = B.shape[2:]
-    rows = (nb, T, G, N)
-    p = ScanProblem(nb, T, nd, N, G, DTYPES[dtype], GDN_SCAN_SOFTPLUS if dt_softplus else 0, 0,
-                    *_tokens(x, "x", shape, dtype, index), *_tokens(dt, "dt", shape, dtype, index),
-                    *((0, 0) if z is None else _tokens(z, "z", shape, dtype, index)),
-                    *_tokens(B, "B", rows, dtype, index), *_tokens(C, "C", rows, dtype, index))
-    pp = ctypes.byref(p)
-    f32 = torch.float32
-    state = (nb, nd, N)
-    a = _dense(A, "A", (nd, N), f32, index)
-    skip, bias = _dense(D, "D", (nd,), f32, index), _dense(dt_bias, "dt_bias", (nd,), f32, index)
-    hi = _dense(h0, "h0", state, f32, index)
-    n = _dense(lengths, "lengths", (nb,), torch.int32, index)
-    need = lib().gdn_scan_workspace_bytes(pp)
-    if need == _INVALID:
-        raise GdnError(_refusal(p), "gdn_scan_fwd")
+    key = (x.shape, x.stride(), x.dtype, x.get_device(), dt.shape, dt.stride(), dt.dtype, dt.get_device(),
+           A.shape, A.stride(), A.dtype, A.get_device(), B.shape, B.stride(), B.dtype, B.get_device(),
+           C.shape, C.stride(), C.dtype, C.get_device(), _form(D), _form(z), _form(dt_bias), _form(h0),
+           _form(lengths), _form(out), _form(final_state), dt_softplus)
+    plan = _scan_plans.get(key)
+    if plan is None:
+        if len(_scan_plans) >= 256:
+            _scan_plans.clear()
+        plan = _scan_plans[key] = _scan_plan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, lengths, out,
+                                             final_state)
+    p, need, state, index = plan
     if need:    # held until the call: freed before, out could be allocated in its place
         workspace = _workspace(workspace, need, x.device)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if not output_final_state:
         final_state = None
     elif final_state is None:
-        final_state = torch.empty(state, dtype=f32, device=x.device)
-    _call(lib().gdn_scan_fwd, "gdn_scan_fwd", index, pp, x.data_ptr(), dt.data_ptr(), a, B.data_ptr(),
-          C.data_ptr(), skip, _ptr(z), bias, hi, n, _dense(out, "out", shape, dtype, index),
-          _dense(final_state, "final_state", state, f32, index), _ptr(workspace) if need else None, need)
+        final_state = torch.empty(state, dtype=torch.float32, device=x.device)
+    _call(lib().gdn_scan_fwd, "gdn_scan_fwd", index, p, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+          B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lengths),
+          out.data_ptr(), _ptr(final_state), _ptr(workspace) if need else None, need)
     return out, final_state
 
 
