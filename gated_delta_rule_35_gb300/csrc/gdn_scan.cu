@@ -75,7 +75,7 @@ __device__ __forceinline__ float4 widen4(const __nv_bfloat16 *p, int left) {
 constexpr int kBatch = 4;
 
 template <typename E, int NP, int NB>
-__global__ void __launch_bounds__(kThreads) gdn_scan_step_kernel(const ScanParams<E> p) {
+__global__ void __launch_bounds__(kThreads, NB > 1 ? 12 : 1) gdn_scan_step_kernel(const ScanParams<E> p) {
     constexpr int L = NP / 4, channels = kThreads / L, OWN = (NB + L - 1) / L;
     __shared__ __align__(16) float bc[NB][2][NP];      // a token's B and C rows
     const int per = p.D / p.G, blocks = (per + channels - 1) / channels;
