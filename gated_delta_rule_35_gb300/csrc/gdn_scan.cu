@@ -183,47 +183,49 @@ __global__ void __launch_bounds__(kThreads, NB > 1 ? 12 : 1) gdn_scan_step_kerne
 
 // ---------------------------------------------------------------------- prompts
 //
-// A block takes 128 / L channels of one group of one sequence, L lanes to a channel with
-// NP / L states each, and walks the tokens in tiles of 32:
+// A block takes 64 channels of one group of one sequence, two lanes to a channel with half of
+// its states each (four, then the other lane's four), and walks the tokens in tiles of 32:
 //   copy    the next tile's rows on their way to shared memory;
 //   widen   Delta and Delta x of every token and channel, B and C as fp32;
 //   scan    per token and state: ex2(Delta A), h = a h + (Delta x) B, y += C h, on pairs
-//           of states; after four tokens the lanes of a channel add their shares of
-//           y so that the sums end spread over them;
+//           of states; after four tokens the two lanes exchange their shares of y,
+//           each keeping two tokens' sums;
 //   finish  D x, the gate, and rows of y in 16-byte pieces.
-// The decay's exponentials dominate; Delta's and the gate's are taken once per token and
-// channel, not in every lane. Few lanes to a channel keep the exchange of y small, eight
-// or more states to a lane keep the arithmetic pipes fed from few warps.
+// The decay's exponentials and the state's multiply-adds dominate; Delta's and the gate's
+// special functions are taken once per token and channel, not in both lanes.
+//
+// Two lanes, because shared memory hands a warp B and C 16 bytes a lane in 2 cycles for
+// two addresses but in 4 for more: with four lanes to a channel N = 64 took 1237 us for B4
+// T2048 D4096 (654 with two), with eight N = 128 4720 us (1489).
 constexpr int kTile = 32;
+constexpr int kChannels = kThreads / 2;
 
 template <typename E, int NP>
 struct Tile {
-    static constexpr int L = NP <= 32 ? 2 : NP / 16;         // lanes to a channel
-    static constexpr int channels = kThreads / L;
-    static constexpr int row = channels * sizeof(E) + 16;    // bytes; 16 more: no bank conflicts
+    static constexpr int row = kChannels * sizeof(E) + 16;   // bytes; 16 more: no bank conflicts
     static constexpr int du_row = 2 * kTile + 4;             // floats of a channel's (Delta, Delta x)
-    static constexpr int y_row = channels + 32 / L;
+    static constexpr int y_row = kChannels + 16;
     static constexpr int bc = kTile * NP * sizeof(E);
     static constexpr int raw = 3 * kTile * row + 2 * bc;     // x, dt, z, B, C
-    static constexpr int du = channels * du_row * 4;
+    static constexpr int du = kChannels * du_row * 4;
     static constexpr int wide = kTile * NP * 4;
     static constexpr int bytes = 2 * raw + du + 2 * wide + kTile * y_row * 4;
 };
 
 // PARTIAL: only the state at the end of a segment that starts from zero.
 template <typename E, int NP, bool VEC, bool PARTIAL>
-__global__ void __launch_bounds__(kThreads, 3) gdn_scan_kernel(const ScanParams<E> p) {
+__global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn_scan_kernel(const ScanParams<E> p) {
     using S = Tile<E, NP>;
-    constexpr int L = S::L, SP = NP / L, SP2 = SP / 2, TT = kTile;
+    constexpr int SP2 = NP / 4, TT = kTile;          // pairs of states of a lane
     constexpr int V = VEC ? 16 / sizeof(E) : 1;      // channels per piece
-    constexpr int PR = S::channels / V;              // pieces per row
+    constexpr int PR = kChannels / V;              // pieces per row
     extern __shared__ __align__(16) unsigned char smem[];
     float *du = reinterpret_cast<float *>(smem + 2 * S::raw);
     float *bw = du + S::du / 4, *cw = bw + TT * NP, *yb = cw + TT * NP;
 
-    const int per = p.D / p.G, blocks = (per + S::channels - 1) / S::channels;
-    const int g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * S::channels;
-    const int nc = min(S::channels, per - c0);       // channels of this block
+    const int per = p.D / p.G, blocks = (per + kChannels - 1) / kChannels;
+    const int g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * kChannels;
+    const int nc = min(kChannels, per - c0);       // channels of this block
     const int d0 = g * per + c0;
     const int64_t b = blockIdx.y;
     const int s = blockIdx.z;
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 3) gdn_scan_kernel(const ScanParams<
     const int t_begin = s * p.seg, t_end = min(n, t_begin + p.seg);
     if (s > 0 && t_begin >= n) return;
 
-    const int tid = threadIdx.x, c = tid / L, j = tid % L;
+    const int tid = threadIdx.x, c = tid / 2, j = tid % 2;
     const bool live = c < nc;
     const int d = d0 + (live ? c : 0);
     const int64_t state = (b * p.D + d) * p.N;
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 3) gdn_scan_kernel(const ScanParams<
     auto load_states = [&](const float *row, F2 (&f)[SP2], float scale) {
 #pragma unroll
         for (int q = 0; q < SP2; ++q) {
-            const int k = j * SP + 2 * q;
+            const int k = (q / 2 * 2 + j) * 4 + q % 2 * 2;
             f[q] = pack2(live && k < p.N ? scale * row[k] : 0.f,
                          live && k + 1 < p.N ? scale * row[k + 1] : 0.f);
         }
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 3) gdn_scan_kernel(const ScanParams<
         if (!live) return;
 #pragma unroll
         for (int q = 0; q < SP2; ++q) {
-            const int k = j * SP + 2 * q;
+            const int k = (q / 2 * 2 + j) * 4 + q % 2 * 2;
             float lo, hi;
             unpack2(h[q], lo, hi);
             if (k < p.N) row[k] = lo;
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 3) gdn_scan_kernel(const ScanParams<
             const int t = tid % TT;
             const bool in = t < rows;
 #pragma unroll
-            for (int q = tid / TT * V; q < S::channels; q += kThreads / TT * V) {
+            for (int q = tid / TT * V; q < kChannels; q += kThreads / TT * V) {
                 if (q >= nc) break;
                 float x[V], dt[V + 1], bias[V];
                 Piece<E, V> pc;
@@ -395,16 +397,16 @@ __global__ void __launch_bounds__(kThreads, 3) gdn_scan_kernel(const ScanParams<
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const F2 dd = pack2(step[m], step[m]), uu = pack2(in[m], in[m]);
-                const ulonglong2 *br = reinterpret_cast<const ulonglong2 *>(bw + (t + m) * NP + j * SP);
-                const ulonglong2 *cr = reinterpret_cast<const ulonglong2 *>(cw + (t + m) * NP + j * SP);
+                const ulonglong2 *br = reinterpret_cast<const ulonglong2 *>(bw + (t + m) * NP) + j;
+                const ulonglong2 *cr = reinterpret_cast<const ulonglong2 *>(cw + (t + m) * NP) + j;
                 F2 acc = 0;
 #pragma unroll
                 for (int q = 0; q < SP2; q += 2) {
-                    const ulonglong2 bq = br[q / 2];
+                    const ulonglong2 bq = br[q];
                     h[q] = fma2(decay(dd, A2[q]), h[q], mul2(uu, bq.x));
                     h[q + 1] = fma2(decay(dd, A2[q + 1]), h[q + 1], mul2(uu, bq.y));
                     if (!PARTIAL) {
-                        const ulonglong2 cq = cr[q / 2];
+                        const ulonglong2 cq = cr[q];
                         acc = q == 0 ? mul2(cq.x, h[q]) : fma2(cq.x, h[q], acc);
                         acc = fma2(cq.y, h[q + 1], acc);
                     }
@@ -417,22 +419,12 @@ __global__ void __launch_bounds__(kThreads, 3) gdn_scan_kernel(const ScanParams<
                 dt_sum += (step[0] + step[1]) + (step[2] + step[3]);
                 continue;
             }
-            const bool odd = j & 1;
+            // lane j keeps tokens j and 2 + j
             float *y = yb + t * S::y_row + c;
-            if constexpr (L == 2) {     // lane j: tokens j and 2 + j
-                const float r0 = __shfl_xor_sync(0xffffffffu, odd ? yt[0] : yt[1], 1);
-                const float r1 = __shfl_xor_sync(0xffffffffu, odd ? yt[2] : yt[3], 1);
-                y[j * S::y_row] = (odd ? yt[1] : yt[0]) + r0;
-                y[(2 + j) * S::y_row] = (odd ? yt[3] : yt[2]) + r1;
-            } else {                    // lane j: token j of the first four lanes
-                const bool up = j & 2;
-                const float r0 = __shfl_xor_sync(0xffffffffu, up ? yt[0] : yt[2], 2);
-                const float r1 = __shfl_xor_sync(0xffffffffu, up ? yt[1] : yt[3], 2);
-                const float k0 = (up ? yt[2] : yt[0]) + r0, k1 = (up ? yt[3] : yt[1]) + r1;
-                float sum = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 1);
-                if constexpr (L == 8) sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                if (j < 4) y[j * S::y_row] = sum;
-            }
+            const float r0 = __shfl_xor_sync(0xffffffffu, j ? yt[0] : yt[1], 1);
+            const float r1 = __shfl_xor_sync(0xffffffffu, j ? yt[2] : yt[3], 1);
+            y[j * S::y_row] = (j ? yt[1] : yt[0]) + r0;
+            y[(2 + j) * S::y_row] = (j ? yt[3] : yt[2]) + r1;
         }
         if (PARTIAL) continue;
         __syncthreads();
@@ -498,11 +490,9 @@ gdn_status check(const gdn_scan_problem *p) {
 // half of those places are not cut. One sequence of 32768 tokens and 2048 channels (32
 // blocks): 572 us in 14 segments, 655 in 9, 590 in 23; 512 tokens of it 27 us in 8, 49
 // in 2. Four of 2048 tokens and 4096 channels (256 blocks): 230 us whole, 296 in 2.
-int block_channels(int N) { return N <= 32 ? kThreads / 2 : N <= 64 ? kThreads / 4 : kThreads / 8; }
-
 int64_t row_blocks(const gdn_scan_problem *p) {
-    const int per = p->D / p->G, c = block_channels(p->N);
-    return static_cast<int64_t>(p->G) * ((per + c - 1) / c);
+    const int per = p->D / p->G;
+    return static_cast<int64_t>(p->G) * ((per + kChannels - 1) / kChannels);
 }
 
 int segments(const gdn_scan_problem *p) {
@@ -520,7 +510,6 @@ size_t workspace_need(const gdn_scan_problem *p) {
 
 template <typename E, int NP, bool VEC>
 cudaError_t launch_prompt(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace, cudaStream_t s) {
-    static_assert(Tile<E, NP>::channels == kThreads / (NP <= 32 ? 2 : NP / 16), "block_channels");
     const int n = segments(pr);
     p.seg = ((pr->T + n - 1) / n + kTile - 1) / kTile * kTile;
     p.segs = (pr->T + p.seg - 1) / p.seg;
