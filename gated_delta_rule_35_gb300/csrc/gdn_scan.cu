@@ -21,6 +21,7 @@ struct ScanParams {
     int64_t x_sb, x_st, dt_sb, dt_st, z_sb, z_st, b_sb, b_st, c_sb, c_st;
     int B, T, D, N, G, softplus;
     int rows16;          // B and C rows are whole 16-byte pieces
+    int pieces;          // so are those of x, dt, z and y, and each block's part of them
     // Segments of seg tokens each; with more than one, the state at the end of a
     // segment that started from zero (the first one: from h0), h0 itself behind those,
     // and each segment's sum of Delta.
@@ -31,10 +32,11 @@ struct ScanParams {
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), with log1p(e) = 2 atanh(s),
 // s = e / (2 + e) <= 1/3, by the series s (1 + s^2/3 + s^4/5 + ...) through s^13: the rest
 // is below 2e-8 of it, so small Delta keep their relative accuracy. Of two values.
-__device__ __forceinline__ void softplus2(float &a, float &b) {
-    auto two = [](float v) { return pack2(v, v); };
+__device__ __forceinline__ F2 softplus2(F2 v) {
+    auto two = [](float f) { return pack2(f, f); };
+    float a, b, p, q;
+    unpack2(v, a, b);
     const F2 e = pack2(exp2_ftz(-kLog2e * fabsf(a)), exp2_ftz(-kLog2e * fabsf(b)));
-    float p, q;
     unpack2(add2(e, two(2.f)), p, q);
     const F2 s = mul2(e, pack2(rcp_ftz(p), rcp_ftz(q))), s2 = mul2(s, s);
     F2 r = fma2(s2, two(1.f / 13.f), two(1.f / 11.f));
@@ -43,27 +45,25 @@ __device__ __forceinline__ void softplus2(float &a, float &b) {
     r = fma2(s2, r, two(1.f / 5.f));
     r = fma2(s2, r, two(1.f / 3.f));
     r = fma2(s2, r, two(1.f));
-    unpack2(fma2(add2(s, s), r, pack2(fmaxf(a, 0.f), fmaxf(b, 0.f))), a, b);
+    return fma2(add2(s, s), r, pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
 
 __device__ __forceinline__ float softplus(float v) {
-    float unused = v;
-    softplus2(v, unused);
-    return v;
+    float r, unused;
+    unpack2(softplus2(pack2(v, v)), r, unused);
+    return r;
 }
 
-// Four consecutive elements of an aligned shared row, those from `left` on as 0.
-__device__ __forceinline__ float4 widen4(const float *p, int left) {
+// Four consecutive elements of an aligned shared row, or zeros.
+__device__ __forceinline__ float4 widen4(const float *p, bool in) {
     const float4 q = *reinterpret_cast<const float4 *>(p);
-    return make_float4(left > 0 ? q.x : 0.f, left > 1 ? q.y : 0.f, left > 2 ? q.z : 0.f,
-                       left > 3 ? q.w : 0.f);
+    return in ? q : make_float4(0.f, 0.f, 0.f, 0.f);
 }
-__device__ __forceinline__ float4 widen4(const __nv_bfloat16 *p, int left) {
-    const uint2 q = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(left > 0 ? __uint_as_float(q.x << 16) : 0.f,
-                       left > 1 ? __uint_as_float(q.x & 0xffff0000u) : 0.f,
-                       left > 2 ? __uint_as_float(q.y << 16) : 0.f,
-                       left > 3 ? __uint_as_float(q.y & 0xffff0000u) : 0.f);
+__device__ __forceinline__ float4 widen4(const __nv_bfloat16 *p, bool in) {
+    uint2 q = *reinterpret_cast<const uint2 *>(p);
+    if (!in) q = make_uint2(0, 0);
+    return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u),
+                       __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u));
 }
 
 // ----------------------------------------------------------------- a few tokens
@@ -191,17 +191,27 @@ __global__ void __launch_bounds__(kThreads, NB > 1 ? 12 : 1) gdn_scan_step_kerne
 //           of states; after four tokens the two lanes exchange their shares of y,
 //           each keeping two tokens' sums;
 //   finish  D x, the gate, and rows of y in 16-byte pieces.
-// The decay's exponentials and the state's multiply-adds dominate; Delta's and the gate's
-// special functions are taken once per token and channel, not in both lanes.
+// Delta's and the gate's special functions are taken once per token and channel, not in both
+// lanes. Rows that are not whole 16-byte pieces are copied and stored element by element,
+// everything between is alike.
+//
+// Bound by the scan's instructions: 16 states take about 105 cycles of an SM quarter for 32
+// (token, channel) pairs however they are written (packed, scalar or mixed: their
+// operands leave the register file no faster), 55 us of 232 for each 8 states on B4 T2048
+// D4096; widening and finishing take the rest. Measured against this, in us there:
+// the scan of a tile between the widening of the next and the finishing of the last in
+// straight code 230, warps of their own for these 264, four lanes to a channel 262.
 //
 // Two lanes, because shared memory hands a warp B and C 16 bytes a lane in 2 cycles for
-// two addresses but in 4 for more: with four lanes to a channel N = 64 took 1237 us for B4
-// T2048 D4096 (654 with two), with eight N = 128 4720 us (1489).
+// two addresses but in 4 for more: with four lanes to a channel N = 64 took 1237 us (556
+// with two), with eight N = 128 in fp32 4720 us (1397).
 constexpr int kTile = 32;
 constexpr int kChannels = kThreads / 2;
 
 template <typename E, int NP>
 struct Tile {
+    static constexpr int V = 16 / sizeof(E);                 // channels of a piece
+    static constexpr int pieces = kChannels / V;             // of a row
     static constexpr int row = kChannels * sizeof(E) + 16;   // bytes; 16 more: no bank conflicts
     static constexpr int du_row = 2 * kTile + 4;             // floats of a channel's (Delta, Delta x)
     static constexpr int y_row = kChannels + 16;
@@ -209,19 +219,22 @@ struct Tile {
     static constexpr int raw = 3 * kTile * row + 2 * bc;     // x, dt, z, B, C
     static constexpr int du = kChannels * du_row * 4;
     static constexpr int wide = kTile * NP * 4;
-    static constexpr int bytes = 2 * raw + du + 2 * wide + kTile * y_row * 4;
+    static constexpr int y = kTile * y_row * 4;
+    static constexpr int bytes = 2 * raw + du + 2 * wide + y;
 };
 
-// PARTIAL: only the state at the end of a segment that starts from zero.
-template <typename E, int NP, bool VEC, bool PARTIAL>
-__global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn_scan_kernel(const ScanParams<E> p) {
+// GATE: with z. PARTIAL: only the state at the end of a segment that starts from zero.
+template <typename E, int NP, bool GATE, bool PARTIAL>
+__global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn_scan_kernel(ScanParams<E> p) {
     using S = Tile<E, NP>;
-    constexpr int SP2 = NP / 4, TT = kTile;          // pairs of states of a lane
-    constexpr int V = VEC ? 16 / sizeof(E) : 1;      // channels per piece
-    constexpr int PR = kChannels / V;              // pieces per row
+    constexpr int SP2 = NP / 4, TT = kTile, V = S::V, PR = S::pieces;     // SP2: pairs of states of a lane
+    constexpr int TURNS = TT * PR / kThreads;                // of a thread over a tile's pieces
+    static_assert(TT * PR % kThreads == 0, "whole turns");
     extern __shared__ __align__(16) unsigned char smem[];
-    float *du = reinterpret_cast<float *>(smem + 2 * S::raw);
-    float *bw = du + S::du / 4, *cw = bw + TT * NP, *yb = cw + TT * NP;
+    // tile k's rows; the tile's (Delta, Delta x), B and C, y
+    auto raw_of = [&](int k) { return smem + (k & 1) * S::raw; };
+    float *const du = reinterpret_cast<float *>(smem + 2 * S::raw), *const bc = du + S::du / 4;
+    float *const yb = bc + 2 * S::wide / 4;
 
     const int per = p.D / p.G, blocks = (per + kChannels - 1) / kChannels;
     const int g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * kChannels;
@@ -232,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
     const int n = valid_tokens(p.lengths, b, p.T);
     const int t_begin = s * p.seg, t_end = min(n, t_begin + p.seg);
     if (s > 0 && t_begin >= n) return;
+    const int tokens = t_end - t_begin, tiles = (tokens + TT - 1) / TT;
 
     const int tid = threadIdx.x, c = tid / 2, j = tid % 2;
     const bool live = c < nc;
@@ -288,23 +302,31 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
         }
     }
 
-    // A tile's rows into a raw buffer: this thread's piece of every kThreads / PR-th row.
+    // ------------------------------------------------------------------------- copy
+    // Row by row: this thread's piece of every kThreads / PR-th row.
     const int piece = tid % PR * V;
     auto copy_rows = [&](unsigned char *dst, const E *src, int64_t sb, int64_t st, int t0, int rows) {
-        if (piece >= nc) return;
-        const E *from = src + b * sb + (t0 + tid / PR) * st + d0 + piece;
-        E *to = reinterpret_cast<E *>(dst + tid / PR * S::row) + piece;
-        constexpr int step = kThreads / PR;
+        if (p.pieces) {
+            if (piece >= nc) return;
+            const E *from = src + b * sb + (t0 + tid / PR) * st + d0 + piece;
 #pragma unroll
-        for (int t = 0; t < TT; t += step) {
-            if (t + tid / PR < rows) {
-                if constexpr (VEC)
-                    copy16_async(to, from);
+            for (int i = 0; i < TURNS; ++i) {
+                const int t = tid / PR + i * (kThreads / PR);
+                if (t < rows) copy16_async(dst + t * S::row + piece * sizeof(E), from);
+                from += kThreads / PR * st;
+            }
+        } else {
+            const int q = tid % kChannels;
+            if (q >= nc) return;
+#pragma unroll 8
+            for (int t = tid / kChannels; t < rows; t += kThreads / kChannels) {
+                E *to = reinterpret_cast<E *>(dst + t * S::row) + q;
+                const E *from = src + b * sb + (t0 + t) * st + d0 + q;
+                if constexpr (sizeof(E) == 4)
+                    copy4_async(to, from);
                 else
                     *to = *from;
             }
-            from += step * st;
-            to += step * S::row / sizeof(E);
         }
     };
     auto copy_bc = [&](unsigned char *dst, const E *src, int64_t sb, int64_t st, int t0, int rows) {
@@ -312,9 +334,10 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
         E *to = reinterpret_cast<E *>(dst);
         if (p.rows16) {
             constexpr int W = 16 / sizeof(E), most = NP / W;
-            for (int i = tid; i < rows * most; i += kThreads) {
-                const int t = i / most, q = i % most * W;
-                if (q < p.N) copy16_async(to + t * NP + q, from + t * st + q);
+#pragma unroll
+            for (int i0 = 0; i0 < TT * most; i0 += kThreads) {
+                const int i = i0 + tid, t = i / most, q = i % most * W;
+                if (t < rows && q < p.N) copy16_async(to + t * NP + q, from + t * st + q);
             }
         } else {
             for (int i = tid; i < rows * NP; i += kThreads) {
@@ -323,102 +346,156 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
             }
         }
     };
-    auto fetch = [&](int k, int t0) {
-        unsigned char *raw = smem + k * S::raw;
-        const int rows = min(TT, t_end - t0);
+    auto fetch = [&](int k) {
+        const int t0 = t_begin + k * TT, rows = min(TT, t_end - t0);
+        unsigned char *raw = raw_of(k);
         if (rows > 0) {
             copy_rows(raw, p.x, p.x_sb, p.x_st, t0, rows);
             copy_rows(raw + TT * S::row, p.dt, p.dt_sb, p.dt_st, t0, rows);
             copy_bc(raw + 3 * TT * S::row, p.Bm, p.b_sb, p.b_st, t0, rows);
             if (!PARTIAL) {
-                if (p.z) copy_rows(raw + 2 * TT * S::row, p.z, p.z_sb, p.z_st, t0, rows);
+                if (GATE) copy_rows(raw + 2 * TT * S::row, p.z, p.z_sb, p.z_st, t0, rows);
                 copy_bc(raw + 3 * TT * S::row + S::bc, p.Cm, p.c_sb, p.c_st, t0, rows);
             }
         }
         copy_commit();
     };
 
-    float skip[V];
+    // ------------------------------------------------------------------------ widen
+    // A thread takes one token of a few pieces; a tile's copies never write B and C behind N,
+    // which are 0 from the start. Tokens behind the segment (full: there are none) get Delta = 0
+    // and B = C = 0 and change nothing.
+    F2 bias[TURNS][V / 2];
 #pragma unroll
-    for (int v = 0; v < V; ++v) skip[v] = 0.f;
-    if (!PARTIAL && p.skip && piece < nc) load_f32<V>(p.skip + d0 + piece, skip);
+    for (int i = 0; i < TURNS; ++i) {
+        const int q = (i * kThreads + tid) / TT * V;
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v)
+            bias[i][v] = p.dt_bias ? pack2(q + 2 * v < nc ? p.dt_bias[d0 + q + 2 * v] : 0.f,
+                                           q + 2 * v + 1 < nc ? p.dt_bias[d0 + q + 2 * v + 1] : 0.f)
+                                   : 0;
+    }
+    auto widen = [&](int k, auto full) {
+        const unsigned char *raw = raw_of(k);
+        const int rows = tokens - k * TT;
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int at = i * kThreads + tid, t = at % TT, q = at / TT * V;
+            F2 x[V / 2], step[V / 2];
+            Piece<E, V> pc;
+            pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + q);
+            pc.widen(x);
+            pc.load_rw(reinterpret_cast<const E *>(raw + (TT + t) * S::row) + q);
+            pc.widen(step);
+            float *to = du + q * S::du_row + 2 * t;
+#pragma unroll
+            for (int v = 0; v < V / 2; ++v) {
+                step[v] = add2(step[v], bias[i][v]);
+                const F2 soft = softplus2(step[v]);
+                step[v] = p.softplus ? soft : step[v];
+                F2 u = mul2(step[v], x[v]);
+                if (!full && t >= rows) step[v] = u = 0;
+                float s0, s1, u0, u1;
+                unpack2(step[v], s0, s1);
+                unpack2(u, u0, u1);
+                *reinterpret_cast<float2 *>(to + 2 * v * S::du_row) = make_float2(s0, u0);
+                *reinterpret_cast<float2 *>(to + (2 * v + 1) * S::du_row) = make_float2(s1, u1);
+            }
+        }
+        constexpr int ROWS = PARTIAL ? TT : 2 * TT;             // B's rows, then C's
+#pragma unroll
+        for (int i0 = 0; i0 < ROWS * NP; i0 += kThreads * 4) {
+            const int i = i0 + tid * 4;
+            if (ROWS * NP % (kThreads * 4) != 0 && i >= ROWS * NP) break;
+            const E *from = reinterpret_cast<const E *>(raw + 3 * TT * S::row) + i;
+            *reinterpret_cast<float4 *>(bc + i) = widen4(from, full || i / NP % TT < rows);
+        }
+    };
 
+    // ----------------------------------------------------------------------- finish
+    F2 skip[V / 2];
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v)
+        skip[v] = p.skip && !PARTIAL ? pack2(piece + 2 * v < nc ? p.skip[d0 + piece + 2 * v] : 0.f,
+                                             piece + 2 * v + 1 < nc ? p.skip[d0 + piece + 2 * v + 1] : 0.f)
+                                     : 0;
+    auto finish = [&](int k) {
+        const unsigned char *raw = raw_of(k);
+        const int t0 = t_begin + k * TT;
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int t = tid / PR + i * (kThreads / PR);
+            F2 v[V / 2], w[V / 2];
+            Piece<E, V> pc;
+#pragma unroll
+            for (int q = 0; q < V / 2; q += 2) {
+                const ulonglong2 two =
+                    *reinterpret_cast<const ulonglong2 *>(yb + t * S::y_row + piece + 2 * q);
+                v[q] = two.x;
+                v[q + 1] = two.y;
+            }
+            if (p.skip) {                 // without: x may be anything
+                pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + piece);
+                pc.widen(w);
+#pragma unroll
+                for (int q = 0; q < V / 2; ++q) v[q] = fma2(skip[q], w[q], v[q]);
+            }
+            if constexpr (GATE) {
+                pc.load_rw(reinterpret_cast<const E *>(raw + (2 * TT + t) * S::row) + piece);
+                pc.widen(w);
+#pragma unroll
+                for (int q = 0; q < V / 2; ++q) v[q] = mul2(v[q], mul2(w[q], sigmoid2(w[q])));
+            }
+            pc.round(v);
+            E *to = p.y + (b * p.T + t0 + t) * p.D + d0 + piece;
+            if (t0 + t < t_end && piece < nc) {
+                if (p.pieces) {
+                    pc.store(to);
+                } else {
+                    float f[V];
+#pragma unroll
+                    for (int q = 0; q < V / 2; ++q) unpack2(v[q], f[2 * q], f[2 * q + 1]);
+#pragma unroll
+                    for (int q = 0; q < V; ++q)
+                        if (piece + q < nc) to[q] = from_f32<E>(f[q]);
+                }
+            }
+        }
+    };
+
+    // ------------------------------------------------------------------------- scan
     float dt_sum = 0.f;
-    fetch(0, t_begin);
-    for (int t0 = t_begin, k = 0; t0 < t_end; t0 += TT, k ^= 1) {
-        const int rows = min(TT, t_end - t0);
-        copy_wait<0>();
-        __syncthreads();
-        fetch(k ^ 1, t0 + TT);
-        const unsigned char *raw = smem + k * S::raw;
-        // widen: tokens behind the segment get Delta = 0, B = C = 0 and change nothing
-        {
-            const int t = tid % TT;
-            const bool in = t < rows;
+    auto scan = [&](int t) {
+        const float *my = du + c * S::du_row + 2 * t;
+        const float *bw = bc + t * NP;
+        float yt[4];
+        const float4 da = *reinterpret_cast<const float4 *>(my);
+        const float4 db = *reinterpret_cast<const float4 *>(my + 4);
+        const float step[4] = {da.x, da.z, db.x, db.z}, in[4] = {da.y, da.w, db.y, db.w};
 #pragma unroll
-            for (int q = tid / TT * V; q < kChannels; q += kThreads / TT * V) {
-                if (q >= nc) break;
-                float x[V], dt[V + 1], bias[V];
-                Piece<E, V> pc;
-                pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + q);
-                pc.widen(x);
-                pc.load_rw(reinterpret_cast<const E *>(raw + (TT + t) * S::row) + q);
-                pc.widen(reinterpret_cast<float (&)[V]>(dt));
-                if (p.dt_bias) {
-                    load_f32<V>(p.dt_bias + d0 + q, bias);
+        for (int m = 0; m < 4; ++m) {
+            const F2 dd = pack2(step[m], step[m]), uu = pack2(in[m], in[m]);
+            const ulonglong2 *br = reinterpret_cast<const ulonglong2 *>(bw + m * NP) + j;
+            const ulonglong2 *cr = reinterpret_cast<const ulonglong2 *>(bw + (TT + m) * NP) + j;
+            F2 acc = 0;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) dt[v] += bias[v];
+            for (int q = 0; q < SP2; q += 2) {
+                const ulonglong2 bq = br[q];
+                h[q] = fma2(decay(dd, A2[q]), h[q], mul2(uu, bq.x));
+                h[q + 1] = fma2(decay(dd, A2[q + 1]), h[q + 1], mul2(uu, bq.y));
+                if (!PARTIAL) {
+                    const ulonglong2 cq = cr[q];
+                    acc = q == 0 ? mul2(cq.x, h[q]) : fma2(cq.x, h[q], acc);
+                    acc = fma2(cq.y, h[q + 1], acc);
                 }
-                if (p.softplus) {
-                    if constexpr (V == 1) dt[1] = dt[0];
-#pragma unroll
-                    for (int v = 0; v < V; v += 2) softplus2(dt[v], dt[v + 1]);
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    *reinterpret_cast<float2 *>(du + (q + v) * S::du_row + 2 * t) =
-                        make_float2(in ? dt[v] : 0.f, in ? dt[v] * x[v] : 0.f);
             }
+            float lo, hi;
+            unpack2(acc, lo, hi);
+            yt[m] = lo + hi;
         }
-        for (int i = tid * 4; i < TT * NP; i += kThreads * 4) {
-            const E *br = reinterpret_cast<const E *>(raw + 3 * TT * S::row);
-            const int left = i / NP < rows ? p.N - i % NP : 0;
-            *reinterpret_cast<float4 *>(bw + i) = widen4(br + i, left);
-            if (!PARTIAL) *reinterpret_cast<float4 *>(cw + i) = widen4(br + TT * NP + i, left);
-        }
-        __syncthreads();
-        // scan
-        const float *my = du + c * S::du_row;
-        for (int t = 0; t < rows; t += 4) {
-            float yt[4];
-            const float4 da = *reinterpret_cast<const float4 *>(my + 2 * t);
-            const float4 db = *reinterpret_cast<const float4 *>(my + 2 * t + 4);
-            const float step[4] = {da.x, da.z, db.x, db.z}, in[4] = {da.y, da.w, db.y, db.w};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const F2 dd = pack2(step[m], step[m]), uu = pack2(in[m], in[m]);
-                const ulonglong2 *br = reinterpret_cast<const ulonglong2 *>(bw + (t + m) * NP) + j;
-                const ulonglong2 *cr = reinterpret_cast<const ulonglong2 *>(cw + (t + m) * NP) + j;
-                F2 acc = 0;
-#pragma unroll
-                for (int q = 0; q < SP2; q += 2) {
-                    const ulonglong2 bq = br[q];
-                    h[q] = fma2(decay(dd, A2[q]), h[q], mul2(uu, bq.x));
-                    h[q + 1] = fma2(decay(dd, A2[q + 1]), h[q + 1], mul2(uu, bq.y));
-                    if (!PARTIAL) {
-                        const ulonglong2 cq = cr[q];
-                        acc = q == 0 ? mul2(cq.x, h[q]) : fma2(cq.x, h[q], acc);
-                        acc = fma2(cq.y, h[q + 1], acc);
-                    }
-                }
-                float lo, hi;
-                unpack2(acc, lo, hi);
-                yt[m] = lo + hi;
-            }
-            if (PARTIAL) {
-                dt_sum += (step[0] + step[1]) + (step[2] + step[3]);
-                continue;
-            }
+        if constexpr (PARTIAL) {
+            dt_sum += (step[0] + step[1]) + (step[2] + step[3]);
+        } else {
             // lane j keeps tokens j and 2 + j
             float *y = yb + t * S::y_row + c;
             const float r0 = __shfl_xor_sync(0xffffffffu, j ? yt[0] : yt[1], 1);
@@ -426,45 +503,30 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
             y[j * S::y_row] = (j ? yt[1] : yt[0]) + r0;
             y[(2 + j) * S::y_row] = (j ? yt[3] : yt[2]) + r1;
         }
-        if (PARTIAL) continue;
+    };
+
+    if (p.N < NP) {     // B and C behind N, in both raw places
+        for (int i = tid; i < 4 * TT * NP; i += kThreads)
+            reinterpret_cast<E *>(raw_of(i / (2 * TT * NP)) + 3 * TT * S::row)[i % (2 * TT * NP)] =
+                from_f32<E>(0.f);
         __syncthreads();
-        // finish
-        if (piece < nc) {
-            E *to = p.y + (b * p.T + t0) * p.D + d0 + piece;
-            for (int t = tid / PR; t < rows; t += kThreads / PR) {
-                float x[V], z[V];
-                alignas(16) float y[V + 1];
-                Piece<E, V> pc;
-                pc.load_rw(reinterpret_cast<const E *>(raw + t * S::row) + piece);
-                pc.widen(x);
-#pragma unroll
-                for (int v = 0; v < V; v += 4) {
-                    const float *from = yb + t * S::y_row + piece + v;
-                    if constexpr (V == 1)
-                        y[0] = *from;
-                    else
-                        *reinterpret_cast<float4 *>(y + v) = *reinterpret_cast<const float4 *>(from);
-                }
-                if (p.skip) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) y[v] = fmaf(skip[v], x[v], y[v]);
-                }
-                if (p.z) {
-                    pc.load_rw(reinterpret_cast<const E *>(raw + (2 * TT + t) * S::row) + piece);
-                    pc.widen(z);
-#pragma unroll
-                    for (int v = 0; v < V; v += 2) {
-                        const int w = V == 1 ? 0 : v + 1;
-                        const F2 gate = activate2(pack2(z[v], z[w]), GDN_ACT_SILU);
-                        unpack2(mul2(pack2(y[v], y[w]), gate), y[v], y[v + 1]);
-                    }
-                }
-                pc.round(reinterpret_cast<const float (&)[V]>(y));
-                pc.store(to + static_cast<int64_t>(t) * p.D);
-            }
+    }
+    fetch(0);
+    for (int k = 0; k < tiles; ++k) {
+        const int rows = min(TT, tokens - k * TT);
+        copy_wait<0>();
+        __syncthreads();     // tile k's rows are here; tile k - 1 is finished
+        fetch(k + 1);
+        if (rows == TT) widen(k, std::true_type()); else widen(k, std::false_type());
+        __syncthreads();
+        for (int t = 0; t < rows; t += 4) scan(t);
+        if constexpr (!PARTIAL) {
+            __syncthreads();
+            finish(k);
         }
     }
-    if (PARTIAL) {
+    copy_wait<0>();
+    if constexpr (PARTIAL) {
         store_states(p.seg_h + seg_at(s) * p.N);
         if (live && j == 0) p.seg_dt[seg_at(s)] = dt_sum;
     } else if (p.h_final && t_end == n) {
@@ -508,31 +570,34 @@ size_t workspace_need(const gdn_scan_problem *p) {
     return n == 1 ? 0 : align_up(rows * p->N * 4) + align_up(rows * 4);
 }
 
-template <typename E, int NP, bool VEC>
+template <typename E>
+cudaError_t launch_blocks(void (*kernel)(ScanParams<E>), dim3 grid, int bytes, const ScanParams<E> &p,
+                          cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, bytes, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename E, int NP>
 cudaError_t launch_prompt(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace, cudaStream_t s) {
+    using S = Tile<E, NP>;
     const int n = segments(pr);
     p.seg = ((pr->T + n - 1) / n + kTile - 1) / kTile * kTile;
     p.segs = (pr->T + p.seg - 1) / p.seg;
     const dim3 grid(static_cast<unsigned>(row_blocks(pr)), pr->B, p.segs);
-    constexpr int bytes = Tile<E, NP>::bytes;
-    cudaError_t e;
     if (p.segs > 1) {
         p.seg_h = static_cast<float *>(workspace);
         p.seg_dt = reinterpret_cast<float *>(
             static_cast<char *>(workspace) +
             align_up(static_cast<size_t>(pr->B) * p.segs * pr->D * pr->N * 4));
-        auto first = gdn_scan_kernel<E, NP, VEC, true>;
-        e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        first<<<dim3(grid.x, grid.y, p.segs - 1), kThreads, bytes, s>>>(p);
-        e = cudaGetLastError();
+        const cudaError_t e = launch_blocks(gdn_scan_kernel<E, NP, false, true>,
+                                            dim3(grid.x, grid.y, p.segs - 1), S::bytes, p, s);
         if (e != cudaSuccess) return e;
     }
-    auto kernel = gdn_scan_kernel<E, NP, VEC, false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, bytes, s>>>(p);
-    return cudaGetLastError();
+    return launch_blocks(p.z ? gdn_scan_kernel<E, NP, true, false> : gdn_scan_kernel<E, NP, false, false>,
+                         grid, S::bytes, p, s);
 }
 
 template <typename E, int NP>
@@ -549,14 +614,13 @@ cudaError_t launch(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace
         return cudaGetLastError();
     }
     constexpr size_t e = sizeof(E);
-    const bool vec = (pr->D / pr->G) * e % 16 == 0 &&
-                     pieces16(p.x, pr->B, pr->T, pr->D, p.x_sb, p.x_st, e) &&
-                     pieces16(p.dt, pr->B, pr->T, pr->D, p.dt_sb, p.dt_st, e) &&
-                     (!p.z || pieces16(p.z, pr->B, pr->T, pr->D, p.z_sb, p.z_st, e));
+    p.pieces = (pr->D / pr->G) * e % 16 == 0 &&
+               pieces16(p.x, pr->B, pr->T, pr->D, p.x_sb, p.x_st, e) &&
+               pieces16(p.dt, pr->B, pr->T, pr->D, p.dt_sb, p.dt_st, e) &&
+               (!p.z || pieces16(p.z, pr->B, pr->T, pr->D, p.z_sb, p.z_st, e));
     p.rows16 = pieces16(p.Bm, pr->B, pr->T, pr->N, p.b_sb, p.b_st, e) &&
                pieces16(p.Cm, pr->B, pr->T, pr->N, p.c_sb, p.c_st, e);
-    return vec ? launch_prompt<E, NP, true>(pr, p, workspace, s)
-               : launch_prompt<E, NP, false>(pr, p, workspace, s);
+    return launch_prompt<E, NP>(pr, p, workspace, s);
 }
 
 template <typename E>
@@ -568,7 +632,8 @@ cudaError_t dispatch(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspa
     p.c_sb = pr->c_stride_b; p.c_st = pr->c_stride_t;
     p.B = pr->B; p.T = pr->T; p.D = pr->D; p.N = pr->N; p.G = pr->G;
     p.softplus = (pr->flags & GDN_SCAN_SOFTPLUS) ? 1 : 0;
-    p.rows16 = 0; p.segs = 1; p.seg = pr->T; p.seg_h = p.seg_dt = nullptr;
+    p.rows16 = p.pieces = 0;
+    p.segs = 1; p.seg = pr->T; p.seg_h = p.seg_dt = nullptr;
     if (pr->N <= 8) return launch<E, 8>(pr, p, workspace, s);
     if (pr->N <= 16) return launch<E, 16>(pr, p, workspace, s);
     if (pr->N <= 32) return launch<E, 32>(pr, p, workspace, s);
