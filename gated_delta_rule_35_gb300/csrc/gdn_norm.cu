@@ -253,7 +253,7 @@ __device__ __forceinline__ void merge_cluster(float (&part)[3][kThreads], int gr
     if (K > 1) cluster_arrive();
 }
 
-template <typename E, int V>
+template <typename E, int V, bool GATED>
 __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kernel(NormParams<E> p) {
     __shared__ float means[kThreads * V], squares[kThreads * V];   // [token row][channel of the slice]
     __shared__ float columns[kThreads * V];                        // sums over token rows
@@ -325,14 +325,18 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
 #pragma unroll
                 for (int u = 0; u < BT; ++u) {
                     Piece<E, V> q = block_piece(i, u);
-                    if (u >= here) q.zero();
                     q.widen(v[u]);
                 }
                 if (i >= kKept) fetch(i + kRing); else copy_commit();
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    if (i == set)
-                        shift[k] = mul2(add2(add2(v[0][k], v[1][k]), add2(v[2][k], v[3][k])), both(-1.f / here));
+                    if (i == set) {
+                        F2 sum = v[0][k];
+#pragma unroll
+                        for (int u = 1; u < BT; ++u)
+                            if (u < here) sum = add2(sum, v[u][k]);
+                        shift[k] = mul2(sum, both(-1.f / here));
+                    }
                     b1[k] = b2[k] = 0;
                 }
 #pragma unroll
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
             w[k] = mul2(w[k], pack2(g_rstd[ga], g_rstd[gb]));
         }
         const int64_t g_step = RP * p.g_st, y_step = static_cast<int64_t>(RP) * p.C;
-        const E *gate = p.gate ? p.gate + b * p.g_sb + c + (t_begin + row) * p.g_st : nullptr;
+        const E *gate = GATED ? p.gate + b * p.g_sb + c + (t_begin + row) * p.g_st : nullptr;
         E *y = p.y + (b * p.T + t_begin + row) * p.C + c;
         // kept blocks between those that still arrive
         const int kept = min(blocks, kKept), other = blocks - kept, mixed = 2 * min(kept, other);
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
         };
 #pragma unroll
         for (int u = 0; u < BT; ++u) z[u].zero();
-        if (gate && blocks > 0) fetch_gate(order(0));
+        if (GATED && blocks > 0) fetch_gate(order(0));
         for (int i = 0; i < blocks; ++i) {
             const int block = order(i);
             if (block >= kKept) copy_wait<kRing - 1>();
@@ -458,17 +462,17 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
                 zn[u] = z[u];
             }
             if (block >= kKept) fetch(block + kRing);
-            if (gate && i + 1 < blocks) fetch_gate(order(i + 1));
+            if (GATED && i + 1 < blocks) fetch_gate(order(i + 1));
             E *to = y + static_cast<int64_t>(block) * BT * y_step;
 #pragma unroll
             for (int u = 0; u < BT; ++u) {
                 if (block * BT + u >= own) break;
                 F2 v[N], gv[N];
                 r[u].widen(v);
-                zn[u].widen(gv);
+                if constexpr (GATED) zn[u].widen(gv);
 #pragma unroll
                 for (int k = 0; k < N; ++k) v[k] = fma2(add2(v[k], mean[k]), w[k], bias[k]);
-                outputs(v, gv, gate != nullptr, p.act);
+                outputs(v, gv, GATED, p.act);
                 r[u].round(v);
                 r[u].store(to + u * y_step);
             }
@@ -643,7 +647,8 @@ cudaError_t launch_tokens(NormParams<E> &p, cudaStream_t s) {
     }
     p.groups = groups;
     constexpr int bytes = (kKept + kRing) * kBlockTokens * kThreads * sizeof(typename Piece<E, V>::Raw);
-    return launch_cluster(gdn_norm_tokens_kernel<E, V>, K, slices(groups), bytes, p, s);
+    return launch_cluster(p.gate ? gdn_norm_tokens_kernel<E, V, true> : gdn_norm_tokens_kernel<E, V, false>, K,
+                          slices(groups), bytes, p, s);
 }
 
 template <typename E, int V>
