@@ -205,7 +205,9 @@ constexpr int kSetBlocks = 32;
 // output; the others pass through kRing places there, twice.
 constexpr int kKept = 3;
 constexpr int kRing = 2;
-constexpr int kMaxCluster = 8;
+// Clusters of 16 need the kernels' leave and leave SMs empty: for few and long sequences only (two
+// of 16384 tokens and 64 channels 43 -> 23 us; four of 4096 and 1280 would take 49 us for 33).
+constexpr int kMaxCluster = 16;
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
@@ -494,25 +496,40 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
     if (n == 0) return;                                            // the whole cluster
     const int share = (n + K - 1) / K, t_begin = min(n, rank * share), t_end = min(n, t_begin + share);
     const E *x = p.x + b * p.x_sb + c0;
-    float count = 0.f, mean = 0.f, m2 = 0.f;
+    // sums about the first value of every 64 pieces, merged as in the tokens kernel
+    float count = 0.f, mean = 0.f, m2 = 0.f, shift = 0.f, s1 = 0.f, s2 = 0.f;
+    int set = 0;
+    auto merge = [&] {
+        const float nb = static_cast<float>(set) * V, na = count;
+        if (set == 0) return;
+        count += nb;
+        const float off = s1 / nb, d = shift + off - mean, w = nb / count;
+        mean = fmaf(d, w, mean);
+        m2 += fmaf(d * d, na * w, s2 - off * s1);
+        set = 0;
+    };
     for (int64_t t = t_begin; t < t_end; ++t) {
+#pragma unroll 4
         for (int q = threadIdx.x * V; q < cg; q += kThreads * V) {
             Piece<E, V> r;
-            float f[V], s = 0.f, s2 = 0.f;
+            float f[V];
             r.load_rw(x + t * p.x_st + q);
             r.widen(f);
+            if (set == 64) merge();
+            if (set == 0) {
+                shift = f[0];
+                s1 = s2 = 0.f;
+            }
+            ++set;
 #pragma unroll
-            for (int k = 0; k < V; ++k) s += f[k];
-            s *= 1.f / V;
-#pragma unroll
-            for (int k = 0; k < V; ++k) s2 = fmaf(f[k] - s, f[k] - s, s2);
-            const float na = count;
-            count += V;
-            const float d = s - mean, w = V / count;
-            mean = fmaf(d, w, mean);
-            m2 += fmaf(d * d, na * w, s2);
+            for (int k = 0; k < V; ++k) {
+                const float d = f[k] - shift;
+                s1 += d;
+                s2 = fmaf(d, d, s2);
+            }
         }
     }
+    merge();
     part[0][threadIdx.x] = count;
     part[1][threadIdx.x] = mean;
     part[2][threadIdx.x] = m2;
@@ -598,8 +615,9 @@ cudaError_t launch_cluster(void (*kernel)(NormParams<E>), int K, int slices, int
     p.cluster = K;
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = bytes;
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const void *f = reinterpret_cast<const void *>(kernel);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && K > 8) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -620,7 +638,7 @@ cudaError_t launch_tokens(NormParams<E> &p, cudaStream_t s) {
     if (unit <= p.G && unit * static_cast<int64_t>(cg) / V > kThreads) {
         if (cg % V != 0) return launch_tokens<E, 1>(p, s);
         int K = 1;
-        while (K < kMaxCluster && static_cast<int64_t>(p.B) * p.G * K < 4 * 152 && p.T > 2 * K) K *= 2;
+        while (K < 8 && static_cast<int64_t>(p.B) * p.G * K < 4 * 152 && p.T > 2 * K) K *= 2;
         return launch_cluster(gdn_norm_wide_kernel<E, V>, K, p.G, 0, p, s);
     }
     // Slice and cluster by the turns that a thread takes: its tokens, and about 8 for the
@@ -634,6 +652,7 @@ cudaError_t launch_tokens(NormParams<E> &p, cudaStream_t s) {
         const int m = n < p.G ? n : p.G, rows = kThreads / (m * cg / V);
         for (int k = 1; k <= kMaxCluster; k *= 2) {
             const int64_t blocks = static_cast<int64_t>(p.B) * slices(m) * k;
+            if (k > 8 && blocks > 152) break;      // 16 find places only on an empty GPU
             const int share = (p.T + k - 1) / k;
             const float turns = static_cast<float>((share + rows - 1) / rows + 8) *
                                 (1.f + 16.f / (m * cg * sizeof(E)));
