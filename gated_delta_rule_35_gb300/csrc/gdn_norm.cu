@@ -626,7 +626,12 @@ cudaError_t launch_cluster(void (*kernel)(NormParams<E>), int K, int slices, int
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = K > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess && K > 8) {       // no place for 16 (a part of a GPU, say)
+        cudaGetLastError();
+        return launch_cluster(kernel, 8, slices, bytes, p, s);
+    }
+    return e;
 }
 
 template <typename E, int V>

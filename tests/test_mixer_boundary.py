@@ -111,6 +111,24 @@ def test_scan_workspace():
     assert e.value.status == INVALID
 
 
+def test_scan_needs_its_workspace():
+    """One long sequence of few channels is cut into segments."""
+    need = gdn.scan_workspace_bytes(1, 4096, 64, 16)
+    assert need > 0
+    kw = dict(B=1, T=4096, D=64)
+    assert scan(**kw, ws=need - 1) == WORKSPACE
+    assert scan(**kw, workspace=None) == WORKSPACE
+    assert scan(**kw, workspace=fake(12) + 8) == ALIGNMENT
+    for n in ("x", "y", "h_final", "h0"):
+        assert scan(**kw, workspace=fake(SCAN_ARGS.index(n))) == INVALID
+
+
+@pytest.mark.parametrize("call,kw", [(conv, dict(C=1 << 20, T=1 << 12)), (scan, dict(D=(1 << 24) + 16)),
+                                     (norm, dict(B=(1 << 26) + 1)), (norm, dict(C=65536, G=65536))])
+def test_sizes_beyond_the_grids(call, kw):
+    assert call(**kw) == UNSUPPORTED
+
+
 def test_wrappers_take_cuda_tensors_only():
     x = torch.zeros(1, 4, 8)
     with pytest.raises(ValueError):

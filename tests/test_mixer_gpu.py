@@ -138,7 +138,7 @@ def check_scan(y, h, i):
 
 SCAN_SIZES = [(1, 1, 1, 1, 1), (2, 3, 8, 16, 1), (3, 17, 66, 13, 2), (2, 65, 64, 24, 1), (2, 130, 40, 64, 4),
               (1, 200, 33, 100, 3), (4, 64, 128, 16, 2), (2, 127, 96, 8, 1), (1, 70, 16, 128, 1),
-              (2, 40, 130, 4, 1), (1, 31, 264, 16, 1)]
+              (2, 40, 130, 4, 1), (1, 31, 264, 16, 1), (2, 33, 48, 1, 1), (1, 20, 70, 2, 2)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -158,7 +158,7 @@ def test_scan(size, dtype):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("size", [(1, 4001, 16, 16, 1), (2, 1500, 24, 24, 2), (1, 2050, 8, 64, 1),
-                                  (3, 700, 40, 5, 1)])
+                                  (3, 700, 40, 5, 1), (1, 300, 72, 128, 1)])
 def test_scan_long_sequences_of_few_channels(size, dtype):
     """Where the tokens are cut into segments, with the state in place."""
     for kw in (dict(), dict(lengths=True, strided=True)):
@@ -210,7 +210,7 @@ def test_scan_steps_of_extreme_sizes():
 # ------------------------------------------------------------------- group norm
 NORM_SIZES = [(1, 1, 1, 1), (5, 1, 64, 4), (300, 1, 96, 3), (7, 1, 1003, 17), (3, 1, 4096, 1), (2, 1, 12000, 2),
               (2, 2, 8, 8), (3, 33, 40, 4), (2, 257, 330, 11), (1, 1500, 640, 32), (4, 64, 1280, 32),
-              (2, 300, 72, 1), (1, 5, 8200, 2), (1, 4100, 16, 16)]
+              (2, 300, 72, 1), (1, 5, 8200, 2), (1, 4100, 16, 16), (1, 9000, 24, 2), (1, 300, 3001, 1)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -257,6 +257,40 @@ def test_group_norm_of_far_means_and_in_place(T):
     assert gdn.group_norm(same, 3, out=same) is same and torch.equal(same, y)
     const = torch.full((2, T, 8), 5.0, device="cuda")
     assert (gdn.group_norm(const, 2) == 0).all()
+
+
+# ------------------------------------------------------- strides of whole pieces
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_slices_of_aligned_projections(dtype):
+    """Slices that start and step by whole 16-byte pieces take the wide loads."""
+    B, T, D, N = 2, 45, 72, 16
+    g = gen(650)
+    wide = torch.randn(B, T, 3 * D + 4 * N, generator=g).to(dtype).cuda()
+    x, dt, z = wide[..., :D], wide[..., D:2 * D], wide[..., 2 * D:3 * D]
+    bm, cm = (wide[..., 3 * D + k * 2 * N:3 * D + (k + 1) * 2 * N].unflatten(-1, (2, N)) for k in (0, 1))
+    w = torch.randn(D, 4, generator=g).cuda()
+    y, so = gdn.conv_fwd(x, w, act="silu")
+    check_conv(y, so, x, w, None, None, None, "silu")
+    i = dict(scan_inputs(B, T, D, N, 2, dtype, 651), x=x, dt=dt, z=z, B=bm, C=cm)
+    check_scan(*gdn.scan_fwd(**i), i)
+    one = dict(i, **{k: i[k][:, 7:8] for k in ("x", "dt", "z", "B", "C")})
+    check_scan(*gdn.scan_fwd(**one), one)
+    out = torch.full((B, T, D), FILL, dtype=dtype, device="cuda")
+    check_norm(gdn.group_norm(x, 3, act="sigmoid", gate=z, out=out), x, 3, None, None, "sigmoid", z, None)
+
+
+def test_many_sequences_of_one_token():
+    """Batches that fill the GPU take several sequences to a thread; the last batch is partial."""
+    B, D, N = 1030, 64, 16
+    x, w, bi, st, _ = conv_inputs(B, 1, 1000, 4, BF16, 660)
+    y, so = gdn.conv_fwd(x, w, bi, st)
+    check_conv(y, so, x, w, bi, st, None, "silu")
+    n = torch.randint(0, 3, (B,), generator=gen(661)).to(torch.int32).cuda()
+    i = dict(scan_inputs(B, 2, 512, N, 2, F32, 662), lengths=n)
+    spoil(i["x"], n)
+    out = torch.full((B, 2, 512), FILL, device="cuda")
+    y, h = gdn.scan_fwd(**i, out=out)
+    mb.untouched(y, check_scan(y, h, i), FILL)
 
 
 # --------------------------------------------------------------- used together
@@ -360,6 +394,70 @@ def test_calls_repeat_bit_for_bit_on_another_stream_and_from_a_graph():
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_threads_on_streams_of_their_own():
+    import threading
+    calls = all_calls()
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(5):
+            for c, w in zip(calls, want):
+                got = c(stream=s)
+                s.synchronize()
+                bad.extend(1 for a, b in zip(got, w) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+
+
+def test_state_in_place_replays_from_a_graph():
+    """A captured token step advances the state at every replay."""
+    x, w, bi, st, _ = conv_inputs(4, 3, 64, 4, BF16, 20)
+    i = scan_inputs(4, 3, 64, 16, 1, BF16, 21)
+    step = {k: i[k][:, :1].clone() if i[k] is not None else None for k in ("x", "dt", "z", "B", "C")}
+    rest = dict(A=i["A"], D=i["D"], dt_bias=i["dt_bias"], dt_softplus=True)
+    token = x[:, :1].clone()
+
+    def tokens(conv_state, h, run):
+        out = []
+        for t in range(3):
+            token.copy_(x[:, t:t + 1])
+            for k in step:
+                if step[k] is not None:
+                    step[k].copy_(i[k][:, t:t + 1])
+            out.append([a.clone() for a in run(conv_state, h)])
+        return out
+
+    def run(conv_state, h):
+        return gdn.conv_step(token, w, conv_state, bi)[0], gdn.scan_step(**step, **rest, state=h)[0]
+
+    cs, h = st.clone(), i["h0"].clone()
+    want = tokens(cs, h, run)
+    cs2, h2 = st.clone(), i["h0"].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = run(cs2, h2)
+    cs2.copy_(st)
+    h2.copy_(i["h0"])
+
+    def replay(*_):
+        g.replay()
+        return outs
+
+    got = tokens(cs2, h2, replay)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for u, v in zip(got, want) for a, b in zip(u, v))
+    assert torch.equal(cs, cs2) and torch.equal(h, h2)
 
 
 def test_two_graphs_replay_side_by_side():
