@@ -303,17 +303,25 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
     }
 
     // ------------------------------------------------------------------------- copy
-    // Row by row: this thread's piece of every kThreads / PR-th row.
+    // Row by row: this thread's piece of every kThreads / PR-th row, of the next tile.
     const int piece = tid % PR * V;
-    auto copy_rows = [&](unsigned char *dst, const E *src, int64_t sb, int64_t st, int t0, int rows) {
+    struct Rows {
+        const E *at;
+        int64_t turn;        // from row to row of a tile, TURNS of them
+    };
+    auto rows_of = [&](const E *src, int64_t sb, int64_t st) {
+        return Rows{src + b * sb + (t_begin + tid / PR) * st + d0 + piece, kThreads / PR * st};
+    };
+    Rows rx = rows_of(p.x, p.x_sb, p.x_st), rdt = rows_of(p.dt, p.dt_sb, p.dt_st), rz = rx;
+    if (GATE) rz = rows_of(p.z, p.z_sb, p.z_st);
+    auto copy_rows = [&](unsigned char *dst, Rows &r, const E *src, int64_t sb, int64_t st, int t0, int rows) {
         if (p.pieces) {
-            if (piece >= nc) return;
-            const E *from = src + b * sb + (t0 + tid / PR) * st + d0 + piece;
+            unsigned char *to = dst + tid / PR * S::row + piece * sizeof(E);
 #pragma unroll
             for (int i = 0; i < TURNS; ++i) {
-                const int t = tid / PR + i * (kThreads / PR);
-                if (t < rows) copy16_async(dst + t * S::row + piece * sizeof(E), from);
-                from += kThreads / PR * st;
+                if (piece < nc && tid / PR + i * (kThreads / PR) < rows)
+                    copy16_async(to + i * (kThreads / PR) * S::row, r.at);
+                r.at += r.turn;
             }
         } else {
             const int q = tid % kChannels;
@@ -350,11 +358,11 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
         const int t0 = t_begin + k * TT, rows = min(TT, t_end - t0);
         unsigned char *raw = raw_of(k);
         if (rows > 0) {
-            copy_rows(raw, p.x, p.x_sb, p.x_st, t0, rows);
-            copy_rows(raw + TT * S::row, p.dt, p.dt_sb, p.dt_st, t0, rows);
+            copy_rows(raw, rx, p.x, p.x_sb, p.x_st, t0, rows);
+            copy_rows(raw + TT * S::row, rdt, p.dt, p.dt_sb, p.dt_st, t0, rows);
             copy_bc(raw + 3 * TT * S::row, p.Bm, p.b_sb, p.b_st, t0, rows);
             if (!PARTIAL) {
-                if (GATE) copy_rows(raw + 2 * TT * S::row, p.z, p.z_sb, p.z_st, t0, rows);
+                if (GATE) copy_rows(raw + 2 * TT * S::row, rz, p.z, p.z_sb, p.z_st, t0, rows);
                 copy_bc(raw + 3 * TT * S::row + S::bc, p.Cm, p.c_sb, p.c_st, t0, rows);
             }
         }
@@ -419,6 +427,8 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
         skip[v] = p.skip && !PARTIAL ? pack2(piece + 2 * v < nc ? p.skip[d0 + piece + 2 * v] : 0.f,
                                              piece + 2 * v + 1 < nc ? p.skip[d0 + piece + 2 * v + 1] : 0.f)
                                      : 0;
+    E *y_at = p.y + (b * p.T + t_begin + tid / PR) * p.D + d0 + piece;     // this thread's first of a tile
+    const int64_t y_turn = static_cast<int64_t>(kThreads / PR) * p.D;
     auto finish = [&](int k) {
         const unsigned char *raw = raw_of(k);
         const int t0 = t_begin + k * TT;
@@ -447,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
                 for (int q = 0; q < V / 2; ++q) v[q] = mul2(v[q], mul2(w[q], sigmoid2(w[q])));
             }
             pc.round(v);
-            E *to = p.y + (b * p.T + t0 + t) * p.D + d0 + piece;
+            E *const to = y_at;
+            y_at += y_turn;
             if (t0 + t < t_end && piece < nc) {
                 if (p.pieces) {
                     pc.store(to);
