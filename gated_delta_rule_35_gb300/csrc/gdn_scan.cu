@@ -196,14 +196,16 @@ __global__ void __launch_bounds__(kThreads, NB > 1 ? 12 : 1) gdn_scan_step_kerne
 //
 // Bound by the scan's instructions: 16 states take about 105 cycles of an SM quarter for 32
 // (token, channel) pairs however they are written (packed, scalar or mixed: their
-// operands leave the register file no faster), 55 us of 232 for each 8 states on B4 T2048
-// D4096; widening and finishing take the rest. Measured against this, in us there:
-// the scan of a tile between the widening of the next and the finishing of the last in
-// straight code 230, warps of their own for these 264, four lanes to a channel 262.
+// operands leave the register file no faster). Of 201 us for B4 T2048 D4096 N = 16 in bf16
+// the scan takes 131, widening 32, finishing 26, the copies 12. Measured against this,
+// in us there and then: a tile's scan between the widening of the next and the
+// finishing of the last, in straight code, 230 for 232; warps of their own for these 264;
+// four lanes to a channel 262 for 230; blocks of 64 threads 203, of 32 208, of 256 254 (for
+// 201; one sequence of 32768 tokens and 2048 channels 622, 649 and 506 for 511).
 //
 // Two lanes, because shared memory hands a warp B and C 16 bytes a lane in 2 cycles for
-// two addresses but in 4 for more: with four lanes to a channel N = 64 took 1237 us (556
-// with two), with eight N = 128 in fp32 4720 us (1397).
+// two addresses but in 4 for more: with four lanes to a channel N = 64 took 1237 us (523
+// now), with eight N = 128 in fp32 4720 us (1225 now).
 constexpr int kTile = 32;
 constexpr int kChannels = kThreads / 2;
 
@@ -571,16 +573,17 @@ gdn_status check(const gdn_scan_problem *p) {
     return GDN_OK;
 }
 
-// Segments of a prompt: so many that 3 blocks stand on every SM, of 64 tokens at least. The
-// first pass over a segment repeats most of the arithmetic, so channels that alone fill
-// half of those places are not cut. One sequence of 32768 tokens and 2048 channels (32
-// blocks): 572 us in 14 segments, 655 in 9, 590 in 23; 512 tokens of it 27 us in 8, 49
-// in 2. Four of 2048 tokens and 4096 channels (256 blocks): 230 us whole, 296 in 2.
 int64_t row_blocks(const gdn_scan_problem *p) {
     const int per = p->D / p->G;
     return static_cast<int64_t>(p->G) * ((per + kChannels - 1) / kChannels);
 }
 
+// Segments of a prompt: so many that 3 blocks stand on every SM, of 64 tokens at least. The
+// first pass over a segment repeats most of the arithmetic, so channels that alone fill
+// half of those places are not cut. One sequence of 32768 tokens and 2048 channels (32
+// blocks), when chosen: 572 us in 14 segments (511 now), 655 in 9, 590 in 23; 512 tokens
+// of it 27 us in 8, 49 in 2. Four of 2048 tokens and 4096 channels (256 blocks): 230 us
+// whole (201 now), 296 in 2.
 int segments(const gdn_scan_problem *p) {
     const int64_t blocks = p->B * row_blocks(p);
     const int64_t want = 3 * 152 / blocks, most = p->T / 64;
