@@ -339,11 +339,11 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
         }
     };
     // B and C the same way, MOST pieces to a row at most.
-    constexpr int W = 16 / sizeof(E), MOST = NP / W, BC = (TT * MOST + kThreads - 1) / kThreads;
+    constexpr int W = 16 / sizeof(E), MOST = NP / W, STEP = kThreads / MOST, BC = (TT + STEP - 1) / STEP;
     const int at_bc = tid % MOST * W;
     auto bc_rows_of = [&](const E *src, int64_t sb, int64_t st) {
         return Rows{src + b * sb + (t_begin + tid / MOST) * st + static_cast<int64_t>(g) * p.N + at_bc,
-                    (BC > 1 ? kThreads / MOST : TT) * st};
+                    STEP * st};
     };
     Rows rb = bc_rows_of(p.Bm, p.b_sb, p.b_st), rc = bc_rows_of(p.Cm, p.c_sb, p.c_st);
     auto copy_bc = [&](unsigned char *dst, Rows &r, const E *src, int64_t sb, int64_t st, int t0, int rows) {
@@ -351,10 +351,10 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
             E *to = reinterpret_cast<E *>(dst) + tid / MOST * NP + at_bc;
 #pragma unroll
             for (int i = 0; i < BC; ++i) {
-                if (at_bc < p.N && tid / MOST + i * (kThreads / MOST) < rows)
-                    copy16_async(to + i * (kThreads / MOST) * NP, r.at);
-                r.at += r.turn;
+                if (at_bc < p.N && tid / MOST < STEP && tid / MOST + i * STEP < rows)
+                    copy16_async(to + i * STEP * NP, r.at + i * r.turn);
             }
+            r.at += TT * st;
         } else {
             const E *from = src + b * sb + t0 * st + static_cast<int64_t>(g) * p.N;
             E *to = reinterpret_cast<E *>(dst);
@@ -628,26 +628,16 @@ cudaError_t launch_prompt(const gdn_scan_problem *pr, ScanParams<E> &p, void *wo
 }
 
 template <typename E, int NP>
-cudaError_t launch(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspace, cudaStream_t s) {
-    if (pr->T <= kStepTokens) {
-        // kBatch sequences to a thread where that still leaves two blocks to an SM
-        constexpr int channels = kThreads / (NP / 4);
-        const unsigned blocks = pr->G * ((pr->D / pr->G + channels - 1) / channels);
-        if (static_cast<int64_t>(blocks) * ((pr->B + kBatch - 1) / kBatch) >= 2 * 152)
-            gdn_scan_step_kernel<E, NP, kBatch>
-                <<<dim3(blocks, (pr->B + kBatch - 1) / kBatch), kThreads, 0, s>>>(p);
-        else
-            gdn_scan_step_kernel<E, NP, 1><<<dim3(blocks, pr->B), kThreads, 0, s>>>(p);
-        return cudaGetLastError();
-    }
-    constexpr size_t e = sizeof(E);
-    p.pieces = (pr->D / pr->G) * e % 16 == 0 &&
-               pieces16(p.x, pr->B, pr->T, pr->D, p.x_sb, p.x_st, e) &&
-               pieces16(p.dt, pr->B, pr->T, pr->D, p.dt_sb, p.dt_st, e) &&
-               (!p.z || pieces16(p.z, pr->B, pr->T, pr->D, p.z_sb, p.z_st, e));
-    p.rows16 = pieces16(p.Bm, pr->B, pr->T, pr->N, p.b_sb, p.b_st, e) &&
-               pieces16(p.Cm, pr->B, pr->T, pr->N, p.c_sb, p.c_st, e);
-    return launch_prompt<E, NP>(pr, p, workspace, s);
+cudaError_t launch_step(const gdn_scan_problem *pr, const ScanParams<E> &p, cudaStream_t s) {
+    // kBatch sequences to a thread where that still leaves two blocks to an SM
+    constexpr int channels = kThreads / (NP / 4);
+    const unsigned blocks = pr->G * ((pr->D / pr->G + channels - 1) / channels);
+    if (static_cast<int64_t>(blocks) * ((pr->B + kBatch - 1) / kBatch) >= 2 * 152)
+        gdn_scan_step_kernel<E, NP, kBatch>
+            <<<dim3(blocks, (pr->B + kBatch - 1) / kBatch), kThreads, 0, s>>>(p);
+    else
+        gdn_scan_step_kernel<E, NP, 1><<<dim3(blocks, pr->B), kThreads, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename E>
@@ -661,11 +651,29 @@ cudaError_t dispatch(const gdn_scan_problem *pr, ScanParams<E> &p, void *workspa
     p.softplus = (pr->flags & GDN_SCAN_SOFTPLUS) ? 1 : 0;
     p.rows16 = p.pieces = 0;
     p.segs = 1; p.seg = pr->T; p.seg_h = p.seg_dt = nullptr;
-    if (pr->N <= 8) return launch<E, 8>(pr, p, workspace, s);
-    if (pr->N <= 16) return launch<E, 16>(pr, p, workspace, s);
-    if (pr->N <= 32) return launch<E, 32>(pr, p, workspace, s);
-    if (pr->N <= 64) return launch<E, 64>(pr, p, workspace, s);
-    return launch<E, 128>(pr, p, workspace, s);
+    if (pr->T <= kStepTokens) {            // lanes to a channel: a power of two
+        if (pr->N <= 8) return launch_step<E, 8>(pr, p, s);
+        if (pr->N <= 16) return launch_step<E, 16>(pr, p, s);
+        if (pr->N <= 32) return launch_step<E, 32>(pr, p, s);
+        if (pr->N <= 64) return launch_step<E, 64>(pr, p, s);
+        return launch_step<E, 128>(pr, p, s);
+    }
+    constexpr size_t e = sizeof(E);
+    p.pieces = (pr->D / pr->G) * e % 16 == 0 &&
+               pieces16(p.x, pr->B, pr->T, pr->D, p.x_sb, p.x_st, e) &&
+               pieces16(p.dt, pr->B, pr->T, pr->D, p.dt_sb, p.dt_st, e) &&
+               (!p.z || pieces16(p.z, pr->B, pr->T, pr->D, p.z_sb, p.z_st, e));
+    p.rows16 = pieces16(p.Bm, pr->B, pr->T, pr->N, p.b_sb, p.b_st, e) &&
+               pieces16(p.Cm, pr->B, pr->T, pr->N, p.c_sb, p.c_st, e);
+    // states cost time one by one, so the sizes between powers of two are worth their instances
+    if (pr->N <= 8) return launch_prompt<E, 8>(pr, p, workspace, s);
+    if (pr->N <= 16) return launch_prompt<E, 16>(pr, p, workspace, s);
+    if (pr->N <= 24) return launch_prompt<E, 24>(pr, p, workspace, s);
+    if (pr->N <= 32) return launch_prompt<E, 32>(pr, p, workspace, s);
+    if (pr->N <= 48) return launch_prompt<E, 48>(pr, p, workspace, s);
+    if (pr->N <= 64) return launch_prompt<E, 64>(pr, p, workspace, s);
+    if (pr->N <= 96) return launch_prompt<E, 96>(pr, p, workspace, s);
+    return launch_prompt<E, 128>(pr, p, workspace, s);
 }
 
 }  // namespace

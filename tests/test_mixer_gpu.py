@@ -138,7 +138,8 @@ def check_scan(y, h, i):
 
 SCAN_SIZES = [(1, 1, 1, 1, 1), (2, 3, 8, 16, 1), (3, 17, 66, 13, 2), (2, 65, 64, 24, 1), (2, 130, 40, 64, 4),
               (1, 200, 33, 100, 3), (4, 64, 128, 16, 2), (2, 127, 96, 8, 1), (1, 70, 16, 128, 1),
-              (2, 40, 130, 4, 1), (1, 31, 264, 16, 1), (2, 33, 48, 1, 1), (1, 20, 70, 2, 2)]
+              (2, 40, 130, 4, 1), (1, 31, 264, 16, 1), (2, 33, 48, 1, 1), (1, 20, 70, 2, 2),
+              (2, 75, 64, 24, 2), (1, 100, 72, 48, 1), (1, 70, 64, 96, 1), (2, 66, 64, 17, 1), (1, 90, 40, 40, 1)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
