@@ -358,9 +358,19 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
         } else {
             const E *from = src + b * sb + t0 * st + static_cast<int64_t>(g) * p.N;
             E *to = reinterpret_cast<E *>(dst);
-            for (int i = tid; i < rows * NP; i += kThreads) {
-                const int t = i / NP, q = i % NP;
-                if (q < p.N) to[i] = from[t * st + q];
+            // eight loads at a time in flight
+            for (int i0 = tid; i0 < rows * NP; i0 += 8 * kThreads) {
+                E v[8];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    const int i = i0 + m * kThreads, t = i / NP, q = i % NP;
+                    if (t < rows && q < p.N) v[m] = from[t * st + q];
+                }
+#pragma unroll
+                for (int m = 0; m < 8; ++m) {
+                    const int i = i0 + m * kThreads;
+                    if (i / NP < rows && i % NP < p.N) to[i] = v[m];
+                }
             }
         }
     };
