@@ -55,14 +55,13 @@ def _tokens(t, name, shape, dtype, index):
 
 
 def _dense(t, name, shape, dtype, index):
-    """Address of a contiguous tensor, or None."""
+    """A contiguous tensor, or None."""
     if t is None:
-        return None
+        return
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {tuple(shape)} on cuda:{index}")
-    return t.data_ptr()
 
 
 def _x(x, axes="[B,T,C]"):
@@ -107,6 +106,41 @@ def _on_stream(f):
     return call
 
 
+def _form(t):
+    """What a call checks of a tensor: two tensors of one form pass or fail alike."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+# The checked problem of each form of call (as the host entry keeps its plans): checking a
+# scan's eleven tensors again would cost a single token 5 us.
+_plans: dict = {}
+
+
+def _keep(key, plan):
+    if len(_plans) >= 512:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _conv_plan(x, weight, bias, state, lengths, act, out, final_state):
+    """(problem, shape of the window state, device index), or the refusal."""
+    shape, dtype, index = _x(x)
+    B, T, C = shape
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C,W]")
+    W = weight.shape[1]
+    if not 2 <= W <= 4:
+        raise GdnError(GDN_ERR_UNSUPPORTED, "gdn_conv_fwd")
+    window = (B, W - 1, C)
+    p = ConvProblem(B, T, C, W, DTYPES[dtype], _act(act), *_tokens(x, "x", shape, dtype, index))
+    for t, name, form, kind in ((weight, "weight", (C, W), torch.float32), (bias, "bias", (C,), torch.float32),
+                                (lengths, "lengths", (B,), torch.int32), (state, "state", window, dtype),
+                                (out, "out", shape, dtype), (final_state, "final_state", window, dtype)):
+        _dense(t, name, form, kind, index)
+    return ctypes.byref(p), window, index
+
+
 @_on_stream
 def conv_fwd(x, weight, bias=None, state=None, lengths=None, act: str = "silu",
              output_final_state: bool = True, out=None, final_state=None):
@@ -120,28 +154,19 @@ def conv_fwd(x, weight, bias=None, state=None, lengths=None, act: str = "silu",
     token (None: zeros). The returned state holds the last W-1 inputs up to the
     last valid token; ``final_state=state`` updates it in place. ``act``: "silu",
     "none" or "sigmoid". ``out`` [B,T,C] may be passed to reuse a buffer."""
-    shape, dtype, index = _x(x)
-    B, T, C = shape
-    if weight.dim() != 2:
-        raise ValueError("weight must be [C,W]")
-    W = weight.shape[1]
-    if not 2 <= W <= 4:
-        raise GdnError(GDN_ERR_UNSUPPORTED, "gdn_conv_fwd")
-    window = (B, W - 1, C)
-    p = ConvProblem(B, T, C, W, DTYPES[dtype], _act(act), *_tokens(x, "x", shape, dtype, index))
-    w = _dense(weight, "weight", (C, W), torch.float32, index)
-    bi = _dense(bias, "bias", (C,), torch.float32, index)
-    n = _dense(lengths, "lengths", (B,), torch.int32, index)
-    si = _dense(state, "state", window, dtype, index)
+    key = (x.shape, x.stride(), x.dtype, x.get_device(), weight.shape, weight.stride(), weight.dtype,
+           weight.get_device(), _form(bias), _form(state), _form(lengths), _form(out), _form(final_state),
+           act)
+    p, window, index = _plans.get(key) or _keep(key, _conv_plan(
+        x, weight, bias, state, lengths, act, out, final_state))
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if not output_final_state:
         final_state = None
     elif final_state is None:
-        final_state = torch.empty(window, dtype=dtype, device=x.device)
-    _call(lib().gdn_conv_fwd, "gdn_conv_fwd", index, ctypes.byref(p), x.data_ptr(), w, bi, si, n,
-          _dense(out, "out", shape, dtype, index),
-          _dense(final_state, "final_state", window, dtype, index))
+        final_state = torch.empty(window, dtype=x.dtype, device=x.device)
+    _call(lib().gdn_conv_fwd, "gdn_conv_fwd", index, p, x.data_ptr(), weight.data_ptr(), _ptr(bias),
+          _ptr(state), _ptr(lengths), out.data_ptr(), _ptr(final_state))
     return out, final_state
 
 
@@ -169,16 +194,6 @@ def scan_workspace_bytes(B: int, T: int, D: int, N: int, G: int = 1, dtype=torch
 def _refusal(p) -> int:
     """The status of a problem that the library refuses before any pointer."""
     return lib().gdn_scan_fwd(ctypes.byref(p), *[None] * 13, 0, None)
-
-
-def _form(t):
-    """What a call checks of a tensor: two tensors of one form pass or fail alike."""
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
-
-
-# The checked problem of each form of call (as the host entry keeps its plans): its many
-# tensors cost 6 us to check again for a single token.
-_scan_plans: dict = {}
 
 
 def _scan_plan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, lengths, out, final_state):
@@ -222,13 +237,8 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = F
            A.shape, A.stride(), A.dtype, A.get_device(), B.shape, B.stride(), B.dtype, B.get_device(),
            C.shape, C.stride(), C.dtype, C.get_device(), _form(D), _form(z), _form(dt_bias), _form(h0),
            _form(lengths), _form(out), _form(final_state), dt_softplus)
-    plan = _scan_plans.get(key)
-    if plan is None:
-        if len(_scan_plans) >= 256:
-            _scan_plans.clear()
-        plan = _scan_plans[key] = _scan_plan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, lengths, out,
-                                             final_state)
-    p, need, state, index = plan
+    p, need, state, index = _plans.get(key) or _keep(key, _scan_plan(
+        x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, lengths, out, final_state))
     if need:    # held until the call: freed before, out could be allocated in its place
         workspace = _workspace(workspace, need, x.device)
     if out is None:
@@ -253,6 +263,19 @@ def scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softplus: 
                                 out, state if state_out is None else state_out)
 
 
+def _norm_plan(x, groups, weight, bias, eps, act, gate, lengths, out):
+    """(problem, device index), or the refusal."""
+    shape, dtype, index = _x(x)
+    B, T, C = shape
+    p = GroupNormProblem(B, T, C, groups, DTYPES[dtype], _act(act), eps, 0,
+                         *_tokens(x, "x", shape, dtype, index),
+                         *((0, 0) if gate is None else _tokens(gate, "gate", shape, dtype, index)))
+    for t, name, form, kind in ((weight, "weight", (C,), torch.float32), (bias, "bias", (C,), torch.float32),
+                                (lengths, "lengths", (B,), torch.int32), (out, "out", shape, dtype)):
+        _dense(t, name, form, kind, index)
+    return ctypes.byref(p), index
+
+
 @_on_stream
 def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: str = "none",
                gate=None, lengths=None, out=None):
@@ -265,16 +288,12 @@ def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: s
     x and gate [B,T,C] float32 or bfloat16, strided; weight, bias [C] float32 or
     None. For the norm of every token on its own pass x as [tokens,1,C]. ``out``
     may be a contiguous x itself (in place)."""
-    shape, dtype, index = _x(x)
-    B, T, C = shape
-    p = GroupNormProblem(B, T, C, int(groups), DTYPES[dtype], _act(act), float(eps), 0,
-                         *_tokens(x, "x", shape, dtype, index),
-                         *((0, 0) if gate is None else _tokens(gate, "gate", shape, dtype, index)))
-    w = _dense(weight, "weight", (C,), torch.float32, index)
-    bi = _dense(bias, "bias", (C,), torch.float32, index)
-    n = _dense(lengths, "lengths", (B,), torch.int32, index)
+    groups, eps = int(groups), float(eps)
+    key = (x.shape, x.stride(), x.dtype, x.get_device(), groups, _form(weight), _form(bias), eps, act,
+           _form(gate), _form(lengths), _form(out))
+    p, index = _plans.get(key) or _keep(key, _norm_plan(x, groups, weight, bias, eps, act, gate, lengths, out))
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
-    _call(lib().gdn_group_norm, "gdn_group_norm", index, ctypes.byref(p), x.data_ptr(), w, bi,
-          _ptr(gate), n, _dense(out, "out", shape, dtype, index))
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _call(lib().gdn_group_norm, "gdn_group_norm", index, p, x.data_ptr(), _ptr(weight), _ptr(bias),
+          _ptr(gate), _ptr(lengths), out.data_ptr())
     return out
