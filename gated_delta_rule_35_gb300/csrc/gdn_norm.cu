@@ -387,42 +387,40 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
     }
     __syncthreads();
     // Merge the token rows, then the channels, to groups: the weighted means first, then the
-    // squares about the group's mean. Threads take a channel's rows (several threads to
-    // a channel where they suffice), warps the groups.
+    // squares about the group's mean. Threads take the channels, warps the groups; a channel's
+    // rows shared out over idle threads cost 23 us for 19 (B3 T2048 C330 bf16).
     const int tokens = t_end - t_begin, more = tokens % RP;
     const float total = static_cast<float>(tokens) * cg, low = static_cast<float>(tokens / RP), high = low + 1.f;
-    const int CT = min(SC, kThreads), RL = kThreads / CT, rl = threadIdx.x / CT;
     auto over_channels = [&](auto keep) {
         __syncthreads();
         for (int g = threadIdx.x / 32; g < ng; g += kThreads / 32) {
             float sum = 0.f;
-            for (int r = 0; r < RL; ++r)
 #pragma unroll 4
-                for (int i = threadIdx.x % 32; i < cg; i += 32) sum += columns[r * SC + g * cg + i];
+            for (int i = threadIdx.x % 32; i < cg; i += 32) sum += columns[g * cg + i];
             sum = warp_sum(sum);
             if (threadIdx.x % 32 == 0) keep(g, sum);
         }
         __syncthreads();
     };
-    for (int col = threadIdx.x % CT; rl < RL && col < SC; col += CT) {
+    for (int col = threadIdx.x; col < SC; col += kThreads) {
         float sum = 0.f;
 #pragma unroll 8
-        for (int r = rl; r < RP; r += RL) sum = fmaf(r < more ? high : low, means[r * SC + col], sum);
-        columns[rl * SC + col] = sum;
+        for (int r = 0; r < RP; ++r) sum = fmaf(r < more ? high : low, means[r * SC + col], sum);
+        columns[col] = sum;
     }
     over_channels([&](int g, float sum) {
         part[0][g] = total;
         part[1][g] = total > 0.f ? sum / total : 0.f;
     });
-    for (int col = threadIdx.x % CT; rl < RL && col < SC; col += CT) {
+    for (int col = threadIdx.x; col < SC; col += kThreads) {
         const float m = part[1][col / cg];
         float sum = 0.f;
 #pragma unroll 8
-        for (int r = rl; r < RP; r += RL) {
+        for (int r = 0; r < RP; ++r) {
             const float d = means[r * SC + col] - m;
             sum += fmaf((r < more ? high : low) * d, d, squares[r * SC + col]);
         }
-        columns[rl * SC + col] = sum;
+        columns[col] = sum;
     }
     over_channels([&](int g, float sum) { part[2][g] = sum; });
     merge_cluster(part, ng, K, p.eps, g_mean, g_rstd);
