@@ -236,7 +236,7 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = F
     key = (x.shape, x.stride(), x.dtype, x.get_device(), dt.shape, dt.stride(), dt.dtype, dt.get_device(),
            A.shape, A.stride(), A.dtype, A.get_device(), B.shape, B.stride(), B.dtype, B.get_device(),
            C.shape, C.stride(), C.dtype, C.get_device(), _form(D), _form(z), _form(dt_bias), _form(h0),
-           _form(lengths), _form(out), _form(final_state), dt_softplus)
+           _form(lengths), _form(out), _form(final_state), bool(dt_softplus))
     p, need, state, index = _plans.get(key) or _keep(key, _scan_plan(
         x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, lengths, out, final_state))
     if need:    # held until the call: freed before, out could be allocated in its place
