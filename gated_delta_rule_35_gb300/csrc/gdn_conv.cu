@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) gdn_conv_kernel(const ConvParams<E> 
     const int i = blockIdx.x * kThreads + threadIdx.x;
     const int c = i % cv * V, t0 = i / cv * p.run;     // runs of a piece lie cv threads apart
     const int64_t b = blockIdx.y;
-    if (t0 >= max(p.T, 1)) return;
+    if (t0 >= p.T) return;
     const int n = valid_tokens(p.lengths, b, p.T);
     if (t0 < n) {
         // in pairs of channels: one instruction works on both
@@ -367,12 +367,19 @@ GDN_API gdn_status gdn_conv_fwd(const gdn_conv_problem *p, const void *x, const 
         sy.meets(so) || so.meets(sx) || so.meets(sw) || so.meets(sbias) || so.meets(sl) ||
         (state_in != state_out && so.meets(si)))
         return GDN_ERR_INVALID_ARG;
-    if (empty && (!state_out || state_in == state_out)) return GDN_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t err =
-        p->dtype == GDN_BF16
-            ? gdn::dispatch<__nv_bfloat16>(p, x, weight, bias, state_in, lengths, y, state_out, s)
-            : gdn::dispatch<float>(p, x, weight, bias, state_in, lengths, y, state_out, s);
+    cudaError_t err = cudaSuccess;
+    if (empty) {             // x, weight and y may be NULL
+        const size_t bytes = row * (p->W - 1) * p->B;
+        if (state_out && state_in && state_in != state_out)
+            err = cudaMemcpyAsync(state_out, state_in, bytes, cudaMemcpyDeviceToDevice, s);
+        else if (state_out && !state_in)
+            err = cudaMemsetAsync(state_out, 0, bytes, s);
+        return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
+    err = p->dtype == GDN_BF16
+              ? gdn::dispatch<__nv_bfloat16>(p, x, weight, bias, state_in, lengths, y, state_out, s)
+              : gdn::dispatch<float>(p, x, weight, bias, state_in, lengths, y, state_out, s);
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -394,7 +394,7 @@ typedef enum {
  *  - x [B,T,C] strided, y [B,T,C], state_in / state_out [B,W-1,C] in `dtype`;
  *    weight [C,W], bias [C] (or NULL) fp32.
  *  - One call serves prompts and single tokens (T = 1, state in place). T = 0
- *    copies the state. */
+ *    copies the state (x, weight and y may be NULL then). */
 typedef struct {
     int32_t B, T, C, W;
     int32_t dtype;   /* gdn_dtype */
@@ -420,7 +420,7 @@ GDN_API gdn_status gdn_conv_fwd(const gdn_conv_problem *p, const void *x, const 
  *    (no gate). A [D,N], skip (the D of the formula) [D] or NULL, dt_bias [D] or
  *    NULL: fp32 and finite. y [B,T,D] in `dtype`; h0, h_final [B,D,N] fp32.
  *  - One call serves prompts and single tokens (T = 1, h0 and h_final equal). T
- *    = 0 copies the state.
+ *    = 0 copies the state (the other pointers may be NULL then).
  *  - workspace: gdn_scan_workspace_bytes(p) bytes of scratch, 0 for problems that
  *    need none (then it may be NULL). Long sequences of few channels are cut
  *    into segments whose states pass through it. Two calls that may overlap on

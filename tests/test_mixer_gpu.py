@@ -1,12 +1,14 @@
 """The short convolution, the selective scan and the group norm on the GPU against
 their fp64 forms, elementwise within the bounds of mixer_bounds (and, for the scan,
 the bound that the fp64 form carries along the recurrence)."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_35_gb300 as gdn
-from gated_delta_rule_35_gb300 import native
+from gated_delta_rule_35_gb300 import mixer, native
 from oracle import mixer as ref
 from oracle import recurrence
 from tests import mixer_bounds as mb
@@ -513,6 +515,20 @@ def test_no_tokens_pass_the_state_through():
     assert torch.equal(gdn.scan_fwd(x, x, A, bc, bc, h0=h0)[1], h0)
     assert (gdn.scan_fwd(x, x, A, bc, bc)[1] == 0).all()
     assert gdn.group_norm(x, 4).shape == (2, 0, 16)
+
+
+@pytest.mark.parametrize("W,dtype", [(2, BF16), (4, BF16), (3, torch.float32)])
+def test_no_tokens_need_no_weight(W, dtype):
+    """The C entry's T = 0 copies the window state, with nothing else passed."""
+    p = mixer.ConvProblem(3, 0, 24, W, native.DTYPES[dtype], 1, 0, 0)
+    st = torch.randn(3, W - 1, 24, device="cuda").to(dtype)
+    out = torch.full_like(st, 7)
+    s = torch.cuda.current_stream().cuda_stream
+    for given, want in ((st, st), (None, torch.zeros_like(st))):
+        assert native.lib().gdn_conv_fwd(ctypes.byref(p), None, None, None, given.data_ptr() if given is not None
+                                         else None, None, None, out.data_ptr(), s) == native.GDN_OK
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
 
 
 def test_wrapper_refusals():
