@@ -298,8 +298,16 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
             F2 e[SP2];
             load_states(p.seg_h + seg_at(i) * p.N, e, 1.f);
             const float sum = p.seg_dt[seg_at(i)];
+            // exp(A sum) as a square: where Delta A > 0 it may pass the range though its
+            // product with a small state does not (nor 0 times it). A normal number times
+            // 2^254 is beyond the range anyway.
 #pragma unroll
-            for (int q = 0; q < SP2; ++q) h[q] = fma2(decay(pack2(sum, sum), A2[q]), h[q], e[q]);
+            for (int q = 0; q < SP2; ++q) {
+                float lo, hi;
+                unpack2(mul2(pack2(sum, sum), A2[q]), lo, hi);
+                const F2 root = pack2(exp2_ftz(0.5f * fminf(lo, 254.f)), exp2_ftz(0.5f * fminf(hi, 254.f)));
+                h[q] = fma2(mul2(h[q], root), root, e[q]);
+            }
         }
     }
 

@@ -182,6 +182,20 @@ def test_scan_long_sequences_of_few_channels(size, dtype):
             assert torch.equal(again[b, :nb], y[b, :nb])
 
 
+def test_scan_grows_across_segments():
+    """Delta A > 0 over a whole segment: its factor alone, e^128, is beyond fp32's range, the
+    states that it multiplies (0 and 1e-30) stay within."""
+    i = scan_inputs(1, 1024, 16, 4, 1, F32, 350, gate=False, soft=False)
+    assert gdn.scan_workspace_bytes(1, 1024, 16, 4, 1, F32) >= 16 * 16 * 4 * 4    # 16 segments
+    i["dt"].zero_()
+    i["dt"][:, 128:192] = 2
+    i["x"][:, :900] = 0
+    i["dt"][:, 900:] = 0.01
+    i["A"] = torch.tensor([1.0, 0.75, 0.5, -1.0]).repeat(16, 1).cuda()
+    i["h0"] = 1e-30 * (torch.arange(16) % 2).float()[None, :, None].repeat(1, 1, 4).cuda()
+    check_scan(*gdn.scan_fwd(**i), i)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_scan_steps_continue_a_prompt(dtype):
     i = scan_inputs(3, 12, 40, 16, 2, dtype, 400)
