@@ -267,7 +267,10 @@ gdn_status check(const gdn_conv_problem *p) {
     if (p->act != GDN_ACT_NONE && p->act != GDN_ACT_SILU && p->act != GDN_ACT_SIGMOID)
         return GDN_ERR_INVALID_ARG;
     if (p->W < 2 || p->W > 4) return GDN_ERR_UNSUPPORTED;
-    if (p->B > 65535 || static_cast<int64_t>(p->C) * p->T > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    // 2^30: indexes of a few blocks past the end stay in 32 bits
+    if (p->B > 65535 || p->C > (1 << 30) || p->T > (1 << 30) ||
+        static_cast<int64_t>(p->C) * p->T > (1 << 30))
+        return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -587,7 +587,8 @@ gdn_status check(const gdn_group_norm_problem *p) {
     if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
     if (p->act != GDN_ACT_NONE && p->act != GDN_ACT_SILU && p->act != GDN_ACT_SIGMOID)
         return GDN_ERR_INVALID_ARG;
-    if (p->B > (1 << 26) || p->G > 65535) return GDN_ERR_UNSUPPORTED;
+    // 2^30: indexes of a block past the end stay in 32 bits
+    if (p->B > (1 << 26) || p->G > 65535 || p->C > (1 << 30) || p->T > (1 << 30)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

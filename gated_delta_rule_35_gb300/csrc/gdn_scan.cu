@@ -587,7 +587,8 @@ gdn_status check(const gdn_scan_problem *p) {
     for (int64_t s : {p->x_stride_b, p->x_stride_t, p->dt_stride_b, p->dt_stride_t, p->z_stride_b,
                       p->z_stride_t, p->b_stride_b, p->b_stride_t, p->c_stride_b, p->c_stride_t})
         if (s < 0) return GDN_ERR_INVALID_ARG;
-    if (p->N > 128 || p->B > 65535 || p->D > (1 << 24)) return GDN_ERR_UNSUPPORTED;
+    // 2^30: token indexes of a tile past the end stay in 32 bits
+    if (p->N > 128 || p->B > 65535 || p->D > (1 << 24) || p->T > (1 << 30)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

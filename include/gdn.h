@@ -390,7 +390,7 @@ typedef enum {
  * where x at t < 0 is the window state: state_in[b, W - 1 + t, c], the last W - 1
  * inputs before the first token. state_out receives the last W - 1 inputs up to
  * the last valid token (with fewer than W - 1 new tokens the older ones move up).
- *  - W in {2, 3, 4}, B <= 65535, C T < 2^31 (else GDN_ERR_UNSUPPORTED).
+ *  - W in {2, 3, 4}, B <= 65535, C, T and C T <= 2^30 (else GDN_ERR_UNSUPPORTED).
  *  - x [B,T,C] strided, y [B,T,C], state_in / state_out [B,W-1,C] in `dtype`;
  *    weight [C,W], bias [C] (or NULL) fp32.
  *  - One call serves prompts and single tokens (T = 1, state in place). T = 0
@@ -414,8 +414,8 @@ GDN_API gdn_status gdn_conv_fwd(const gdn_conv_problem *p, const void *x, const 
  *   y[b,t,d] = (sum_n C[b,t,g,n] h[d,n] + D[d] x[b,t,d]) * silu(z[b,t,d])
  *
  * with g = d / (D / G) the channel's group of B and C rows.
- *  - D a multiple of G (else GDN_ERR_INVALID_ARG); N in 1..128, B <= 65535, D <= 2^24
- *    (else GDN_ERR_UNSUPPORTED).
+ *  - D a multiple of G (else GDN_ERR_INVALID_ARG); N in 1..128, B <= 65535, D <= 2^24,
+ *    T <= 2^30 (else GDN_ERR_UNSUPPORTED).
  *  - x, dt, z [B,T,D] and Bm, Cm [B,T,G,N] in `dtype`, each strided; z may be NULL
  *    (no gate). A [D,N], skip (the D of the formula) [D] or NULL, dt_bias [D] or
  *    NULL: fp32 and finite. y [B,T,D] in `dtype`; h0, h_final [B,D,N] fp32.
@@ -454,8 +454,8 @@ GDN_API gdn_status gdn_scan_fwd(const gdn_scan_problem *p, const void *x, const 
  *   y = act(v)            without a gate
  *   y = v * act(gate)     with one
  *
- *  - C a multiple of G (else GDN_ERR_INVALID_ARG); B <= 2^26, G <= 65535 (else
- *    GDN_ERR_UNSUPPORTED). x, gate (or NULL) [B,T,C] strided,
+ *  - C a multiple of G (else GDN_ERR_INVALID_ARG); B <= 2^26, G <= 65535, C and T
+ *    <= 2^30 (else GDN_ERR_UNSUPPORTED). x, gate (or NULL) [B,T,C] strided,
  *    y [B,T,C] in `dtype`; weight, bias [C] fp32 or NULL (1 and 0); eps >= 0.
  *  - y == x with x contiguous normalises in place. */
 typedef struct {

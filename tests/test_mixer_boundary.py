@@ -124,7 +124,13 @@ def test_scan_needs_its_workspace():
 
 
 @pytest.mark.parametrize("call,kw", [(conv, dict(C=1 << 20, T=1 << 12)), (scan, dict(D=(1 << 24) + 16)),
-                                     (norm, dict(B=(1 << 26) + 1)), (norm, dict(C=65536, G=65536))])
+                                     (norm, dict(B=(1 << 26) + 1)), (norm, dict(C=65536, G=65536)),
+                                     # one token or channel with 32-bit indexes at their end
+                                     (conv, dict(C=(1 << 31) - 1, T=1)), (conv, dict(C=1, T=(1 << 31) - 1)),
+                                     (conv, dict(C=(1 << 31) - 1, T=0)), (conv, dict(C=(1 << 15) + 1, T=1 << 15)),
+                                     (scan, dict(D=1, N=1, T=(1 << 31) - 1)),
+                                     (norm, dict(C=(1 << 31) - 1, G=1, T=1)),
+                                     (norm, dict(C=1, G=1, T=(1 << 31) - 1))])
 def test_sizes_beyond_the_grids(call, kw):
     assert call(**kw) == UNSUPPORTED
 
