@@ -4,6 +4,7 @@
 // traffic) and gdn_scan_kernel for prompts (bound by arithmetic: N exponentials and 5 N
 // multiply-adds per token and channel against 4 values moved).
 #include "mixer.cuh"
+#include "sm100_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -248,6 +249,12 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
     if (s > 0 && t_begin >= n) return;
     const int tokens = t_end - t_begin, tiles = (tokens + TT - 1) / TT;
 
+    // The second pass begins once all of the first one's blocks have begun, and waits for
+    // their end before it reads what they leave: its first tile is there by then (54 us for 58,
+    // B5 T777 D1000 N24 fp32). Its first segments' blocks always wait, so it ends after the
+    // first pass.
+    if (PARTIAL) ptx::griddep_launch_dependents();
+
     const int tid = threadIdx.x, c = tid / 2, j = tid % 2;
     const bool live = c < nc;
     const int d = d0 + (live ? c : 0);
@@ -282,34 +289,6 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
     load_states(p.A + static_cast<int64_t>(d) * p.N, A2, kLog2e);
 #pragma unroll
     for (int q = 0; q < SP2; ++q) h[q] = 0;
-    if (p.segs == 1) {
-        if (p.h0) load_states(p.h0 + state, h, 1.f);
-    } else if (PARTIAL) {
-        // h0 starts the first segment; a copy serves the second pass, which may write
-        // h_final in h0's place
-        if (s == 0) {
-            if (p.h0) load_states(p.h0 + state, h, 1.f);
-            store_states(p.seg_h + seg_at(p.segs - 1) * p.N);
-        }
-    } else if (s == 0) {
-        load_states(p.seg_h + seg_at(p.segs - 1) * p.N, h, 1.f);
-    } else {
-        for (int i = 0; i < s; ++i) {
-            F2 e[SP2];
-            load_states(p.seg_h + seg_at(i) * p.N, e, 1.f);
-            const float sum = p.seg_dt[seg_at(i)];
-            // exp(A sum) as a square: where Delta A > 0 it may pass the range though its
-            // product with a small state does not (nor 0 times it). A normal number times
-            // 2^254 is beyond the range anyway.
-#pragma unroll
-            for (int q = 0; q < SP2; ++q) {
-                float lo, hi;
-                unpack2(mul2(pack2(sum, sum), A2[q]), lo, hi);
-                const F2 root = pack2(exp2_ftz(0.5f * fminf(lo, 254.f)), exp2_ftz(0.5f * fminf(hi, 254.f)));
-                h[q] = fma2(mul2(h[q], root), root, e[q]);
-            }
-        }
-    }
 
     // ------------------------------------------------------------------------- copy
     // Row by row: this thread's piece of every kThreads / PR-th row, of the next tile.
@@ -551,6 +530,37 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
         __syncthreads();
     }
     fetch(0);
+    // the state, while the first tile arrives
+    if (p.segs == 1) {
+        if (p.h0) load_states(p.h0 + state, h, 1.f);
+    } else if (PARTIAL) {
+        // h0 starts the first segment; a copy serves the second pass, which may write
+        // h_final in h0's place
+        if (s == 0) {
+            if (p.h0) load_states(p.h0 + state, h, 1.f);
+            store_states(p.seg_h + seg_at(p.segs - 1) * p.N);
+        }
+    } else if (s == 0) {
+        ptx::griddep_wait();
+        load_states(p.seg_h + seg_at(p.segs - 1) * p.N, h, 1.f);
+    } else {
+        ptx::griddep_wait();
+        for (int i = 0; i < s; ++i) {
+            F2 e[SP2];
+            load_states(p.seg_h + seg_at(i) * p.N, e, 1.f);
+            const float sum = p.seg_dt[seg_at(i)];
+            // exp(A sum) as a square: where Delta A > 0 it may pass the range though its
+            // product with a small state does not (nor 0 times it). A normal number times
+            // 2^254 is beyond the range anyway.
+#pragma unroll
+            for (int q = 0; q < SP2; ++q) {
+                float lo, hi;
+                unpack2(mul2(pack2(sum, sum), A2[q]), lo, hi);
+                const F2 root = pack2(exp2_ftz(0.5f * fminf(lo, 254.f)), exp2_ftz(0.5f * fminf(hi, 254.f)));
+                h[q] = fma2(mul2(h[q], root), root, e[q]);
+            }
+        }
+    }
     for (int k = 0; k < tiles; ++k) {
         const int rows = min(TT, tokens - k * TT);
         copy_wait<0>();
@@ -616,14 +626,24 @@ size_t workspace_need(const gdn_scan_problem *p) {
     return n == 1 ? 0 : align_up(rows * p->N * 4) + align_up(rows * 4);
 }
 
+// second: behind the first pass on the same stream, which it waits for by itself.
 template <typename E>
 cudaError_t launch_blocks(void (*kernel)(ScanParams<E>), dim3 grid, int bytes, const ScanParams<E> &p,
-                          cudaStream_t s) {
+                          bool second, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, bytes, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = second ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <typename E, int NP>
@@ -639,11 +659,11 @@ cudaError_t launch_prompt(const gdn_scan_problem *pr, ScanParams<E> &p, void *wo
             static_cast<char *>(workspace) +
             align_up(static_cast<size_t>(pr->B) * p.segs * pr->D * pr->N * 4));
         const cudaError_t e = launch_blocks(gdn_scan_kernel<E, NP, false, true>,
-                                            dim3(grid.x, grid.y, p.segs - 1), S::bytes, p, s);
+                                            dim3(grid.x, grid.y, p.segs - 1), S::bytes, p, false, s);
         if (e != cudaSuccess) return e;
     }
     return launch_blocks(p.z ? gdn_scan_kernel<E, NP, true, false> : gdn_scan_kernel<E, NP, false, false>,
-                         grid, S::bytes, p, s);
+                         grid, S::bytes, p, p.segs > 1, s);
 }
 
 template <typename E, int NP>
