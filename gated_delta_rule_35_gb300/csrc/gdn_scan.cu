@@ -3,6 +3,8 @@
 // Two kernels by length: gdn_scan_step_kernel for a few tokens (bound by the state's
 // traffic) and gdn_scan_kernel for prompts (bound by arithmetic: N exponentials and 5 N
 // multiply-adds per token and channel against 4 values moved).
+#include <algorithm>
+
 #include "mixer.cuh"
 #include "sm100_ptx.cuh"
 
@@ -21,6 +23,7 @@ struct ScanParams {
     float *h_final;
     int64_t x_sb, x_st, dt_sb, dt_st, z_sb, z_st, b_sb, b_st, c_sb, c_st;
     int B, T, D, N, G, softplus;
+    int turns;           // few tokens: sets of sequences to a block
     int rows16;          // B and C rows are whole 16-byte pieces
     int pieces;          // so are those of x, dt, z and y, and each block's part of them
     // Segments of seg tokens each; with more than one, the state at the end of a
@@ -69,21 +72,26 @@ __device__ __forceinline__ float4 widen4(const __nv_bfloat16 *p, bool in) {
 // ----------------------------------------------------------------- a few tokens
 //
 // Bound by the states' traffic: each is read and written once. L = NP / 4 lanes share a
-// channel, four states to a lane, and a thread advances NB sequences, so that their
-// states' loads are in flight together and A is read once for all of them. Of a channel's
-// L lanes, lane m % L takes Delta, the gate and the output of sequence m.
+// channel, four states to a lane. A thread advances NB sequences at a time, whose states'
+// loads are in flight together, and p.turns such sets one after the other: A is read
+// once for all of them, and a set's states and tokens arrive while the one before is
+// worked on. Of a channel's L lanes, lane m % L takes Delta, the gate and the output of
+// sequence m. One token of 256 sequences, 4096 channels, N = 16, bf16: 33 us, 4.3 TB/s (one set
+// to a block, 12 blocks to an SM: 40; six, eight and ten blocks of several sets: 35, 33, 48);
+// N = 64 in fp32 101 us, 5.5 TB/s (134; 107, 162, -).
 constexpr int kBatch = 4;
+constexpr int kStepBlocks = 7;      // to an SM, by registers
 
 template <typename E, int NP, int NB>
-__global__ void __launch_bounds__(kThreads, NB > 1 ? 12 : 1) gdn_scan_step_kernel(const ScanParams<E> p) {
+__global__ void __launch_bounds__(kThreads, NB > 1 ? kStepBlocks : 1) gdn_scan_step_kernel(const ScanParams<E> p) {
     constexpr int L = NP / 4, channels = kThreads / L, OWN = (NB + L - 1) / L;
-    __shared__ __align__(16) float bc[NB][2][NP];      // a token's B and C rows
+    constexpr int BC = NB * 2 * NP, BCT = (BC + kThreads - 1) / kThreads;
+    __shared__ __align__(16) float bc[2][NB][2][NP];   // a token's B and C rows, of two tokens in turn
     const int per = p.D / p.G, blocks = (per + channels - 1) / channels;
     const int g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * channels;
     const int tid = threadIdx.x, c = tid / L, j = tid % L, n0 = j * 4;
     const bool live = c0 + c < per;
     const int d = g * per + c0 + (live ? c : 0);
-    const int b0 = blockIdx.y * NB;
     const bool quads = p.N % 4 == 0;   // rows of states are whole 16-byte pieces
     auto quad = [&](const float *row, float (&f)[4]) {
 #pragma unroll
@@ -99,84 +107,118 @@ __global__ void __launch_bounds__(kThreads, NB > 1 ? 12 : 1) gdn_scan_step_kerne
                 if (n0 + k < p.N) f[k] = row[n0 + k];
         }
     };
-    auto state = [&](int m) { return (static_cast<int64_t>(b0 + m) * p.D + d) * p.N; };
-    float A2[4], h[NB][4];
+    const int64_t state = static_cast<int64_t>(p.D) * p.N, row = static_cast<int64_t>(d) * p.N;
+    const int b_first = blockIdx.y * p.turns * NB, b_end = min(p.B, b_first + p.turns * NB);
+    float hn[NB][4];
+    auto load_states = [&](int b0) {
 #pragma unroll
-    for (int m = 0; m < NB; ++m) {
+        for (int m = 0; m < NB; ++m) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h[m][k] = 0.f;
-        if (p.h0 && b0 + m < p.B) quad(p.h0 + state(m), h[m]);
-    }
-    quad(p.A + static_cast<int64_t>(d) * p.N, A2);
+            for (int k = 0; k < 4; ++k) hn[m][k] = 0.f;
+            if (p.h0 && b0 + m < b_end) quad(p.h0 + (b0 + m) * state + row, hn[m]);
+        }
+    };
+    // A token's rows: B and C of all NB sequences over the block, x, dt and z of this lane's.
+    E rbc[BCT], rx[OWN], rdt[OWN], rz[OWN];
+    auto load_token = [&](int b0, int t) {
+#pragma unroll
+        for (int i = 0; i < BCT; ++i) {
+            const int at = i * kThreads + tid, q = at % NP;
+            const int64_t b = b0 + at / (2 * NP);
+            rbc[i] = from_f32<E>(0.f);    // behind a sequence's end: B = C = 0, Delta = 0
+            if (at < BC && b < b_end && q < p.N && t < valid_tokens(p.lengths, b, p.T)) {
+                const int64_t of = static_cast<int64_t>(g) * p.N + q;
+                rbc[i] = at / NP % 2 ? p.Cm[b * p.c_sb + t * p.c_st + of] : p.Bm[b * p.b_sb + t * p.b_st + of];
+            }
+        }
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            const int64_t b = b0 + o * L + j;
+            rx[o] = rdt[o] = rz[o] = from_f32<E>(0.f);
+            if (o * L + j < NB && b < b_end && t < valid_tokens(p.lengths, b, p.T)) {
+                rx[o] = p.x[b * p.x_sb + t * p.x_st + d];
+                rdt[o] = p.dt[b * p.dt_sb + t * p.dt_st + d];
+                if (p.z) rz[o] = p.z[b * p.z_sb + t * p.z_st + d];
+            }
+        }
+    };
+    load_states(b_first);
+    load_token(b_first, 0);
+    float A2[4];
+    quad(p.A + row, A2);
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.skip ? p.skip[d] : 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) A2[k] *= kLog2e;
 
-    for (int t = 0; t < p.T; ++t) {
-        if (t > 0) __syncthreads();
-        // behind a sequence's end: B = C = 0, Delta = 0
-        for (int i = tid; i < NB * 2 * NP; i += kThreads) {
-            const int q = i % NP;
-            const int64_t b = b0 + i / (2 * NP);
-            float v = 0.f;
-            if (b < p.B && q < p.N && t < valid_tokens(p.lengths, b, p.T))
-                v = to_f32(i / NP % 2 ? p.Cm[b * p.c_sb + t * p.c_st + static_cast<int64_t>(g) * p.N + q]
-                                      : p.Bm[b * p.b_sb + t * p.b_st + static_cast<int64_t>(g) * p.N + q]);
-            (&bc[0][0][0])[i] = v;
-        }
-        float x[OWN], z[OWN], step[OWN], u[OWN], y[OWN];
-        bool mine[OWN];
+    int place = 0;
+    for (int b0 = b_first; b0 < b_end; b0 += NB) {
+        float h[NB][4];
 #pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            const int64_t b = b0 + o * L + j;
-            mine[o] = o * L + j < NB && b < p.B && t < valid_tokens(p.lengths, b < p.B ? b : 0, p.T);
-            x[o] = z[o] = step[o] = y[o] = 0.f;
-            if (mine[o]) {
-                x[o] = to_f32(p.x[b * p.x_sb + t * p.x_st + d]);
-                step[o] = to_f32(p.dt[b * p.dt_sb + t * p.dt_st + d]) + bias;
-                if (p.z) z[o] = to_f32(p.z[b * p.z_sb + t * p.z_st + d]);
-                if (p.softplus) step[o] = softplus(step[o]);
+        for (int m = 0; m < NB; ++m)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[m][k] = hn[m][k];
+        if (NB > 1) load_states(b0 + NB);
+        for (int t = 0; t < p.T; ++t, place ^= 1) {
+#pragma unroll
+            for (int i = 0; i < BCT; ++i)
+                if (BC % kThreads == 0 || i * kThreads + tid < BC)
+                    (&bc[place][0][0][0])[i * kThreads + tid] = to_f32(rbc[i]);
+            float x[OWN], z[OWN], step[OWN], u[OWN], y[OWN];
+            bool mine[OWN];
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                const int64_t b = b0 + o * L + j;
+                mine[o] = o * L + j < NB && b < b_end && t < valid_tokens(p.lengths, b < b_end ? b : 0, p.T);
+                x[o] = to_f32(rx[o]);
+                z[o] = to_f32(rz[o]);
+                step[o] = y[o] = 0.f;
+                if (mine[o]) {
+                    step[o] = to_f32(rdt[o]) + bias;
+                    if (p.softplus) step[o] = softplus(step[o]);
+                }
+                u[o] = step[o] * x[o];
             }
-            u[o] = step[o] * x[o];
+            const bool same = t + 1 < p.T;
+            load_token(same ? b0 : b0 + NB, same ? t + 1 : 0);
+            __syncthreads();      // the other place is read by then
+#pragma unroll
+            for (int m = 0; m < NB; ++m) {
+                const int from = (tid & 31 & ~(L - 1)) | m % L;
+                const float dt = __shfl_sync(0xffffffffu, step[m / L], from);
+                const float du = __shfl_sync(0xffffffffu, u[m / L], from);
+                const float4 bq = *reinterpret_cast<const float4 *>(&bc[place][m][0][n0]);
+                const float4 cq = *reinterpret_cast<const float4 *>(&bc[place][m][1][n0]);
+                const float bv[4] = {bq.x, bq.y, bq.z, bq.w}, cv[4] = {cq.x, cq.y, cq.z, cq.w};
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    h[m][k] = fmaf(exp2_ftz(dt * A2[k]), h[m][k], du * bv[k]);
+                    sum = fmaf(cv[k], h[m][k], sum);
+                }
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (m % L == j) y[m / L] = sum;
+            }
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                if (!mine[o] || !live) continue;
+                if (p.skip) y[o] = fmaf(skip, x[o], y[o]);
+                if (p.z) y[o] *= activate(z[o], GDN_ACT_SILU);
+                p.y[(static_cast<int64_t>(b0 + o * L + j) * p.T + t) * p.D + d] = from_f32<E>(y[o]);
+            }
         }
-        __syncthreads();
+        if (!p.h_final || !live) continue;
 #pragma unroll
         for (int m = 0; m < NB; ++m) {
-            const int from = (tid & 31 & ~(L - 1)) | m % L;
-            const float dt = __shfl_sync(0xffffffffu, step[m / L], from);
-            const float du = __shfl_sync(0xffffffffu, u[m / L], from);
-            const float4 bq = *reinterpret_cast<const float4 *>(&bc[m][0][n0]);
-            const float4 cq = *reinterpret_cast<const float4 *>(&bc[m][1][n0]);
-            const float bv[4] = {bq.x, bq.y, bq.z, bq.w}, cv[4] = {cq.x, cq.y, cq.z, cq.w};
-            float sum = 0.f;
+            if (b0 + m >= b_end) break;
+            float *to = p.h_final + (b0 + m) * state + row + n0;
+            if (quads) {
+                if (n0 < p.N) *reinterpret_cast<float4 *>(to) = make_float4(h[m][0], h[m][1], h[m][2], h[m][3]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h[m][k] = fmaf(exp2_ftz(dt * A2[k]), h[m][k], du * bv[k]);
-                sum = fmaf(cv[k], h[m][k], sum);
+                for (int k = 0; k < 4; ++k)
+                    if (n0 + k < p.N) to[k] = h[m][k];
             }
-#pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (m % L == j) y[m / L] = sum;
-        }
-#pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            if (!mine[o] || !live) continue;
-            if (p.skip) y[o] = fmaf(skip, x[o], y[o]);
-            if (p.z) y[o] *= activate(z[o], GDN_ACT_SILU);
-            p.y[(static_cast<int64_t>(b0 + o * L + j) * p.T + t) * p.D + d] = from_f32<E>(y[o]);
-        }
-    }
-    if (!p.h_final || !live) return;
-#pragma unroll
-    for (int m = 0; m < NB; ++m) {
-        if (b0 + m >= p.B) break;
-        float *row = p.h_final + state(m) + n0;
-        if (quads) {
-            if (n0 < p.N) *reinterpret_cast<float4 *>(row) = make_float4(h[m][0], h[m][1], h[m][2], h[m][3]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (n0 + k < p.N) row[k] = h[m][k];
         }
     }
 }
@@ -667,15 +709,30 @@ cudaError_t launch_prompt(const gdn_scan_problem *pr, ScanParams<E> &p, void *wo
 }
 
 template <typename E, int NP>
-cudaError_t launch_step(const gdn_scan_problem *pr, const ScanParams<E> &p, cudaStream_t s) {
+cudaError_t launch_step(const gdn_scan_problem *pr, ScanParams<E> &p, cudaStream_t s) {
     // kBatch sequences to a thread where that still leaves two blocks to an SM
     constexpr int channels = kThreads / (NP / 4);
-    const unsigned blocks = pr->G * ((pr->D / pr->G + channels - 1) / channels);
-    if (static_cast<int64_t>(blocks) * ((pr->B + kBatch - 1) / kBatch) >= 2 * 152)
-        gdn_scan_step_kernel<E, NP, kBatch>
-            <<<dim3(blocks, (pr->B + kBatch - 1) / kBatch), kThreads, 0, s>>>(p);
-    else
+    const int64_t blocks = pr->G * ((pr->D / pr->G + channels - 1) / channels);
+    const int64_t sets = (pr->B + kBatch - 1) / kBatch;
+    p.turns = 1;
+    if (blocks * sets < 2 * 152) {
         gdn_scan_step_kernel<E, NP, 1><<<dim3(blocks, pr->B), kThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    // Sets to a block by the turns of all waves, with one more for a block's start.
+    constexpr int64_t wave = 152 * kStepBlocks;
+    int64_t best = 0;
+    for (int w = 1; w <= 4; ++w) {
+        const int64_t rows = std::max<int64_t>(1, std::min(sets, w * wave / blocks));
+        const int64_t turns = (sets + rows - 1) / rows;
+        const int64_t cost = (blocks * ((sets + turns - 1) / turns) + wave - 1) / wave * (turns + 1);
+        if (best == 0 || cost < best) {
+            best = cost;
+            p.turns = static_cast<int>(turns);
+        }
+    }
+    gdn_scan_step_kernel<E, NP, kBatch>
+        <<<dim3(blocks, (sets + p.turns - 1) / p.turns), kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
