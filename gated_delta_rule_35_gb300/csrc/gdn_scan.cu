@@ -57,6 +57,12 @@ __device__ __forceinline__ F2 softplus2(F2 v) {
     return pack2(softplus(a), softplus(b));
 }
 
+// ex2.approx lies 0.5e-8 to 2.7e-8 of its value too low on average for arguments in [-0.5, 0]
+// (measured on 2^20 points in each of ten ranges), which a state that hardly decays adds up
+// token by token: 1.3e-8 each, 1.9e-6 after 153. With this added to the argument the mean
+// lies within 1.3e-8 on both sides of 0, and 2^kLift is 1, so Delta = 0 keeps a state's bits.
+constexpr float kLift = 2e-8f;
+
 // Four consecutive elements of an aligned shared row, or zeros.
 __device__ __forceinline__ float4 widen4(const float *p, bool in) {
     const float4 q = *reinterpret_cast<const float4 *>(p);
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, NB > 1 ? kStepBlocks : 1) gdn_scan_s
                 float sum = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    h[m][k] = fmaf(exp2_ftz(dt * A2[k]), h[m][k], du * bv[k]);
+                    h[m][k] = fmaf(exp2_ftz(fmaf(dt, A2[k], kLift)), h[m][k], du * bv[k]);
                     sum = fmaf(cv[k], h[m][k], sum);
                 }
 #pragma unroll
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
     };
     auto decay = [&](F2 step, F2 A2) {
         float lo, hi;
-        unpack2(mul2(step, A2), lo, hi);
+        unpack2(fma2(step, A2, pack2(kLift, kLift)), lo, hi);
         return pack2(exp2_ftz(lo), exp2_ftz(hi));
     };
     load_states(p.A + static_cast<int64_t>(d) * p.N, A2, kLog2e);
@@ -591,15 +597,17 @@ __global__ void __launch_bounds__(kThreads, NP <= 32 ? 3 : NP <= 64 ? 2 : 1) gdn
             F2 e[SP2];
             load_states(p.seg_h + seg_at(i) * p.N, e, 1.f);
             const float sum = p.seg_dt[seg_at(i)];
-            // exp(A sum) as a square: where Delta A > 0 it may pass the range though its
+            // exp(A sum) in two factors: where Delta A > 0 it may pass the range though its
             // product with a small state does not (nor 0 times it). A normal number times
             // 2^254 is beyond the range anyway.
 #pragma unroll
             for (int q = 0; q < SP2; ++q) {
                 float lo, hi;
                 unpack2(mul2(pack2(sum, sum), A2[q]), lo, hi);
-                const F2 root = pack2(exp2_ftz(0.5f * fminf(lo, 254.f)), exp2_ftz(0.5f * fminf(hi, 254.f)));
-                h[q] = fma2(mul2(h[q], root), root, e[q]);
+                const F2 f = pack2(exp2_ftz(fminf(lo, 127.f)), exp2_ftz(fminf(hi, 127.f)));
+                const F2 rest = pack2(exp2_ftz(fminf(fmaxf(lo - 127.f, 0.f), 127.f)),
+                                      exp2_ftz(fminf(fmaxf(hi - 127.f, 0.f), 127.f)));
+                h[q] = fma2(mul2(h[q], f), rest, e[q]);
             }
         }
     }

@@ -182,6 +182,14 @@ def test_scan_long_sequences_of_few_channels(size, dtype):
             assert torch.equal(again[b, :nb], y[b, :nb])
 
 
+@pytest.mark.parametrize("T", [1, 7, 120, 1024])
+def test_scan_without_a_step_keeps_its_state(T):
+    """Delta = 0: exp(0) is 1 exactly, whatever x holds."""
+    i = scan_inputs(2, T, 40, 13, 1, F32, 360, soft=False)
+    i["dt"].zero_()
+    assert torch.equal(gdn.scan_fwd(**i)[1], i["h0"])
+
+
 def test_scan_grows_across_segments():
     """Delta A > 0 over a whole segment: its factor alone, e^128, is beyond fp32's range, the
     states that it multiplies (0 and 1e-30) stay within."""
