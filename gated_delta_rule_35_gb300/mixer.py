@@ -74,6 +74,13 @@ def _x(x, axes="[B,T,C]"):
     return x.shape, x.dtype, x.get_device()
 
 
+def _int32(what, *sizes):
+    """The sizes, refused where a problem's 32-bit field would wrap one."""
+    if any(not -2 ** 31 <= n < 2 ** 31 for n in sizes):
+        raise GdnError(GDN_ERR_UNSUPPORTED, what)
+    return sizes
+
+
 def _act(act):
     a = ACTS.get(act)
     if a is None:
@@ -133,7 +140,8 @@ def _conv_plan(x, weight, bias, state, lengths, act, out, final_state):
     if not 2 <= W <= 4:
         raise GdnError(GDN_ERR_UNSUPPORTED, "gdn_conv_fwd")
     window = (B, W - 1, C)
-    p = ConvProblem(B, T, C, W, DTYPES[dtype], _act(act), *_tokens(x, "x", shape, dtype, index))
+    p = ConvProblem(*_int32("gdn_conv_fwd", B, T, C, W), DTYPES[dtype], _act(act),
+                    *_tokens(x, "x", shape, dtype, index))
     for t, name, form, kind in ((weight, "weight", (C, W), torch.float32), (bias, "bias", (C,), torch.float32),
                                 (lengths, "lengths", (B,), torch.int32), (state, "state", window, dtype),
                                 (out, "out", shape, dtype), (final_state, "final_state", window, dtype)):
@@ -184,7 +192,8 @@ _INVALID = ctypes.c_size_t(-1).value
 
 def scan_workspace_bytes(B: int, T: int, D: int, N: int, G: int = 1, dtype=torch.bfloat16) -> int:
     """Bytes of workspace a scan_fwd of these sizes takes (0: none)."""
-    p = ScanProblem(B, T, D, N, G, DTYPES[dtype], 0, 0, *(0,) * 10)
+    sizes = _int32("gdn_scan_workspace_bytes", B, T, D, N, G)
+    p = ScanProblem(*sizes, DTYPES[dtype], 0, 0, *(0,) * 10)
     need = lib().gdn_scan_workspace_bytes(ctypes.byref(p))
     if need == _INVALID:
         raise GdnError(_refusal(p), "gdn_scan_workspace_bytes")
@@ -204,7 +213,8 @@ def _scan_plan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0, lengths, out, fin
         raise ValueError("B and C must be [B,T,G,N]")
     G, N = B.shape[2:]
     rows, state, f32 = (nb, T, G, N), (nb, nd, N), torch.float32
-    p = ScanProblem(nb, T, nd, N, G, DTYPES[dtype], GDN_SCAN_SOFTPLUS if dt_softplus else 0, 0,
+    p = ScanProblem(*_int32("gdn_scan_fwd", nb, T, nd, N, G), DTYPES[dtype],
+                    GDN_SCAN_SOFTPLUS if dt_softplus else 0, 0,
                     *_tokens(x, "x", shape, dtype, index), *_tokens(dt, "dt", shape, dtype, index),
                     *((0, 0) if z is None else _tokens(z, "z", shape, dtype, index)),
                     *_tokens(B, "B", rows, dtype, index), *_tokens(C, "C", rows, dtype, index))
@@ -267,7 +277,7 @@ def _norm_plan(x, groups, weight, bias, eps, act, gate, lengths, out):
     """(problem, device index), or the refusal."""
     shape, dtype, index = _x(x)
     B, T, C = shape
-    p = GroupNormProblem(B, T, C, groups, DTYPES[dtype], _act(act), eps, 0,
+    p = GroupNormProblem(*_int32("gdn_group_norm", B, T, C, groups), DTYPES[dtype], _act(act), eps, 0,
                          *_tokens(x, "x", shape, dtype, index),
                          *((0, 0) if gate is None else _tokens(gate, "gate", shape, dtype, index)))
     for t, name, form, kind in ((weight, "weight", (C,), torch.float32), (bias, "bias", (C,), torch.float32),
