@@ -7,7 +7,8 @@ the library's kernels on the current stream of the tensors' device, and the
 contracts are those of include/gdn.h. Tokens are channels-last; inputs marked
 *strided* may be slices of wider tensors (their innermost axes contiguous).
 ``lengths`` ([B] int32, on the device) holds the valid tokens of each sequence of a
-padded batch: rows at or past it are not used, and not written in the outputs.
+padded batch: rows at or past it are not used, and not written in the outputs (zeros,
+then, in an output that the call allocates).
 With ``stream`` the call runs, and allocates what it returns, on that stream.
 """
 from __future__ import annotations
@@ -86,6 +87,11 @@ def _act(act):
     if a is None:
         raise ValueError(f"act must be one of {', '.join(ACTS)}")
     return a
+
+
+def _new(x, lengths):
+    """An output of x's form; of a padded batch zeros, since some rows stay unwritten."""
+    return (torch.empty if lengths is None else torch.zeros)(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _call(f, what, index, *args):
@@ -168,7 +174,7 @@ def conv_fwd(x, weight, bias=None, state=None, lengths=None, act: str = "silu",
     p, window, index = _plans.get(key) or _keep(key, _conv_plan(
         x, weight, bias, state, lengths, act, out, final_state))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x, lengths)
     if not output_final_state:
         final_state = None
     elif final_state is None:
@@ -252,7 +258,7 @@ def scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = F
     if need:    # held until the call: freed before, out could be allocated in its place
         workspace = _workspace(workspace, need, x.device)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x, lengths)
     if not output_final_state:
         final_state = None
     elif final_state is None:
@@ -303,7 +309,7 @@ def group_norm(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: s
            _form(gate), _form(lengths), _form(out))
     p, index = _plans.get(key) or _keep(key, _norm_plan(x, groups, weight, bias, eps, act, gate, lengths, out))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x, lengths)
     _call(lib().gdn_group_norm, "gdn_group_norm", index, p, x.data_ptr(), _ptr(weight), _ptr(bias),
           _ptr(gate), _ptr(lengths), out.data_ptr())
     return out
