@@ -199,6 +199,10 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p
 // The mean of a set lies at most sqrt(32) of its deviations from k, so at most 33 times the
 // variance's rounding is lost, however far the mean is from zero. Channels and threads then
 // merge to groups, and the CTAs' groups through distributed shared memory, in rank order.
+// Means are added up as differences from one of those that are merged (from a thread's first
+// k, a group's first channel, the first rank), so a mean is rounded at its own size three times
+// however many are merged; summed as they were, means of 1e4 to 1e6 deviations were up to 41
+// roundings off (20000 tokens of 4 channels).
 constexpr int kBlockTokens = 4;
 constexpr int kSetBlocks = 32;
 // Of a thread's blocks the first kKept stay in shared memory between the statistics and the
@@ -244,7 +248,8 @@ __device__ __forceinline__ void merge_cluster(float (&part)[3][kThreads], int gr
             m = of_rank(&part[1][g]);
             s = of_rank(&part[2][g]);
         }
-        const float total = warp_sum(n), all = warp_sum(n * m) / total, d = m - all;
+        const float first = __shfl_sync(0xffffffffu, m, 0);     // rank 0 has tokens
+        const float total = warp_sum(n), all = first + warp_sum(n * (m - first)) / total, d = m - all;
         s = warp_sum(fmaf(n * d, d, s));
         if (lane == 0) {
             mean[g] = all;
@@ -308,7 +313,17 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
     };
     for (int i = 0; i < kKept + kRing; ++i) fetch(i);
     if (mine) {
+        // The mean of the sets so far less the first set's k, which waits in this thread's part of
+        // means; behind the last set the mean itself.
         F2 mean[N], m2[N];
+        float *const to = means + row * SC + q, *const to2 = squares + row * SC + q;
+        auto first_shift = [&](int k) { return pack2(to[2 * k], to[V > 1 ? 2 * k + 1 : 0]); };
+        auto keep = [](float *at, F2 v) {
+            float a, b;
+            unpack2(v, a, b);
+            at[0] = a;
+            if (V > 1) at[1] = b;
+        };
 #pragma unroll
         for (int k = 0; k < N; ++k) mean[k] = m2[k] = 0;
         float count = 0.f;
@@ -362,11 +377,18 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
             const float f = nb / count;
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const F2 off = mul2(s1[k], both(1.f / nb));             // the set's mean - k
+                const F2 off = mul2(s1[k], both(1.f / nb));             // the set's mean - its k
                 const F2 set2 = fma2(mul2(off, s1[k]), both(-1.f), s2[k]);
-                const F2 set1 = fma2(shift[k], both(-1.f), off);        // the set's mean
+                F2 first = shift[k], set1 = off;                        // - the first k
+                if (set > 0) {
+                    first = first_shift(k);
+                    set1 = add2(set1, fma2(shift[k], both(-1.f), first));
+                } else if (end < blocks) {
+                    keep(to + 2 * k, first);
+                }
                 const F2 d = fma2(mean[k], both(-1.f), set1);
                 mean[k] = fma2(d, both(f), mean[k]);
+                if (end == blocks) mean[k] = fma2(first, both(-1.f), mean[k]);
                 m2[k] = add2(m2[k], fma2(mul2(d, d), both(na * f), set2));
             }
         }
@@ -375,14 +397,8 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
         for (int i = kKept; i < kKept + kRing; ++i) fetch(i);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            float a, b;
-            float *to = means + row * SC + q + 2 * k, *to2 = squares + row * SC + q + 2 * k;
-            unpack2(mean[k], a, b);
-            to[0] = a;
-            if (V > 1) to[1] = b;
-            unpack2(m2[k], a, b);
-            to2[0] = a;
-            if (V > 1) to2[1] = b;
+            keep(to + 2 * k, mean[k]);
+            keep(to2 + 2 * k, m2[k]);
         }
     }
     __syncthreads();
@@ -403,14 +419,15 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
         __syncthreads();
     };
     for (int col = threadIdx.x; col < SC; col += kThreads) {
+        const float first = means[col / cg * cg];
         float sum = 0.f;
 #pragma unroll 8
-        for (int r = 0; r < RP; ++r) sum = fmaf(r < more ? high : low, means[r * SC + col], sum);
+        for (int r = 0; r < RP; ++r) sum = fmaf(r < more ? high : low, means[r * SC + col] - first, sum);
         columns[col] = sum;
     }
     over_channels([&](int g, float sum) {
         part[0][g] = total;
-        part[1][g] = total > 0.f ? sum / total : 0.f;
+        part[1][g] = total > 0.f ? means[g * cg] + sum / total : 0.f;
     });
     for (int col = threadIdx.x; col < SC; col += kThreads) {
         const float m = part[1][col / cg];
@@ -494,14 +511,16 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
     if (n == 0) return;                                            // the whole cluster
     const int share = (n + K - 1) / K, t_begin = min(n, rank * share), t_end = min(n, t_begin + share);
     const E *x = p.x + b * p.x_sb + c0;
-    // sums about the first value of every 64 pieces, merged as in the tokens kernel
-    float count = 0.f, mean = 0.f, m2 = 0.f, shift = 0.f, s1 = 0.f, s2 = 0.f;
+    // sums about the first value of every 64 pieces, merged as in the tokens kernel: mean is less
+    // the first of these values
+    float count = 0.f, first = 0.f, mean = 0.f, m2 = 0.f, shift = 0.f, s1 = 0.f, s2 = 0.f;
     int set = 0;
     auto merge = [&] {
         const float nb = static_cast<float>(set) * V, na = count;
         if (set == 0) return;
         count += nb;
-        const float off = s1 / nb, d = shift + off - mean, w = nb / count;
+        if (na == 0.f) first = shift;
+        const float off = s1 / nb, d = shift - first + off - mean, w = nb / count;
         mean = fmaf(d, w, mean);
         m2 += fmaf(d * d, na * w, s2 - off * s1);
         set = 0;
@@ -529,21 +548,32 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
     }
     merge();
     part[0][threadIdx.x] = count;
-    part[1][threadIdx.x] = mean;
+    part[1][threadIdx.x] = first + mean;
     part[2][threadIdx.x] = m2;
     __syncthreads();
     if (threadIdx.x < 32) {
-        float na = 0.f, m = 0.f, s = 0.f;
-        for (int i = threadIdx.x; i < kThreads; i += 32) {
-            na += part[0][i];
-            m = fmaf(part[0][i], part[1][i], m);
+        constexpr int M = kThreads / 32;
+        float n_of[M], m_of[M], s_of[M], na = 0.f, m = 0.f, s = 0.f;
+        first = part[1][0];                                       // thread 0 has a piece of every token
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            n_of[i] = part[0][i * 32 + threadIdx.x];
+            m_of[i] = part[1][i * 32 + threadIdx.x] - first;
+            s_of[i] = part[2][i * 32 + threadIdx.x];
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            na += n_of[i];
+            m = fmaf(n_of[i], m_of[i], m);
         }
         na = warp_sum(na);
         m = na > 0.f ? warp_sum(m) / na : 0.f;
-        for (int i = threadIdx.x; i < kThreads; i += 32) {
-            const float d = part[1][i] - m;
-            s += fmaf(part[0][i] * d, d, part[2][i]);
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float d = m_of[i] - m;
+            s += fmaf(n_of[i] * d, d, s_of[i]);
         }
+        m += first;
         s = warp_sum(s);
         __syncwarp();
         if (threadIdx.x == 0) {
