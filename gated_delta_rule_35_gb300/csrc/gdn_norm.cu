@@ -511,38 +511,62 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
     if (n == 0) return;                                            // the whole cluster
     const int share = (n + K - 1) / K, t_begin = min(n, rank * share), t_end = min(n, t_begin + share);
     const E *x = p.x + b * p.x_sb + c0;
-    // sums about the first value of every 64 pieces, merged as in the tokens kernel: mean is less
-    // the first of these values
+    // Blocks of up to four pieces of a token, loaded together, in sets of 1, 1, 2, 4, .. 64 pieces or
+    // a block more. The first set's sums are taken about its first piece's mean (at most sqrt(3) of
+    // its deviations from the set's), the others' about the mean of all before them; merged as in
+    // the tokens kernel (mean is less the first of these points). A set whose mean lies D from
+    // its point adds its own squares and at least D^2 / 2 a value to the total, since it is no
+    // larger than what lies before: at most 4 times the variance's rounding is lost. (Sets of 64
+    // about their first value: up to 64 V times where that is an outlier, and one load at a time:
+    // 65536 rows of 4096 in bf16 420 us for 394, 16384 tokens of 4096 4921 for 4179.)
     float count = 0.f, first = 0.f, mean = 0.f, m2 = 0.f, shift = 0.f, s1 = 0.f, s2 = 0.f;
-    int set = 0;
+    int set = 0, most = 1;
     auto merge = [&] {
         const float nb = static_cast<float>(set) * V, na = count;
         if (set == 0) return;
         count += nb;
-        if (na == 0.f) first = shift;
+        if (na == 0.f) first = shift; else most = min(2 * most, 64);
         const float off = s1 / nb, d = shift - first + off - mean, w = nb / count;
         mean = fmaf(d, w, mean);
-        m2 += fmaf(d * d, na * w, s2 - off * s1);
+        m2 += fmaf(d * d, na * w, fmaf(-off, s1, s2));
         set = 0;
     };
+    constexpr int U = 4, TURN = kThreads * V;
     for (int64_t t = t_begin; t < t_end; ++t) {
-#pragma unroll 4
-        for (int q = threadIdx.x * V; q < cg; q += kThreads * V) {
-            Piece<E, V> r;
-            float f[V];
-            r.load_rw(x + t * p.x_st + q);
-            r.widen(f);
-            if (set == 64) merge();
+        for (int q = threadIdx.x * V; q < cg; q += U * TURN) {
+            Piece<E, V> r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                r[u].zero();
+                if (q + u * TURN < cg) r[u].load_rw(x + t * p.x_st + q + u * TURN);
+            }
+            if (set >= most) merge();
             if (set == 0) {
-                shift = f[0];
+                shift = first + mean;
+                if (count == 0.f) {
+                    float f[V];
+                    r[0].widen(f);
+                    shift = f[0];
+#pragma unroll
+                    for (int k = 1; k < V; ++k) shift += f[k];
+                    shift *= 1.f / V;
+                }
                 s1 = s2 = 0.f;
             }
-            ++set;
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float d = f[k] - shift;
-                s1 += d;
-                s2 = fmaf(d, d, s2);
+            for (int u = 0; u < U; ++u) {
+                if (q + u * TURN >= cg) break;
+                float f[V], p1 = 0.f, p2 = 0.f;      // of the piece
+                r[u].widen(f);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float d = f[k] - shift;
+                    p1 += d;
+                    p2 = fmaf(d, d, p2);
+                }
+                ++set;
+                s1 += p1;
+                s2 += p2;
             }
         }
     }

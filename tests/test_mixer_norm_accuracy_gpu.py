@@ -1,10 +1,13 @@
-"""The group norm's statistics where rounding shows: means far from zero.
+"""The group norm's statistics where rounding shows: means far from zero, and outliers.
 
 u = 2^-24. The mean of a sequence's group is held as a sample of it plus a sum of
 differences: the sample's own channel mean, the group's and the cluster's take one rounding
 of the mean's size each (3u |mean|), everything else is summed at the size of the
 deviations, at most 256 + 64 terms in a row of sizes up to 8 deviations in these inputs
-(2560u of a deviation)."""
+(2560u of a deviation). The variance adds per-piece sums, at most 64 of a set and 256 of a
+group in a row, with at most four times the variance in a small set, and three times in a
+large one, lost to the point they are taken about: within (3 (67 + 8) + 256 + 16)u, the
+deviation within half of that, below 256u."""
 import numpy as np
 import pytest
 import torch
@@ -36,6 +39,20 @@ def test_mean_far_from_zero(size):
     check(x, G)
     if T > 1:
         check(x, G, [max(1, T - 7 * b) for b in range(B)])
+
+
+@pytest.mark.parametrize("size", [(1, 128, 4096), (1, 128, 1023), (2, 37, 2052), (1, 64, 1024), (3, 1, 4096)])
+@pytest.mark.parametrize("value", [180.5, -3.0e4])
+def test_outliers_first(size, value):
+    """The first value of each thread's share is all there is: what sums are taken about must
+    not be that value alone."""
+    B, T, C = size
+    x = torch.zeros(B, T, C, device="cuda")
+    V = 4 if C % 4 == 0 else 1
+    x[:, ::16, :256 * V:V] = value
+    want, v, xhat, size = ref.group_norm(f64(x), 1, None, None, 1e-5, "none")
+    bound = abs(xhat) * 260 * mb.U + 256 * mb.U * size + 2 * mb.U * abs(v)
+    mb.check(gdn.group_norm(x, 1), want, bound, x.dtype)
 
 
 def test_constant_rows_of_wide_groups():
