@@ -278,7 +278,7 @@ template <typename E, int W, int V>
 cudaError_t launch(const gdn_conv_problem *pr, ConvParams<E> &p, cudaStream_t s) {
     const int64_t cv = pr->C / V;
     if (pr->T <= kStepTokens) {
-        // kStepBatch sequences to a thread where that still leaves each SM its four blocks
+        // kStepBatch sequences to a thread where that still leaves each SM two blocks
         const unsigned blocks = static_cast<unsigned>((cv + kThreads - 1) / kThreads);
         const unsigned batches = (pr->B + kStepBatch - 1) / kStepBatch;
         const bool silu = pr->act == GDN_ACT_SILU;

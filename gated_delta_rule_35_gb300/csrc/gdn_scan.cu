@@ -35,8 +35,8 @@ struct ScanParams {
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1]. log1p(e) = e P(e) with P the
 // polynomial of degree 9 through log1p(e) / e at the ten Chebyshev points of [0, 1]: off by at
-// most 5.4e-9 of it, 1.4e-7 with its coefficients and steps in fp32, so small Delta keep
-// their relative accuracy. (2 atanh(e / (2 + e)) by its series, with a reciprocal: 2% more
+// most 5.4e-9 of it, 1.5e-8 with its coefficients in fp32, 1.4e-7 with its steps in fp32 too, so
+// small Delta keep their relative accuracy. (2 atanh(e / (2 + e)) by its series, with a reciprocal: 2% more
 // for the whole scan.)
 __device__ __forceinline__ float softplus(float v) {
     const float e = exp2_ftz(-kLog2e * fabsf(v));

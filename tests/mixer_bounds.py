@@ -1,12 +1,14 @@
 """Elementwise error bounds of the mixer operators' tests, from rounding analysis.
 
 u = 2^-24 is fp32's rounding. An output is rounded once to its type, off by at
-most eps(type) / 2 of its value. __expf(v) is within 2 + 1.173 |v| ulp (CUDA's
-stated bound) and __fdividef within 2 ulp, an ulp being 2u at most, so a
-sigmoid(v) is off by at most (6 + 1.2 |v|) 2u of itself, and so is v sigmoid(v)
-beside the error of v (slope of silu at most 1.1, of sigmoid 0.25). The quotient
-1 / (1 + exp(-v)) is flushed to 0 below fp32's normal range: what it multiplies is then
-off by that times 2^-126 at most (TINY)."""
+most eps(type) / 2 of its value. exp(-v) is ex2.approx of -v log2 e: the constant
+and the product are rounded, 2u |v| of the result, and PTX states a relative error of
+2^-22 = 4u for the instruction; 1 + exp(-v) takes u, rcp.approx 1 ulp, 2u at most,
+and the product with v another u. A sigmoid(v) is so off by at most (7 + 2 |v|)u of
+itself, v sigmoid(v) by (8 + 2 |v|)u beside the error of v (slope of silu at most 1.1, of
+sigmoid 0.25): within the (6 + 1.2 |v|) 2u used here. The quotient 1 / (1 + exp(-v)) is
+flushed to 0 below fp32's normal range: what it multiplies is then off by that times
+2^-126 at most (TINY)."""
 import numpy as np
 import torch
 
