@@ -230,29 +230,31 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// From each CTA's (count, mean, squares) of the groups: their mean and 1 / deviation over all
-// K CTAs, a lane to a CTA. Ends with an arrival at the cluster's barrier: a CTA waits
-// there before it leaves, since others may still read its part.
-__device__ __forceinline__ void merge_cluster(float (&part)[3][kThreads], int groups, int K, float eps,
-                                              float *mean, float *rstd) {
+// From each CTA's mean and squares of the groups: their mean and 1 / deviation over all K CTAs, a
+// lane to a CTA, which has `share` of the n tokens while they last. Ends with an arrival at the
+// cluster's barrier: a CTA waits there before it leaves, since others may still read its part.
+__device__ __forceinline__ void merge_cluster(float (&part)[2][kThreads], int groups, int K, int n, int share,
+                                              int cg, float eps, float *mean, float *rstd) {
     __syncthreads();
     if (K > 1) cluster_sync();
     const int lane = threadIdx.x % 32;
+    const float total = static_cast<float>(n) * cg;
+    const float count = lane < K ? static_cast<float>(min(n, (lane + 1) * share) - min(n, lane * share)) * cg : 0.f;
     for (int g = threadIdx.x / 32; g < groups; g += kThreads / 32) {
-        float n = 0.f, m = 0.f, s = 0.f;
+        float m = 0.f, s = 0.f;
         if (lane < K) {
             auto of_rank = [&](float *f) {
                 return K > 1 ? ld_cluster_f32(mapa_shared(smem_u32(f), lane)) : *f;
             };
-            n = of_rank(&part[0][g]);
-            m = of_rank(&part[1][g]);
-            s = of_rank(&part[2][g]);
+            m = of_rank(&part[0][g]);
+            s = of_rank(&part[1][g]);
         }
         const float first = __shfl_sync(0xffffffffu, m, 0);     // rank 0 has tokens
-        const float total = warp_sum(n), all = first + warp_sum(n * (m - first)) / total, d = m - all;
-        s = warp_sum(fmaf(n * d, d, s));
+        m -= first;
+        const float all = warp_sum(count * m) / total, d = m - all;
+        s = warp_sum(fmaf(count * d, d, s));
         if (lane == 0) {
-            mean[g] = all;
+            mean[g] = first + all;
             rstd[g] = rsqrtf(s / total + eps);
         }
     }
@@ -264,7 +266,7 @@ template <typename E, int V, bool GATED>
 __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kernel(NormParams<E> p) {
     __shared__ float means[kThreads * V], squares[kThreads * V];   // [token row][channel of the slice]
     __shared__ float columns[kThreads * V];                        // sums over token rows
-    __shared__ float part[3][kThreads];                            // count, mean, squares of a group
+    __shared__ float part[2][kThreads];                            // mean, squares of a group
     __shared__ float g_mean[kThreads], g_rstd[kThreads];
     const int cg = p.C / p.G, K = p.cluster, rank = blockIdx.x % K;
     const int g0 = blockIdx.y * p.groups, ng = min(p.groups, p.G - g0);
@@ -406,7 +408,9 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
     // squares about the group's mean. Threads take the channels, warps the groups; a channel's
     // rows shared out over idle threads cost 23 us for 19 (B3 T2048 C330 bf16).
     const int tokens = t_end - t_begin, more = tokens % RP;
-    const float total = static_cast<float>(tokens) * cg, low = static_cast<float>(tokens / RP), high = low + 1.f;
+    const float total = static_cast<float>(tokens) * cg, by_cg = 1.f / cg, low = static_cast<float>(tokens / RP), high = low + 1.f;
+    // col / cg: cg and col are at most 2048, and col + 1/2 is no nearer than 1/2 to a multiple of cg
+    auto group_of = [&](int col) { return static_cast<int>((col + 0.5f) * by_cg); };
     auto over_channels = [&](auto keep) {
         __syncthreads();
         for (int g = threadIdx.x / 32; g < ng; g += kThreads / 32) {
@@ -419,18 +423,17 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
         __syncthreads();
     };
     for (int col = threadIdx.x; col < SC; col += kThreads) {
-        const float first = means[col / cg * cg];
+        const float first = means[group_of(col) * cg];
         float sum = 0.f;
 #pragma unroll 8
         for (int r = 0; r < RP; ++r) sum = fmaf(r < more ? high : low, means[r * SC + col] - first, sum);
         columns[col] = sum;
     }
     over_channels([&](int g, float sum) {
-        part[0][g] = total;
-        part[1][g] = total > 0.f ? means[g * cg] + sum / total : 0.f;
+        part[0][g] = total > 0.f ? means[g * cg] + sum / total : 0.f;
     });
     for (int col = threadIdx.x; col < SC; col += kThreads) {
-        const float m = part[1][col / cg];
+        const float m = part[0][group_of(col)];
         float sum = 0.f;
 #pragma unroll 8
         for (int r = 0; r < RP; ++r) {
@@ -439,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
         }
         columns[col] = sum;
     }
-    over_channels([&](int g, float sum) { part[2][g] = sum; });
-    merge_cluster(part, ng, K, p.eps, g_mean, g_rstd);
+    over_channels([&](int g, float sum) { part[1][g] = sum; });
+    merge_cluster(part, ng, K, n, share, cg, p.eps, g_mean, g_rstd);
     if (mine) {
         F2 w[N], bias[N], mean[N];
         params<V>(p.w, c, 1.f, w);
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
 // thread taking every kThreads-th piece of a token and merging all its values.
 template <typename E, int V>
 __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p) {
-    __shared__ float part[3][kThreads];
+    __shared__ float part[2][kThreads], counts[kThreads];
     __shared__ float g_mean[1], g_rstd[1];
     const int cg = p.C / p.G, K = p.cluster, rank = blockIdx.x % K, c0 = blockIdx.y * cg;
     const int64_t b = blockIdx.x / K;
@@ -571,19 +574,19 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
         }
     }
     merge();
-    part[0][threadIdx.x] = count;
-    part[1][threadIdx.x] = first + mean;
-    part[2][threadIdx.x] = m2;
+    counts[threadIdx.x] = count;
+    part[0][threadIdx.x] = first + mean;
+    part[1][threadIdx.x] = m2;
     __syncthreads();
     if (threadIdx.x < 32) {
         constexpr int M = kThreads / 32;
         float n_of[M], m_of[M], s_of[M], na = 0.f, m = 0.f, s = 0.f;
-        first = part[1][0];                                       // thread 0 has a piece of every token
+        first = part[0][0];                                       // thread 0 has a piece of every token
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-            n_of[i] = part[0][i * 32 + threadIdx.x];
-            m_of[i] = part[1][i * 32 + threadIdx.x] - first;
-            s_of[i] = part[2][i * 32 + threadIdx.x];
+            n_of[i] = counts[i * 32 + threadIdx.x];
+            m_of[i] = part[0][i * 32 + threadIdx.x] - first;
+            s_of[i] = part[1][i * 32 + threadIdx.x];
         }
 #pragma unroll
         for (int i = 0; i < M; ++i) {
@@ -601,12 +604,11 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p
         s = warp_sum(s);
         __syncwarp();
         if (threadIdx.x == 0) {
-            part[0][0] = na;
-            part[1][0] = m;
-            part[2][0] = s;
+            part[0][0] = m;
+            part[1][0] = s;
         }
     }
-    merge_cluster(part, 1, K, p.eps, g_mean, g_rstd);
+    merge_cluster(part, 1, K, n, share, cg, p.eps, g_mean, g_rstd);
     const E *gate = p.gate ? p.gate + b * p.g_sb + c0 : nullptr;
     E *y = p.y + b * p.T * p.C + c0;
     for (int64_t t = t_begin; t < t_end; ++t) {
