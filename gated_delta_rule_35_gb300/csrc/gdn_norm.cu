@@ -1,13 +1,15 @@
 // Group norm of channels-last rows with an activation or a gate: gdn_group_norm of
 // include/gdn.h.
 //
-// Bound by memory: one read of x (and of the gate) and one write of y. Two kernels, both
-// with the mean first and the variance about it:
+// Bound by memory: one read of x (and of the gate) and one write of y. Three kernels:
 //   gdn_norm_rows_kernel   T = 1: a group is cg consecutive values, held in the registers of a
-//                          part of a warp between the statistics and the output;
+//                          part of a warp between the statistics (the mean first, the
+//                          variance about it) and the output;
 //   gdn_norm_tokens_kernel any T: a cluster of CTAs shares a sequence's tokens for a slice of
 //                          whole groups; what shared memory does not keep is read from
-//                          L2 the second time.
+//                          L2 the second time;
+//   gdn_norm_wide_kernel   groups of more pieces than a block has threads: a cluster to a group
+//                          of a sequence, x read twice.
 #include "mixer.cuh"
 #include "sm100_ptx.cuh"
 
@@ -503,7 +505,9 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
 }
 
 // The same for a group of more pieces than a block has threads: a cluster to a group, each
-// thread taking every kThreads-th piece of a token and merging all its values.
+// thread taking every kThreads-th piece of a token and merging all its values. 65536 rows of 4096
+// channels in bf16 take 396 us (2.7 TB/s): issue 72%, a block's merge for two pieces a thread.
+// One sequence of 16384 tokens takes 4145 us, on the 8 SMs of its one cluster.
 template <typename E, int V>
 __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p) {
     __shared__ float part[2][kThreads], counts[kThreads];
