@@ -410,8 +410,10 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
     // squares about the group's mean. Threads take the channels, warps the groups; a channel's
     // rows shared out over idle threads cost 23 us for 19 (B3 T2048 C330 bf16).
     const int tokens = t_end - t_begin, more = tokens % RP;
-    const float total = static_cast<float>(tokens) * cg, by_cg = 1.f / cg, low = static_cast<float>(tokens / RP), high = low + 1.f;
-    // col / cg: cg and col are at most 2048, and col + 1/2 is no nearer than 1/2 to a multiple of cg
+    const float total = static_cast<float>(tokens) * cg, low = static_cast<float>(tokens / RP), high = low + 1.f;
+    // col / cg: with both at most 2048 the product is off by less than 2048 2^-23 / cg, and the
+    // quotient no nearer than 1 / (2 cg) to a whole number.
+    const float by_cg = 1.f / cg;
     auto group_of = [&](int col) { return static_cast<int>((col + 0.5f) * by_cg); };
     auto over_channels = [&](auto keep) {
         __syncthreads();
