@@ -79,3 +79,38 @@ def test_padded_calls_replay_from_a_graph():
             want = call()
             torch.cuda.synchronize()
             assert torch.equal(got, want) and all((got[b, m:] == 0).all() for b, m in enumerate(lengths))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [1, 40, 900])
+def test_nan_and_infinity_stay_in_their_channel(T, dtype, value):
+    """One bad value changes its sequence's channel (the norm: its group) from its token on, and
+    not a bit of anything else."""
+    B, D, G = 6, 72, 9
+    t, c = T // 2, 37
+    w = torch.randn(D, 3, generator=gen(118)).cuda()
+    x, gate = draw(gen(119), (B, T, D), dtype), draw(gen(120), (B, T, D), dtype)
+    i = scan_inputs(B, T, D, 16, 1, dtype, 121)
+    bad = x.clone()
+    bad[2, t, c] = value
+
+    def elsewhere(a, b, *hit):
+        same = torch.ones_like(a, dtype=torch.bool)
+        same[hit] = False
+        return torch.equal(a[same], b[same])
+
+    (y0, s0), (y1, s1) = gdn.conv_fwd(x, w), gdn.conv_fwd(bad, w)
+    assert elsewhere(y0, y1, 2, slice(t, t + 3), c) and elsewhere(s0, s1, 2, slice(None), c)
+    assert not torch.isfinite(y1[2, t, c])
+    (y0, h0), (y1, h1) = gdn.scan_fwd(**dict(i, x=x)), gdn.scan_fwd(**dict(i, x=bad))
+    assert elsewhere(y0, y1, 2, slice(t, None), c) and elsewhere(h0, h1, 2, c)
+    assert not torch.isfinite(y1[2, t, c])
+    g = slice(c // (D // G) * (D // G), (c // (D // G) + 1) * (D // G))
+    y0, y1 = gdn.group_norm(x, G, gate=gate, act="silu"), gdn.group_norm(bad, G, gate=gate, act="silu")
+    assert elsewhere(y0, y1, 2, slice(None), g) and torch.isnan(y1[2, :, g]).all()
+    wide = draw(gen(122), (B, 3, 8192), dtype)
+    y0 = gdn.group_norm(wide, 2)
+    wide[2, 1, 4100] = value
+    y1 = gdn.group_norm(wide, 2)
+    assert elsewhere(y0, y1, 2, slice(None), slice(4096, None)) and torch.isnan(y1[2, :, 4096:]).all()
