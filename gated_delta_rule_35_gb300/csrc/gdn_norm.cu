@@ -201,10 +201,12 @@ __global__ void __launch_bounds__(kThreads) gdn_norm_rows_kernel(NormParams<E> p
 // The mean of a set lies at most sqrt(32) of its deviations from k, so at most 33 times the
 // variance's rounding is lost, however far the mean is from zero. Channels and threads then
 // merge to groups, and the CTAs' groups through distributed shared memory, in rank order.
-// Means are added up as differences from one of those that are merged (from a thread's first
-// k, a group's first channel, the first rank), so a mean is rounded at its own size three times
+// Means are added up as differences from one of those that are merged (from a set's k, a
+// group's first channel, the first rank), so a mean is rounded at its own size three times
 // however many are merged; summed as they were, means of 1e4 to 1e6 deviations were up to 41
-// roundings off (20000 tokens of 4 channels).
+// roundings off (20000 tokens of 4 channels). What is scaled by a reciprocal here is such a
+// difference or a square, so 1 ulp of rcp_ftz does; divisions took 7.0 us for 6.7 (B3 T1001 C330
+// fp32 in a graph).
 constexpr int kBlockTokens = 4;
 constexpr int kSetBlocks = 32;
 // Of a thread's blocks the first kKept stay in shared memory between the statistics and the
@@ -237,11 +239,15 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // cluster's barrier: a CTA waits there before it leaves, since others may still read its part.
 __device__ __forceinline__ void merge_cluster(float (&part)[2][kThreads], int groups, int K, int n, int share,
                                               int cg, float eps, float *mean, float *rstd) {
+    const int lane = threadIdx.x % 32;
+    const float share_of_one = rcp_ftz(static_cast<float>(n) * cg);
+    const float count = lane < K ? static_cast<float>(min(n, (lane + 1) * share) - min(n, lane * share)) * cg : 0.f;
+    auto over_ranks = [&](float v) {       // K is a power of two: lanes 0.. K - 1 have the sum
+        for (int o = K / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
     __syncthreads();
     if (K > 1) cluster_sync();
-    const int lane = threadIdx.x % 32;
-    const float total = static_cast<float>(n) * cg;
-    const float count = lane < K ? static_cast<float>(min(n, (lane + 1) * share) - min(n, lane * share)) * cg : 0.f;
     for (int g = threadIdx.x / 32; g < groups; g += kThreads / 32) {
         float m = 0.f, s = 0.f;
         if (lane < K) {
@@ -253,11 +259,11 @@ __device__ __forceinline__ void merge_cluster(float (&part)[2][kThreads], int gr
         }
         const float first = __shfl_sync(0xffffffffu, m, 0);     // rank 0 has tokens
         m -= first;
-        const float all = warp_sum(count * m) / total, d = m - all;
-        s = warp_sum(fmaf(count * d, d, s));
+        const float all = over_ranks(count * m) * share_of_one, d = m - all;
+        s = over_ranks(fmaf(count * d, d, s));
         if (lane == 0) {
             mean[g] = first + all;
-            rstd[g] = rsqrtf(s / total + eps);
+            rstd[g] = rsqrtf(fmaf(s, share_of_one, eps));
         }
     }
     __syncthreads();
@@ -317,22 +323,13 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
     };
     for (int i = 0; i < kKept + kRing; ++i) fetch(i);
     if (mine) {
-        // The mean of the sets so far less the first set's k, which waits in this thread's part of
-        // means; behind the last set the mean itself.
-        F2 mean[N], m2[N];
-        float *const to = means + row * SC + q, *const to2 = squares + row * SC + q;
-        auto first_shift = [&](int k) { return pack2(to[2 * k], to[V > 1 ? 2 * k + 1 : 0]); };
-        auto keep = [](float *at, F2 v) {
-            float a, b;
-            unpack2(v, a, b);
-            at[0] = a;
-            if (V > 1) at[1] = b;
-        };
+        // the mean of the sets so far, less the current set's k (shift is -k)
+        F2 mean[N], m2[N], shift[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) mean[k] = m2[k] = 0;
+        for (int k = 0; k < N; ++k) mean[k] = m2[k] = shift[k] = 0;
         float count = 0.f;
         for (int set = 0; set < blocks; set += kSetBlocks) {
-            F2 shift[N], s1[N], s2[N];
+            F2 s1[N], s2[N];
 #pragma unroll
             for (int k = 0; k < N; ++k) s1[k] = s2[k] = 0;
             const int end = min(blocks, set + kSetBlocks);
@@ -356,7 +353,9 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
 #pragma unroll
                         for (int u = 1; u < BT; ++u)
                             if (u < here) sum = add2(sum, v[u][k]);
-                        shift[k] = mul2(sum, both(-1.f / here));
+                        sum = mul2(sum, both(-rcp_ftz(here)));
+                        mean[k] = add2(mean[k], fma2(shift[k], both(-1.f), sum));
+                        shift[k] = sum;
                     }
                     b1[k] = b2[k] = 0;
                 }
@@ -376,23 +375,19 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
                     s2[k] = add2(s2[k], b2[k]);
                 }
             }
+            if (set == 0) {      // no sets before (a branch where k is taken: 12.2 us for 11.3, B3 T2048 C330 bf16)
+#pragma unroll
+                for (int k = 0; k < N; ++k) mean[k] = 0;
+            }
             const float nb = static_cast<float>(min(own - set * BT, kSetBlocks * BT)), na = count;
             count += nb;
-            const float f = nb / count;
+            const float f = nb * rcp_ftz(count), by_nb = rcp_ftz(nb);
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const F2 off = mul2(s1[k], both(1.f / nb));             // the set's mean - its k
+                const F2 off = mul2(s1[k], both(by_nb));                // the set's mean - its k
                 const F2 set2 = fma2(mul2(off, s1[k]), both(-1.f), s2[k]);
-                F2 first = shift[k], set1 = off;                        // - the first k
-                if (set > 0) {
-                    first = first_shift(k);
-                    set1 = add2(set1, fma2(shift[k], both(-1.f), first));
-                } else if (end < blocks) {
-                    keep(to + 2 * k, first);
-                }
-                const F2 d = fma2(mean[k], both(-1.f), set1);
+                const F2 d = fma2(mean[k], both(-1.f), off);
                 mean[k] = fma2(d, both(f), mean[k]);
-                if (end == blocks) mean[k] = fma2(first, both(-1.f), mean[k]);
                 m2[k] = add2(m2[k], fma2(mul2(d, d), both(na * f), set2));
             }
         }
@@ -401,8 +396,14 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
         for (int i = kKept; i < kKept + kRing; ++i) fetch(i);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            keep(to + 2 * k, mean[k]);
-            keep(to2 + 2 * k, m2[k]);
+            float a, b;
+            float *to = means + row * SC + q + 2 * k, *to2 = squares + row * SC + q + 2 * k;
+            unpack2(fma2(shift[k], both(-1.f), mean[k]), a, b);
+            to[0] = a;
+            if (V > 1) to[1] = b;
+            unpack2(m2[k], a, b);
+            to2[0] = a;
+            if (V > 1) to2[1] = b;
         }
     }
     __syncthreads();
@@ -410,10 +411,11 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
     // squares about the group's mean. Threads take the channels, warps the groups; a channel's
     // rows shared out over idle threads cost 23 us for 19 (B3 T2048 C330 bf16).
     const int tokens = t_end - t_begin, more = tokens % RP;
-    const float total = static_cast<float>(tokens) * cg, low = static_cast<float>(tokens / RP), high = low + 1.f;
-    // col / cg: with both at most 2048 the product is off by less than 2048 2^-23 / cg, and the
+    const float share_of_one = tokens > 0 ? rcp_ftz(static_cast<float>(tokens) * cg) : 0.f;
+    const float low = static_cast<float>(tokens / RP), high = low + 1.f;
+    // col / cg: with both at most 2048 the product is off by less than 2048 2^-22 / cg, and the
     // quotient no nearer than 1 / (2 cg) to a whole number.
-    const float by_cg = 1.f / cg;
+    const float by_cg = rcp_ftz(cg);
     auto group_of = [&](int col) { return static_cast<int>((col + 0.5f) * by_cg); };
     auto over_channels = [&](auto keep) {
         __syncthreads();
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
         columns[col] = sum;
     }
     over_channels([&](int g, float sum) {
-        part[0][g] = total > 0.f ? means[g * cg] + sum / total : 0.f;
+        part[0][g] = fmaf(sum, share_of_one, means[g * cg]);
     });
     for (int col = threadIdx.x; col < SC; col += kThreads) {
         const float m = part[0][group_of(col)];
