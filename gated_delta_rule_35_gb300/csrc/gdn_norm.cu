@@ -510,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, V > 1 ? 2 : 4) gdn_norm_tokens_kerne
 
 // The same for a group of more pieces than a block has threads: a cluster to a group, each
 // thread taking every kThreads-th piece of a token and merging all its values. 65536 rows of 4096
-// channels in bf16 take 396 us (2.7 TB/s): issue 72%, a block's merge for two pieces a thread.
-// One sequence of 16384 tokens takes 4145 us, on the 8 SMs of its one cluster.
+// channels in bf16 take 369 us (2.9 TB/s): issue 76%, a block's merge for two pieces a thread.
+// One sequence of 16384 tokens takes 4116 us, on the 8 SMs of its one cluster.
 template <typename E, int V>
 __global__ void __launch_bounds__(kThreads) gdn_norm_wide_kernel(NormParams<E> p) {
     __shared__ float part[2][kThreads], counts[kThreads];
