@@ -277,6 +277,6 @@ GDN_API const char *gdn_status_string(gdn_status s) {
     return "unknown status";
 }
 
-GDN_API uint32_t gdn_version(void) { return (0u << 16) | (2u << 8) | 0u; }
+GDN_API uint32_t gdn_version(void) { return (0u << 16) | (3u << 8) | 0u; }
 
 }  // extern "C"

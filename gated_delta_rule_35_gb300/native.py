@@ -28,7 +28,10 @@ EXPORTS = ("gdn_chunk_fwd_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_fwd_stag
            "gdn_chunk_fwd_noalloc", "gdn_decode_step", "gdn_decode_step_launches",
            "gdn_chunk_fwd_ex", "gdn_decode_step_ex", "gdn_chunk_fwd_host_bytes",
            "gdn_chunk_fwd_host", "gdn_conv_fwd", "gdn_scan_fwd", "gdn_scan_workspace_bytes",
-           "gdn_group_norm", "gdn_debug_arm_stall", "gdn_status_string", "gdn_version")
+           "gdn_group_norm", "gdn_recur_fwd", "gdn_recur_bwd_workspace_bytes", "gdn_recur_bwd",
+           "gdn_layer_norm", "gdn_layer_norm_bwd_workspace_bytes", "gdn_layer_norm_bwd",
+           "gdn_conv_bwd_workspace_bytes", "gdn_conv_bwd", "gdn_debug_arm_stall", "gdn_status_string",
+           "gdn_version")
 
 
 class GdnError(RuntimeError):
@@ -97,7 +100,7 @@ def lib():
         L.gdn_decode_step_launches.restype = ctypes.c_int32
         L.gdn_decode_step_launches.argtypes = [pp, ctypes.POINTER(ctypes.c_char_p),
                                                ctypes.c_int32]
-        # the problems of these (mixer.py) are structures of their own
+        # the problems of these (mixer.py, training.py) are structures of their own
         L.gdn_conv_fwd.restype = ctypes.c_int
         L.gdn_conv_fwd.argtypes = [vp] * 9
         L.gdn_scan_workspace_bytes.restype = sz
@@ -106,6 +109,19 @@ def lib():
         L.gdn_scan_fwd.argtypes = [vp] * 14 + [sz, vp]
         L.gdn_group_norm.restype = ctypes.c_int
         L.gdn_group_norm.argtypes = [vp] * 8
+        L.gdn_recur_fwd.restype = ctypes.c_int
+        L.gdn_recur_fwd.argtypes = [vp] * 11
+        L.gdn_recur_bwd.restype = ctypes.c_int
+        L.gdn_recur_bwd.argtypes = [vp] * 15 + [sz, vp]
+        L.gdn_layer_norm.restype = ctypes.c_int
+        L.gdn_layer_norm.argtypes = [vp] * 8
+        L.gdn_layer_norm_bwd.restype = ctypes.c_int
+        L.gdn_layer_norm_bwd.argtypes = [vp] * 10 + [sz, vp]
+        L.gdn_conv_bwd.restype = ctypes.c_int
+        L.gdn_conv_bwd.argtypes = [vp] * 13 + [sz, vp]
+        for f in (L.gdn_recur_bwd_workspace_bytes, L.gdn_layer_norm_bwd_workspace_bytes,
+                  L.gdn_conv_bwd_workspace_bytes):
+            f.restype, f.argtypes = sz, [vp]
         L.gdn_status_string.restype = ctypes.c_char_p
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_version.restype = ctypes.c_uint32

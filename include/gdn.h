@@ -471,6 +471,137 @@ GDN_API gdn_status gdn_group_norm(const gdn_group_norm_problem *p, const void *x
                                   const float *weight, const float *bias, const void *gate,
                                   const int32_t *lengths, void *y, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Training a mixing layer: the gated linear recurrence and layer norm with their
+ * backward passes, and the backward pass of the short convolution. The conventions are
+ * those of the operators above; further:
+ *  - A backward pass takes dy, the gradient of y, strided like x, in `dtype`, and what the
+ *    forward pass kept. Rows at or past a sequence's length add nothing to a gradient,
+ *    whatever they hold, and the gradients' rows there are left as they were. Outputs
+ *    may not overlap any input.
+ *  - Gradients of what the tokens share (rate, weight, bias) are sums over all valid
+ *    tokens, written, not added to: fp32, taken in an order that depends on the sizes
+ *    alone. Their blocks' parts pass through the workspace, which two calls that may
+ *    overlap on the GPU (two captured graphs among them) cannot share. The
+ *    *_workspace_bytes functions depend on the sizes and the dtype alone and give SIZE_MAX
+ *    for an invalid problem.
+ * ------------------------------------------------------------------------- */
+
+/* Gated linear recurrence: every channel is a state of its own with a decay and an input
+ * gate chosen per token,
+ *
+ *   s = sigmoid(decay[b,t,d]);   a = exp(-rate[d] s), or s itself where rate is NULL
+ *   h <- a h + m sigmoid(gate[b,t,d]) x[b,t,d],   y[b,t,d] = h
+ *
+ * with m = 1 (GDN_RECUR_PLAIN), 1 - a (GDN_RECUR_COMPLEMENT) or sqrt(1 - a^2)
+ * (GDN_RECUR_ROOT), and without the sigmoid where gate is NULL.
+ *  - x, decay, gate (or NULL) [B,T,D] in `dtype`, each strided; y [B,T,D] in `dtype`; rate
+ *    [D] (or NULL) fp32, finite and >= 0 (> 0 for the gradients of GDN_RECUR_ROOT, whose
+ *    m has none at rate 0: taken as 0 there); h0, h_final [B,D] fp32.
+ *  - states [B, ceil(T / GDN_RECUR_EVERY), D] fp32 or NULL: state k of a sequence is the one
+ *    entering its token k GDN_RECUR_EVERY, written where that token is valid. The backward
+ *    pass starts from them.
+ *  - B <= 65535, D <= 2^24, T <= 2^30 (else GDN_ERR_UNSUPPORTED). T = 0 copies the state
+ *    (the other pointers may be NULL then).
+ *  - One call serves prompts and single tokens (T = 1, h0 and h_final equal). */
+enum { GDN_RECUR_EVERY = 16 };
+
+typedef enum {
+    GDN_RECUR_PLAIN = 0,
+    GDN_RECUR_COMPLEMENT = 1,
+    GDN_RECUR_ROOT = 2
+} gdn_recur_scaling;
+
+typedef struct {
+    int32_t B, T, D;
+    int32_t dtype;     /* gdn_dtype */
+    int32_t scaling;   /* gdn_recur_scaling */
+    int32_t reserved;  /* 0 */
+    int64_t x_stride_b, x_stride_t, decay_stride_b, decay_stride_t, gate_stride_b, gate_stride_t;
+    int64_t dy_stride_b, dy_stride_t;   /* of the backward pass */
+} gdn_recur_problem;
+
+GDN_API gdn_status gdn_recur_fwd(const gdn_recur_problem *p, const void *x, const void *decay,
+                                 const void *gate, const float *rate, const float *h0,
+                                 const int32_t *lengths, void *y, float *h_final, float *states,
+                                 void *stream);
+
+/* Its gradients, from dy and dh_final [B,D] fp32 (NULL: zeros), the gradient of h_final: dx,
+ * d_decay, d_gate (given exactly where gate is) [B,T,D] in `dtype`, d_rate (or NULL; NULL
+ * where rate is) [D] and dh0 (or NULL) [B,D] fp32. states are the forward pass's; dh0 may
+ * be dh_final itself. */
+GDN_API size_t gdn_recur_bwd_workspace_bytes(const gdn_recur_problem *p);
+
+GDN_API gdn_status gdn_recur_bwd(const gdn_recur_problem *p, const void *dy, const void *x,
+                                 const void *decay, const void *gate, const float *rate,
+                                 const float *states, const float *dh_final, const int32_t *lengths,
+                                 void *dx, void *d_decay, void *d_gate, float *d_rate, float *dh0,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Layer norm of every token's C channels, its statistics kept for the backward pass:
+ *
+ *   xhat = (x - mean) rstd, rstd = 1 / sqrt(mean((x - mean)^2) + eps),   y = xhat weight + bias
+ *
+ * with mean = 0 under GDN_LAYER_NORM_RMS.
+ *  - x [B,T,C] strided, y [B,T,C] in `dtype`; weight, bias [C] fp32 or NULL (1 and 0);
+ *    stats [B,T,2] fp32 (mean, rstd) or NULL; eps >= 0.
+ *  - B, C and T <= 2^30, B T <= 2^31 - 1 (else GDN_ERR_UNSUPPORTED).
+ *  - y == x with x contiguous normalises in place (the backward pass wants x). */
+enum { GDN_LAYER_NORM_RMS = 1 };
+
+typedef struct {
+    int32_t B, T, C;
+    int32_t dtype;   /* gdn_dtype */
+    int32_t flags;   /* GDN_LAYER_NORM_* bits */
+    float eps;
+    int64_t x_stride_b, x_stride_t;
+    int64_t dy_stride_b, dy_stride_t;   /* of the backward pass */
+} gdn_layer_norm_problem;
+
+GDN_API gdn_status gdn_layer_norm(const gdn_layer_norm_problem *p, const void *x,
+                                  const float *weight, const float *bias, const int32_t *lengths,
+                                  void *y, float *stats, void *stream);
+
+/* Its gradients, from dy and the stats of the forward pass:
+ *
+ *   dx = rstd (w dy - mean(w dy) - xhat mean(w dy xhat))   (without mean(w dy) under RMS)
+ *   d_weight = sum dy xhat,   d_bias = sum dy              over all valid tokens
+ *
+ * dx [B,T,C] in `dtype`; d_weight, d_bias [C] fp32 or NULL. */
+GDN_API size_t gdn_layer_norm_bwd_workspace_bytes(const gdn_layer_norm_problem *p);
+
+GDN_API gdn_status gdn_layer_norm_bwd(const gdn_layer_norm_problem *p, const void *dy,
+                                      const void *x, const float *stats, const float *weight,
+                                      const int32_t *lengths, void *dx, float *d_weight,
+                                      float *d_bias, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/* Backward pass of gdn_conv_fwd: with v the value before the activation and p = dy act'(v),
+ *
+ *   dx[b,t,c] = sum_k weight[c,k] p[b, t + W - 1 - k, c]     (p = 0 past the last token)
+ *   d_weight[c,k] = sum_{b,t} p[b,t,c] x[b, t - W + 1 + k, c],   d_bias[c] = sum_{b,t} p[b,t,c]
+ *
+ * where the last W - 1 inputs take d_state_out[b,k,c] too, the gradient of state_out, and
+ * d_state_in is the gradient of the window state, laid out like it.
+ *  - x, weight, bias, state_in and lengths as in the forward pass. dy strided; dx [B,T,C],
+ *    d_state_out and d_state_in (each or NULL) [B,W-1,C] in `dtype`; d_weight [C,W],
+ *    d_bias [C] (or NULL) fp32. d_state_in may be d_state_out itself.
+ *  - The forward pass's limits. T = 0: d_state_in = d_state_out, d_weight = d_bias = 0. */
+typedef struct {
+    int32_t B, T, C, W;
+    int32_t dtype;   /* gdn_dtype */
+    int32_t act;     /* gdn_act */
+    int64_t x_stride_b, x_stride_t, dy_stride_b, dy_stride_t;
+} gdn_conv_bwd_problem;
+
+GDN_API size_t gdn_conv_bwd_workspace_bytes(const gdn_conv_bwd_problem *p);
+
+GDN_API gdn_status gdn_conv_bwd(const gdn_conv_bwd_problem *p, const void *dy, const void *x,
+                                const float *weight, const float *bias, const void *state_in,
+                                const void *d_state_out, const int32_t *lengths, void *dx,
+                                float *d_weight, float *d_bias, void *d_state_in, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
 /* Static description of a status code. Never NULL. */
 GDN_API const char *gdn_status_string(gdn_status s);
 
