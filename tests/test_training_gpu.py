@@ -205,6 +205,23 @@ def test_recur_extreme_gates(rate, scaling):
     checked(dict(zip(("dx", "d_decay", "d_gate", "d_rate", "d_state"), got)), want, bound, {})
 
 
+@pytest.mark.parametrize("scaling", ["root", "complement"])
+@pytest.mark.parametrize("rate", [True, False])
+def test_recur_where_factors_leave_the_normal_range(rate, scaling):
+    """sigmoid(decay) and 1 - a on both sides of 2^-126, down to where they vanish."""
+    i = recur_inputs(2, 50, 64, F32, 805, rate=rate, scaling=scaling)
+    i["decay"] = (84 + 6 * torch.rand(2, 50, 64, generator=gen(806))).cuda() * (-1 if rate else 1)
+    y, h, states = gdn.recur_fwd(**i, output_states=True)
+    want, bound, _ = recur_ref(i)
+    checked(dict(y=y, h=h, states=states), want, bound, {})
+    dy = draw(gen(807), (2, 50, 64), F32)
+    h0 = i.pop("h0")
+    got = gdn.recur_bwd(dy, states=states, **i)
+    i["h0"] = h0
+    want, bound = recur_bwd_ref(dy, i, None)
+    checked(dict(zip(("dx", "d_decay", "d_gate", "d_rate", "d_state"), got)), want, bound, {})
+
+
 def test_recur_keeps_a_state_that_no_token_changes():
     """decay far below 0: a = 1 exactly, no input, so the state and its gradient pass whole.
     The sigmoid may be 2^-126 for 0; with rates up to 8, m is then 2^-61 at most, as is rate s
