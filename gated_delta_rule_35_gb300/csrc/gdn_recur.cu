@@ -3,89 +3,101 @@
 // Bound by memory: one read of x, decay and gate and one write of y; instructions (about 30 to a
 // value) and their special functions come close to it. recur.cuh describes the tiles; a few
 // tokens go to a kernel of their own, a thread to four channels of a sequence.
+#include <utility>
+
 #include "recur.cuh"
 
 namespace gdn {
 namespace {
 
+constexpr int kMaxWarps = 8;
 constexpr int kStages = 2;         // tiles in the ring
 constexpr int kStepTokens = 8;     // up to here the step kernel
 constexpr int kStepThreads = 256;
 
 // A token's decay factor and input of two channels; t_scale: -rate log2 e.
-template <bool GATED, bool RATED>
-__device__ __forceinline__ void token2(F2 x, F2 decay, F2 gate, F2 t_scale, int scaling, F2 &a, F2 &u) {
-    F2 n, inverse;
-    if constexpr (RATED)
+__device__ __forceinline__ void token2(F2 x, F2 decay, F2 gate, F2 t_scale, bool gated, bool rated, int scaling,
+                                       F2 &a, F2 &u) {
+    F2 n;
+    if (rated)
         decay_factor2(mul2(sigmoid2(decay), t_scale), a, n);
     else
         sigmoids2(decay, a, n);
-    u = mul2(input_factor2(a, n, scaling, inverse), x);
-    if constexpr (GATED) u = mul2(u, sigmoid2(gate));
+    u = x;
+    if (gated) u = mul2(u, sigmoid2(gate));
+    if (scaling == GDN_RECUR_ROOT) {
+        float v0, v1;
+        unpack2(fma2(n, a, n), v0, v1);                // 1 - a^2
+        u = mul2(u, pack2(sqrt_ftz(v0), sqrt_ftz(v1)));
+    } else if (scaling == GDN_RECUR_COMPLEMENT) {
+        u = mul2(u, n);
+    }
 }
 
-template <typename E, bool GATED>
-constexpr int tile_bytes() { return (GATED ? 3 : 2) * Rows<E>::bytes; }
-
-template <typename E, bool GATED, bool RATED>
+template <typename E, int FORM>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_kernel(const RecurParams<E> p) {
-    __shared__ Exchange ex;
+    __shared__ Exchange<kMaxWarps> ex;
     extern __shared__ uint4 ring[];
+    const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.pairs != 0 : true;
+    const int scaling = scaling_of<FORM>(p);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int ranks = p.ranks, rank = blockIdx.x % ranks, c0 = blockIdx.x / ranks * kRecurChannels;
     const int c = c0 + 2 * lane, D = p.D;
+    const bool second = c + 1 < D;
     const int64_t b = blockIdx.y;
     const int n = valid_tokens(p.lengths, b, p.T);
     const int tile = warps * kRecurEvery * ranks;          // of the cluster
     const int tiles = (n + tile - 1) / tile, first = (rank * warps + warp) * kRecurEvery;
-    E *mine = reinterpret_cast<E *>(ring) + warp * (kStages * tile_bytes<E, GATED>() / sizeof(E));
     constexpr int rows = Rows<E>::bytes / sizeof(E);
+    const int slot = (gated ? 3 : 2) * rows;
+    E *mine = reinterpret_cast<E *>(ring) + warp * kStages * slot;
     auto fill = [&](int i) {
         if (i < tiles) {
-            E *to = mine + i % kStages * (GATED ? 3 : 2) * rows;
+            E *to = mine + i % kStages * slot;
             const int t = i * tile + first;
             fill_rows(to, p.x + b * p.x_sb, p.x_st, t, n, c0, D, p.fill, 0.f);
             // behind the sequence a is 1
-            fill_rows(to + rows, p.decay + b * p.a_sb, p.a_st, t, n, c0, D, p.fill, RATED ? -INFINITY : INFINITY);
-            if constexpr (GATED) fill_rows(to + 2 * rows, p.gate + b * p.g_sb, p.g_st, t, n, c0, D, p.fill, 0.f);
+            fill_rows(to + rows, p.decay + b * p.a_sb, p.a_st, t, n, c0, D, p.fill, rated ? -INFINITY : INFINITY);
+            if (gated) fill_rows(to + 2 * rows, p.gate + b * p.g_sb, p.g_st, t, n, c0, D, p.fill, 0.f);
         }
         copy_commit();
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fill(i);
-    const F2 t_scale = RATED ? mul2(load_pair(p.rate, c, D, p.pairs), both(-kLog2e)) : both(0.f);
-    F2 state = p.h0 ? load_pair(p.h0 + b * D, c, D, p.pairs) : both(0.f);
+    const F2 t_scale = rated ? mul2(load_pair(p.rate, c, D, pairs), both(-kLog2e)) : both(0.f);
     const int64_t chunks = (static_cast<int64_t>(p.T) + kRecurEvery - 1) / kRecurEvery;
-    if (ranks > 1) ptx::cluster_sync();                    // all blocks are there to be written to
+    Scan<false, kMaxWarps> scan(ex, ranks, rank, p.h0 ? load_pair(p.h0 + b * D, c, D, pairs) : both(0.f));
     for (int i = 0; i < tiles; ++i) {
         copy_wait<kStages - 1>();
         __syncwarp();
-        const E *from = mine + i % kStages * (GATED ? 3 : 2) * rows + 2 * lane;
+        const E *from = mine + i % kStages * slot + 2 * lane;
         F2 a[kRecurEvery], u[kRecurEvery];
         Through through = {both(1.f), both(0.f)};
 #pragma unroll
         for (int j = 0; j < kRecurEvery; ++j) {
             const E *at = from + j * kRecurChannels;
-            token2<GATED, RATED>(pair_of(at), pair_of(at + rows), GATED ? pair_of(at + 2 * rows) : both(0.f),
-                                 t_scale, p.scaling, a[j], u[j]);
+            token2(pair_of(at), pair_of(at + rows), gated ? pair_of(at + 2 * rows) : both(0.f), t_scale, gated,
+                   rated, scaling, a[j], u[j]);
             through.h = fma2(a[j], through.h, u[j]);
             through.a = mul2(a[j], through.a);
         }
         __syncwarp();
         fill(i + kStages);
-        F2 h = exchange<false>(ex, i, ranks, rank, through, state);
-        const int t = i * tile + first, left = n - t;
-        if (p.states && left > 0) store_pair(p.states + (b * chunks + t / kRecurEvery) * D, c, D, p.pairs, h);
-        E *y = p.y + (b * p.T + t) * D;
+        F2 h = scan.step(i, through);
+        const int t = i * tile + first, left = c < D ? n - t : 0;
+        if (p.states)
+            store_pair(p.states + (b * chunks + t / kRecurEvery) * D + c, h, left > 0, second, pairs);
+        E *y = p.y + (b * p.T + t) * D + c;
 #pragma unroll
         for (int j = 0; j < kRecurEvery; ++j) {
             h = fma2(a[j], h, u[j]);
-            if (j < left) store_pair(y, c, D, p.pairs, h);
+            store_pair(y, h, j < left, second, pairs);
             y += D;
         }
     }
     copy_wait<0>();
-    if (p.h_final && rank == 0 && warp == 0) store_pair(p.h_final + b * D, c, D, p.pairs, state);
+    const F2 state = scan.last(tiles);
+    if (p.h_final && rank == 0 && warp == 0) store_pair(p.h_final + b * D + c, state, c < D, second, pairs);
 }
 
 // V consecutive values in pairs (a single one in both halves), and back, rounded.
@@ -148,7 +160,7 @@ __global__ void __launch_bounds__(kStepThreads) gdn_recur_step_kernel(const Recu
 #pragma unroll
         for (int k = 0; k < P; ++k) {
             F2 a, u;
-            token2<GATED, RATED>(xs[k], ds[k], GATED ? gs[k] : both(0.f), t_scale[k], p.scaling, a, u);
+            token2(xs[k], ds[k], GATED ? gs[k] : both(0.f), t_scale[k], GATED, RATED, p.scaling, a, u);
             h[k] = fma2(a, h[k], u);
         }
         store_values<V>(y + static_cast<int64_t>(t) * p.D, h);
@@ -158,24 +170,31 @@ __global__ void __launch_bounds__(kStepThreads) gdn_recur_step_kernel(const Recu
 static_assert(kStepTokens <= kRecurEvery, "the step kernel keeps one state");
 
 template <typename E, bool GATED, bool RATED>
-cudaError_t launch(RecurParams<E> &p, cudaStream_t s) {
+cudaError_t launch_step(const RecurParams<E> &p, cudaStream_t s) {
+    constexpr size_t a = 4 * sizeof(E);
+    const bool wide = p.D % 4 == 0 && aligned_rows(p.x, p.B, p.T, p.x_sb, p.x_st, sizeof(E), a) &&
+                      aligned_rows(p.decay, p.B, p.T, p.a_sb, p.a_st, sizeof(E), a) &&
+                      (!GATED || aligned_rows(p.gate, p.B, p.T, p.g_sb, p.g_st, sizeof(E), a));
+    const int pieces = wide ? p.D / 4 : p.D;
+    const dim3 grid((pieces + kStepThreads - 1) / kStepThreads, p.B);
+    if (wide)
+        gdn_recur_step_kernel<E, 4, GATED, RATED><<<grid, kStepThreads, 0, s>>>(p);
+    else
+        gdn_recur_step_kernel<E, 1, GATED, RATED><<<grid, kStepThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename E, int... FORMS>
+cudaError_t launch(RecurParams<E> &p, cudaStream_t s, std::integer_sequence<int, FORMS...>) {
     if (p.T <= kStepTokens) {
-        constexpr size_t a = 4 * sizeof(E);
-        const bool wide = p.D % 4 == 0 && aligned_rows(p.x, p.B, p.T, p.x_sb, p.x_st, sizeof(E), a) &&
-                          aligned_rows(p.decay, p.B, p.T, p.a_sb, p.a_st, sizeof(E), a) &&
-                          (!GATED || aligned_rows(p.gate, p.B, p.T, p.g_sb, p.g_st, sizeof(E), a));
-        const int pieces = wide ? p.D / 4 : p.D;
-        const dim3 grid((pieces + kStepThreads - 1) / kStepThreads, p.B);
-        if (wide)
-            gdn_recur_step_kernel<E, 4, GATED, RATED><<<grid, kStepThreads, 0, s>>>(p);
-        else
-            gdn_recur_step_kernel<E, 1, GATED, RATED><<<grid, kStepThreads, 0, s>>>(p);
-        return cudaGetLastError();
+        if (p.gate) return p.rate ? launch_step<E, true, true>(p, s) : launch_step<E, true, false>(p, s);
+        return p.rate ? launch_step<E, false, true>(p, s) : launch_step<E, false, false>(p, s);
     }
+    using Kernel = void (*)(RecurParams<E>);
+    static constexpr Kernel table[] = {gdn_recur_kernel<E, kAnyForm>, gdn_recur_kernel<E, FORMS>...};
     recur_alignment(p);
-    int warps;
-    recur_shape(p, sizeof(E) == 2 ? 8 : 4, 2 * 152, warps);
-    return recur_launch(gdn_recur_kernel<E, GATED, RATED>, p, warps, warps * kStages * tile_bytes<E, GATED>(), s);
+    const int warps = recur_shape(p, sizeof(E) == 2 ? kMaxWarps : kMaxWarps / 2, 2 * 152);
+    return recur_launch(recur_kernel<E>(table, p), p, warps, warps * kStages * (p.gate ? 3 : 2) * Rows<E>::bytes, s);
 }
 
 }  // namespace
@@ -222,8 +241,7 @@ GDN_API gdn_status gdn_recur_fwd(const gdn_recur_problem *p, const void *x, cons
         a.y = static_cast<E *>(y);
         a.h_final = h_final;
         a.states = states;
-        if (gate) return rate ? launch<E, true, true>(a, s) : launch<E, true, false>(a, s);
-        return rate ? launch<E, false, true>(a, s) : launch<E, false, false>(a, s);
+        return launch<E>(a, s, std::make_integer_sequence<int, kForms>());
     };
     const cudaError_t err = p->dtype == GDN_BF16 ? go(__nv_bfloat16()) : go(float());
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

@@ -8,129 +8,127 @@
 //   ddecay = -dlog rate s (1 - s) (or dlog (1 - a)),  drate = -sum dlog s
 // with dm/dlog a = -a^2 / m for the root, -a for the complement. Bound by memory: four tensors
 // read and three written, the states a thirtieth of that.
+#include <utility>
+
 #include "recur.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kStages = 2;
+constexpr int kMaxWarps = 6;
+constexpr int kStages = 2;         // tiles in the ring
 
-template <bool RATED>
-__device__ __forceinline__ void decay2(F2 decay, F2 t_scale, F2 &s, F2 &s_n, F2 &a, F2 &a_n) {
-    sigmoids2(decay, s, s_n);
-    if constexpr (RATED) {
-        decay_factor2(mul2(s, t_scale), a, a_n);
-    } else {
-        a = s;
-        a_n = s_n;
-    }
-}
-
-template <typename E, bool GATED>
-constexpr int tile_bytes() { return (GATED ? 4 : 3) * Rows<E>::bytes; }
-
-template <typename E, bool GATED, bool RATED>
-__global__ void __launch_bounds__(128, 3) gdn_recur_bwd_kernel(const RecurParams<E> p) {
-    __shared__ Exchange ex;
+template <typename E, int FORM>
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const RecurParams<E> p) {
+    __shared__ Exchange<kMaxWarps> ex;
     extern __shared__ uint4 ring[];
+    const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.pairs != 0 : true;
+    const int scaling = scaling_of<FORM>(p);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int ranks = p.ranks, rank = blockIdx.x % ranks, c0 = blockIdx.x / ranks * kRecurChannels;
     const int c = c0 + 2 * lane, D = p.D;
+    const bool second = c + 1 < D;
     const int64_t b = blockIdx.y;
     const int n = valid_tokens(p.lengths, b, p.T);
     const int tile = warps * kRecurEvery * ranks;          // of the cluster
     const int tiles = (n + tile - 1) / tile, first = (rank * warps + warp) * kRecurEvery;
-    E *mine = reinterpret_cast<E *>(ring) + warp * (kStages * tile_bytes<E, GATED>() / sizeof(E));
-    constexpr int rows = Rows<E>::bytes / sizeof(E), tensors = GATED ? 4 : 3;
+    constexpr int rows = Rows<E>::bytes / sizeof(E);
+    const int slot = (gated ? 4 : 3) * rows;
+    E *mine = reinterpret_cast<E *>(ring) + warp * kStages * slot;
     auto fill = [&](int i) {                               // i-th from the last
         if (i < tiles) {
-            E *to = mine + i % kStages * tensors * rows;
+            E *to = mine + i % kStages * slot;
             const int t = (tiles - 1 - i) * tile + first;
             fill_rows(to, p.x + b * p.x_sb, p.x_st, t, n, c0, D, p.fill, 0.f);
             // behind the sequence a is 1
-            fill_rows(to + rows, p.decay + b * p.a_sb, p.a_st, t, n, c0, D, p.fill, RATED ? -INFINITY : INFINITY);
+            fill_rows(to + rows, p.decay + b * p.a_sb, p.a_st, t, n, c0, D, p.fill, rated ? -INFINITY : INFINITY);
             fill_rows(to + 2 * rows, p.dy + b * p.dy_sb, p.dy_st, t, n, c0, D, p.fill, 0.f);
-            if constexpr (GATED) fill_rows(to + 3 * rows, p.gate + b * p.g_sb, p.g_st, t, n, c0, D, p.fill, 0.f);
+            if (gated) fill_rows(to + 3 * rows, p.gate + b * p.g_sb, p.g_st, t, n, c0, D, p.fill, 0.f);
         }
         copy_commit();
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fill(i);
-    const F2 rate = RATED ? load_pair(p.rate, c, D, p.pairs) : both(0.f), t_scale = mul2(rate, both(-kLog2e));
+    const F2 rate = rated ? load_pair(p.rate, c, D, pairs) : both(0.f), t_scale = mul2(rate, both(-kLog2e));
     const F2 minus_rate = mul2(rate, both(-1.f));
-    F2 carry = p.dh_final ? load_pair(p.dh_final + b * D, c, D, p.pairs) : both(0.f), d_rate = both(0.f);
+    F2 d_rate = both(0.f);
     const int64_t chunks = (static_cast<int64_t>(p.T) + kRecurEvery - 1) / kRecurEvery;
-    if (ranks > 1) ptx::cluster_sync();                    // all blocks are there to be written to
+    Scan<true, kMaxWarps> scan(ex, ranks, rank,
+                               p.dh_final ? load_pair(p.dh_final + b * D, c, D, pairs) : both(0.f));
     for (int i = 0; i < tiles; ++i) {
-        const int t = (tiles - 1 - i) * tile + first, left = n - t;
+        const int t = (tiles - 1 - i) * tile + first, left = c < D ? n - t : 0;
         F2 h = both(0.f);
-        if (left > 0) h = load_pair(p.states + (b * chunks + t / kRecurEvery) * D, c, D, p.pairs);
+        if (n > t) h = load_pair(p.states + (b * chunks + t / kRecurEvery) * D, c, D, pairs);
         copy_wait<kStages - 1>();
         __syncwarp();
-        const E *from = mine + i % kStages * tensors * rows + 2 * lane;
+        const E *from = mine + i % kStages * slot + 2 * lane;
         F2 lam[kRecurEvery];                               // first the decay factors
         Through through = {both(1.f), both(0.f)};
 #pragma unroll
         for (int j = kRecurEvery - 1; j >= 0; --j) {
             const E *at = from + j * kRecurChannels;
-            F2 a_n;
-            if constexpr (RATED)
-                decay_factor2(mul2(sigmoid2(pair_of(at + rows)), t_scale), lam[j], a_n);
-            else
-                sigmoids2(pair_of(at + rows), lam[j], a_n);
+            lam[j] = sigmoid2(pair_of(at + rows));
+            if (rated) lam[j] = decay_factor2(mul2(lam[j], t_scale));
             through.h = mul2(lam[j], add2(pair_of(at + 2 * rows), through.h));
             through.a = mul2(lam[j], through.a);
         }
-        F2 next = exchange<true>(ex, i, ranks, rank, through, carry);
+        F2 next = scan.step(i, through);
 #pragma unroll
         for (int j = kRecurEvery - 1; j >= 0; --j) {
             const F2 a = lam[j];
             lam[j] = add2(pair_of(from + j * kRecurChannels + 2 * rows), next);
             next = mul2(a, lam[j]);
         }
-        const int64_t out = (b * p.T + t) * D;
+        int64_t out = (b * p.T + t) * D + c;
 #pragma unroll
         for (int j = 0; j < kRecurEvery; ++j) {
             const E *at = from + j * kRecurChannels;
-            F2 s, s_n, a, a_n, inverse, q, q_n;
-            decay2<RATED>(pair_of(at + rows), t_scale, s, s_n, a, a_n);
-            const F2 m = input_factor2(a, a_n, p.scaling, inverse);
-            const F2 x = pair_of(at);
-            F2 qx = x, mlam = mul2(m, lam[j]);
-            if constexpr (GATED) {
+            F2 s, s_n, a, a_n, inverse;
+            sigmoids2(pair_of(at + rows), s, s_n);
+            if (rated) {
+                decay_factor2(mul2(s, t_scale), a, a_n);
+            } else {
+                a = s;
+                a_n = s_n;
+            }
+            const F2 m = input_factor2(a, a_n, scaling, inverse), x = pair_of(at);
+            F2 qx = x, dx = mul2(m, lam[j]), d_gate;
+            if (gated) {
+                F2 q, q_n;
                 sigmoids2(pair_of(at + 3 * rows), q, q_n);
                 qx = mul2(q, x);
+                d_gate = mul2(mul2(dx, qx), q_n);
+                dx = mul2(dx, q);
             }
             // dlog = lam a (h + q x (dm/dlog a) / a)
             F2 inner = h;
-            if (p.scaling == GDN_RECUR_ROOT)
-                inner = fma2(mul2(mul2(a, inverse), both(-1.f)), qx, h);
-            else if (p.scaling == GDN_RECUR_COMPLEMENT)
+            if (scaling == GDN_RECUR_ROOT)
+                inner = fma2(mul2(mul2(a, inverse), qx), both(-1.f), h);
+            else if (scaling == GDN_RECUR_COMPLEMENT)
                 inner = fma2(qx, both(-1.f), h);
             const F2 dlog = mul2(mul2(lam[j], a), inner);
             h = fma2(a, h, mul2(m, qx));
-            d_rate = RATED ? fma2(dlog, s, d_rate) : d_rate;
-            if (j < left) {
-                const int64_t at_out = out + static_cast<int64_t>(j) * D;
-                store_pair(p.dx + at_out, c, D, p.pairs, GATED ? mul2(mlam, q) : mlam);
-                if constexpr (GATED) store_pair(p.d_gate + at_out, c, D, p.pairs, mul2(mul2(mlam, qx), q_n));
-                store_pair(p.d_decay + at_out, c, D, p.pairs,
-                           mul2(dlog, RATED ? mul2(minus_rate, mul2(s, s_n)) : a_n));
-            }
+            if (rated) d_rate = fma2(dlog, s, d_rate);
+            const bool there = j < left;
+            store_pair(p.dx + out, dx, there, second, pairs);
+            if (gated) store_pair(p.d_gate + out, d_gate, there, second, pairs);
+            store_pair(p.d_decay + out, mul2(dlog, rated ? mul2(minus_rate, mul2(s, s_n)) : a_n), there, second,
+                       pairs);
+            out += D;
         }
         __syncwarp();
         fill(i + kStages);
     }
     copy_wait<0>();
-    if (p.dh0 && rank == 0 && warp == 0) store_pair(p.dh0 + b * D, c, D, p.pairs, carry);
-    if (RATED && p.d_rate_part) {
+    const F2 carry = scan.last(tiles);
+    if (p.dh0 && rank == 0 && warp == 0) store_pair(p.dh0 + b * D + c, carry, c < D, second, pairs);
+    if (rated && p.d_rate_part) {
         F2 *sums = reinterpret_cast<F2 *>(ring);           // [warp][lane]; the ring is empty
-        __syncthreads();
         sums[threadIdx.x] = d_rate;
         __syncthreads();
         if (warp == 0) {
             for (int w = 1; w < warps; ++w) d_rate = add2(d_rate, sums[w * 32 + lane]);
-            store_pair(p.d_rate_part + (b * ranks + rank) * D, c, D, p.pairs, mul2(d_rate, both(-1.f)));
+            store_pair(p.d_rate_part + (b * ranks + rank) * D + c, mul2(d_rate, both(-1.f)), c < D, second, pairs);
         }
     }
 }
@@ -139,13 +137,14 @@ size_t bwd_workspace(const gdn_recur_problem *p) {
     return align_up(static_cast<size_t>(p->B) * kMaxRanks * p->D * 4);
 }
 
-template <typename E, bool GATED, bool RATED>
-cudaError_t launch(RecurParams<E> &p, float *d_rate, cudaStream_t s) {
+template <typename E, int... FORMS>
+cudaError_t launch(RecurParams<E> &p, float *d_rate, cudaStream_t s, std::integer_sequence<int, FORMS...>) {
+    using Kernel = void (*)(RecurParams<E>);
+    static constexpr Kernel table[] = {gdn_recur_bwd_kernel<E, kAnyForm>, gdn_recur_bwd_kernel<E, FORMS>...};
     recur_alignment(p);
-    int warps;
-    recur_shape(p, sizeof(E) == 2 ? 4 : 2, 3 * 152, warps);
-    const cudaError_t err = recur_launch(gdn_recur_bwd_kernel<E, GATED, RATED>, p, warps,
-                                         warps * kStages * tile_bytes<E, GATED>(), s);
+    const int warps = recur_shape(p, sizeof(E) == 2 ? kMaxWarps : kMaxWarps / 2, 2 * 152);
+    const cudaError_t err = recur_launch(recur_kernel<E>(table, p), p, warps,
+                                         warps * kStages * (p.gate ? 4 : 3) * Rows<E>::bytes, s);
     if (err != cudaSuccess || !d_rate) return err;
     return column_sums(p.d_rate_part, p.B * p.ranks, p.D, p.D, d_rate, nullptr, s);
 }
@@ -218,8 +217,7 @@ GDN_API gdn_status gdn_recur_bwd(const gdn_recur_problem *p, const void *dy, con
         a.d_gate = static_cast<E *>(d_gate);
         a.dh0 = dh0;
         a.d_rate_part = d_rate ? static_cast<float *>(workspace) : nullptr;
-        if (gate) return rate ? launch<E, true, true>(a, d_rate, s) : launch<E, true, false>(a, d_rate, s);
-        return rate ? launch<E, false, true>(a, d_rate, s) : launch<E, false, false>(a, d_rate, s);
+        return launch<E>(a, d_rate, s, std::make_integer_sequence<int, kForms>());
     };
     const cudaError_t err = p->dtype == GDN_BF16 ? go(__nv_bfloat16()) : go(float());
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

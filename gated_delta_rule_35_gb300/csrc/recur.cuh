@@ -18,7 +18,6 @@ namespace gdn {
 
 constexpr int kRecurEvery = GDN_RECUR_EVERY;   // tokens to a warp's tile: a kept state for each
 constexpr int kRecurChannels = 64;             // channels of a block
-constexpr int kMaxWarps = 8;
 constexpr int kMaxRanks = 8;                   // blocks of a cluster
 
 template <typename E>
@@ -32,14 +31,9 @@ struct RecurParams {
     int B, T, D, scaling;
     // fill: bytes of a copy to shared memory (16, 4 or, element by element, 2);
     // pairs: whether the outputs' channel pairs are aligned
-    int fill, pairs, ranks;
+    int fill, pairs, ranks;     // ranks: blocks to a cluster
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -48,6 +42,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 __device__ __forceinline__ float rsqrt_ftz(float v) {
     float r;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float sqrt_ftz(float v) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
 __device__ __forceinline__ F2 both(float v) { return pack2(v, v); }
@@ -66,37 +65,54 @@ __device__ __forceinline__ void sigmoids2(F2 v, F2 &s, F2 &n) {
 // a = 2^t and n = 1 - a for t <= 0, both to a few roundings of themselves: with t = k + f, k
 // whole and |f| <= 1/2, a = 2^k + 2^k p and n = (1 - 2^k) - 2^k p, where p = 2^f - 1 is a
 // polynomial in f without a constant term (off by 2.1e-8 of itself at most), so that n keeps its
-// bits where a is next to 1. Below 2^-126 a is 2^-126.
-__device__ __forceinline__ void decay_factor2(F2 t, F2 &a, F2 &n) {
+// bits where a is next to 1. 2^k is exact from the exponential's instruction, 0 below 2^-126.
+__device__ __forceinline__ F2 decay_scale2(F2 t, F2 &p) {
     constexpr float shift = 12582912.f;                // 1.5 2^23: rounds to whole numbers
-    float t0, t1, r0, r1;
-    unpack2(t, t0, t1);
-    t = pack2(max_nan(t0, -126.f), max_nan(t1, -126.f));
-    const F2 r = add2(t, both(shift));
-    const F2 f = add2(t, mul2(add2(r, both(-shift)), both(-1.f)));
-    unpack2(r, r0, r1);
-    const F2 scale = pack2(__int_as_float((__float_as_int(r0) << 23) + (127 << 23)),
-                           __int_as_float((__float_as_int(r1) << 23) + (127 << 23)));
-    F2 p = fma2(both(1.54035122e-4f), f, both(1.33907353e-3f));
+    const F2 k = add2(add2(t, both(shift)), both(-shift));
+    const F2 f = fma2(k, both(-1.f), t);
+    float k0, k1;
+    unpack2(k, k0, k1);
+    p = fma2(both(1.54035122e-4f), f, both(1.33907353e-3f));
     p = fma2(p, f, both(9.61823761e-3f));
     p = fma2(p, f, both(5.55035733e-2f));
     p = fma2(p, f, both(2.40226492e-1f));
     p = fma2(p, f, both(6.93147182e-1f));
     p = mul2(p, f);
-    a = fma2(scale, p, scale);
-    const F2 minus = mul2(scale, both(-1.f));
-    n = fma2(minus, p, add2(minus, both(1.f)));
+    return pack2(exp2_ftz(k0), exp2_ftz(k1));
+}
+__device__ __forceinline__ F2 decay_factor2(F2 t) {
+    F2 p;
+    const F2 scale = decay_scale2(t, p);
+    return fma2(scale, p, scale);
+}
+__device__ __forceinline__ void decay_factor2(F2 t, F2 &a, F2 &n) {
+    F2 p;
+    const F2 scale = decay_scale2(t, p), w = mul2(scale, p);
+    a = add2(scale, w);
+    n = fma2(w, both(-1.f), fma2(scale, both(-1.f), both(1.f)));
 }
 
-// The input's factor m of a and n = 1 - a, and its reciprocal where it is a root; both 0 where 1 -
-// a^2 is below the normal range, where the instruction takes it for 0.
+// The form of a problem: what its kernels know when they are compiled. kAnyForm's kernels ask the
+// problem instead, and take outputs of an odd number of channels.
+constexpr int kForms = 12, kAnyForm = -1;
+constexpr int recur_form(bool gated, bool rated, int scaling) { return scaling * 4 + rated * 2 + gated; }
+
+template <int FORM, typename P>
+__device__ __forceinline__ bool is_gated(const P &p) { return FORM < 0 ? p.gate != nullptr : FORM & 1; }
+template <int FORM, typename P>
+__device__ __forceinline__ bool is_rated(const P &p) { return FORM < 0 ? p.rate != nullptr : (FORM >> 1) & 1; }
+template <int FORM, typename P>
+__device__ __forceinline__ int scaling_of(const P &p) { return FORM < 0 ? p.scaling : FORM >> 2; }
+
+// The input's factor m of a and n = 1 - a, and its reciprocal where it is a root; where 1 - a^2 is
+// below the normal range m is below 2^-63 and the reciprocal 2^63.
 __device__ __forceinline__ F2 input_factor2(F2 a, F2 n, int scaling, F2 &inverse) {
     if (scaling == GDN_RECUR_ROOT) {
+        constexpr float tiny = 1.17549435e-38f;
         const F2 v = fma2(n, a, n);                    // 1 - a^2
         float v0, v1;
         unpack2(v, v0, v1);
-        constexpr float tiny = 1.17549435e-38f;
-        inverse = pack2(v0 >= tiny ? rsqrt_ftz(v0) : 0.f, v1 >= tiny ? rsqrt_ftz(v1) : 0.f);
+        inverse = pack2(rsqrt_ftz(fmaxf(v0, tiny)), rsqrt_ftz(fmaxf(v1, tiny)));
         return mul2(v, inverse);
     }
     return scaling == GDN_RECUR_COMPLEMENT ? n : both(1.f);
@@ -109,30 +125,28 @@ __device__ __forceinline__ F2 pair_of(const __nv_bfloat16 *p) {
 }
 __device__ __forceinline__ F2 pair_of(const float *p) { return *reinterpret_cast<const F2 *>(p); }
 
-// Stores channels c and c + 1 (those below D) of a row, rounded.
-__device__ __forceinline__ void store_pair(__nv_bfloat16 *row, int c, int D, bool pairs, F2 v) {
+// Channels c and c + 1 of a row of D, those that are there: `pairs` where D is even.
+__device__ __forceinline__ F2 load_pair(const float *row, int c, int D, bool pairs) {
+    if (pairs) return c < D ? *reinterpret_cast<const F2 *>(row + c) : both(0.f);
+    return pack2(c < D ? row[c] : 0.f, c + 1 < D ? row[c + 1] : 0.f);
+}
+__device__ __forceinline__ void store_pair(float *at, F2 v) { *reinterpret_cast<F2 *>(at) = v; }
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *at, F2 v) {
     float a, b;
     unpack2(v, a, b);
-    if (pairs) {
-        if (c < D) *reinterpret_cast<__nv_bfloat162 *>(row + c) = __floats2bfloat162_rn(a, b);
-    } else {
-        if (c < D) row[c] = __float2bfloat16_rn(a);
-        if (c + 1 < D) row[c + 1] = __float2bfloat16_rn(b);
-    }
+    *reinterpret_cast<__nv_bfloat162 *>(at) = __floats2bfloat162_rn(a, b);
 }
-__device__ __forceinline__ void store_pair(float *row, int c, int D, bool pairs, F2 v) {
+// `there`: of the pair's first channel, in a row that is to be written.
+template <typename S>
+__device__ __forceinline__ void store_pair(S *at, F2 v, bool there, bool second, bool pairs) {
     if (pairs) {
-        if (c < D) *reinterpret_cast<F2 *>(row + c) = v;
+        if (there) store_pair(at, v);
     } else {
         float a, b;
         unpack2(v, a, b);
-        if (c < D) row[c] = a;
-        if (c + 1 < D) row[c + 1] = b;
+        if (there) at[0] = from_f32<S>(a);
+        if (there && second) at[1] = from_f32<S>(b);
     }
-}
-__device__ __forceinline__ F2 load_pair(const float *row, int c, int D, bool pairs) {
-    if (pairs && c < D) return *reinterpret_cast<const F2 *>(row + c);
-    return pack2(c < D ? row[c] : 0.f, c + 1 < D ? row[c + 1] : 0.f);
 }
 
 // A warp's tile of one tensor: kRecurEvery rows of kRecurChannels values.
@@ -193,47 +207,72 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, const Through &v) {
 }
 
 // The exchange of a tile: every warp gives its (A, H) and receives the state that its part
-// starts from; `state`, the one before all parts, moves on to the one behind them. Parts
-// are in time's order, or in the reverse one (REVERSE), by warp and, above that, by rank.
+// starts from. Parts are in time's order, or in the reverse one (REVERSE), by warp and, above
+// that, by rank. The state before all parts passes on from tile to tile: within a block
+// through `state`, which the last warp writes and the others read behind the next
+// tile's barrier; in a cluster every thread takes it through all blocks' (A, H).
+template <int WARPS>
 struct Exchange {
-    Through warps[2][kMaxWarps][32], ranks[2][kMaxRanks][32];
+    Through warps[2][WARPS][32], ranks[2][kMaxRanks][32];
+    F2 state[2][32];
 };
 
-template <bool REVERSE>
-__device__ __forceinline__ F2 exchange(Exchange &e, int turn, int ranks, int rank, const Through &mine, F2 &state) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-    Through(&part)[kMaxWarps][32] = e.warps[turn & 1];
-    part[warp][lane] = mine;
-    __syncthreads();
-    F2 from = state;
-    if (ranks > 1) {
-        Through(&blocks)[kMaxRanks][32] = e.ranks[turn & 1];
-        if (warp == 0) {
-            Through all = {both(1.f), both(0.f)};
-            for (int i = 0; i < warps; ++i) {
-                const Through &w = part[REVERSE ? warps - 1 - i : i][lane];
-                all.h = fma2(w.a, all.h, w.h);
-                all.a = mul2(w.a, all.a);
+template <bool REVERSE, int WARPS>
+struct Scan {
+    Exchange<WARPS> &e;
+    int warps, ranks, rank, lane, place;               // place: the warp's, in order
+    F2 state;                                          // of a cluster: before the next tile
+
+    __device__ __forceinline__ Scan(Exchange<WARPS> &e, int ranks, int rank, F2 state)
+        : e(e), warps(blockDim.x / 32), ranks(ranks), rank(REVERSE ? ranks - 1 - rank : rank),
+          lane(threadIdx.x % 32), state(state) {
+        place = REVERSE ? warps - 1 - static_cast<int>(threadIdx.x / 32) : threadIdx.x / 32;
+        if (place == 0) e.state[0][lane] = state;
+        if (ranks > 1) ptx::cluster_sync();            // all blocks are there to be written to
+    }
+    __device__ __forceinline__ F2 step(int turn, const Through &mine) {
+        const int now = turn & 1;
+        e.warps[now][place][lane] = mine;
+        __syncthreads();
+        F2 from;
+        if (ranks == 1) {
+            from = e.state[now][lane];
+        } else {
+            if (place == 0) {
+                Through all = mine;
+                for (int w = 1; w < warps; ++w) {
+                    const Through &o = e.warps[now][w][lane];
+                    all.h = fma2(o.a, all.h, o.h);
+                    all.a = mul2(o.a, all.a);
+                }
+                const uint32_t addr = ptx::smem_u32(&e.ranks[now][rank][lane]);
+                for (int r = 0; r < ranks; ++r) store_cluster(ptx::mapa_shared(addr, r), all);
             }
-            const uint32_t addr = ptx::smem_u32(&blocks[rank][lane]);
-            for (int r = 0; r < ranks; ++r) store_cluster(ptx::mapa_shared(addr, r), all);
+            ptx::cluster_sync();
+            from = state;
+#pragma unroll
+            for (int r = 0; r < kMaxRanks; ++r) {
+                if (r >= ranks) break;
+                const Through &o = e.ranks[now][r][lane];
+                if (r == rank) from = state;
+                state = fma2(o.a, state, o.h);
+            }
         }
-        ptx::cluster_sync();
-        for (int i = 0; i < ranks; ++i) {
-            const int r = REVERSE ? ranks - 1 - i : i;
-            if (r == rank) from = state;
-            state = fma2(blocks[r][lane].a, state, blocks[r][lane].h);
+#pragma unroll
+        for (int w = 0; w < WARPS - 1; ++w) {
+            if (w >= place) break;
+            const Through &o = e.warps[now][w][lane];
+            from = fma2(o.a, from, o.h);
         }
+        if (ranks == 1 && place == warps - 1) e.state[now ^ 1][lane] = fma2(mine.a, from, mine.h);
+        return from;
     }
-    F2 start = from;
-    for (int i = 0; i < warps; ++i) {
-        const int w = REVERSE ? warps - 1 - i : i;
-        if (w == warp) start = from;
-        from = fma2(part[w][lane].a, from, part[w][lane].h);
+    // The state behind `turns` tiles, for the lanes of any warp of any block.
+    __device__ __forceinline__ F2 last(int turns) {
+        __syncthreads();
+        return ranks == 1 ? e.state[turns & 1][lane] : state;
     }
-    if (ranks == 1) state = from;
-    return start;
-}
+};
 
 inline gdn_status recur_check(const gdn_recur_problem *p) {
     if (!p) return GDN_ERR_INVALID_ARG;
@@ -295,14 +334,15 @@ void recur_alignment(RecurParams<E> &p) {
 // Warps to a block: as many as a sequence's tokens fill, up to `most`. Blocks to a cluster: as
 // many as leave the GPU's `places` for blocks filled once, and have tokens.
 template <typename E>
-void recur_shape(RecurParams<E> &p, int most, int places, int &warps) {
-    warps = 1;
+int recur_shape(RecurParams<E> &p, int most, int places) {
+    int warps = 1;
     while (warps < most && static_cast<int64_t>(warps) * kRecurEvery < p.T) ++warps;
     const int64_t blocks = static_cast<int64_t>(p.B) * ((p.D + kRecurChannels - 1) / kRecurChannels);
     p.ranks = 1;
     while (p.ranks < kMaxRanks && blocks * p.ranks * 2 <= places &&
            p.T > static_cast<int64_t>(p.ranks) * warps * kRecurEvery)
         p.ranks *= 2;
+    return warps;
 }
 
 template <typename E>
@@ -323,6 +363,12 @@ cudaError_t recur_launch(void (*kernel)(RecurParams<E>), const RecurParams<E> &p
     cfg.attrs = attr;
     cfg.numAttrs = p.ranks > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// The kernel of a problem's form, of a table that begins with kAnyForm's.
+template <typename E, typename K>
+K recur_kernel(const K (&table)[kForms + 1], const RecurParams<E> &p) {
+    return table[p.pairs ? 1 + recur_form(p.gate, p.rate, p.scaling) : 0];
 }
 
 }  // namespace gdn
