@@ -7,7 +7,7 @@
 
 namespace gdn {
 
-constexpr int kColumnLanes = 32, kColumnRows = 8;
+constexpr int kColumnLanes = 32, kColumnRows = 32;
 
 // part [rows, cols] -> first[0 .. split), second[0 .. cols - split); either may be NULL. A
 // thread adds every kColumnRows-th row of one column, then those sums are added in order.
@@ -17,6 +17,7 @@ static __global__ void __launch_bounds__(kColumnLanes * kColumnRows)
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kColumnLanes + threadIdx.x;
     float s = 0.f;
     if (c < cols)
+#pragma unroll 4
         for (int r = threadIdx.y; r < rows; r += kColumnRows) s += part[r * cols + c];
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const 
 }
 
 size_t bwd_workspace(const gdn_recur_problem *p) {
-    return align_up(static_cast<size_t>(p->B) * kMaxRanks * p->D * 4);
+    return p->T ? align_up(static_cast<size_t>(p->B) * kMaxRanks * p->D * 4) : 0;
 }
 
 template <typename E, int... FORMS>
@@ -181,7 +181,7 @@ GDN_API gdn_status gdn_recur_bwd(const gdn_recur_problem *p, const void *dy, con
         if (!is_aligned(ptr, e)) return GDN_ERR_ALIGNMENT;
     if (!is_aligned(lengths, 4)) return GDN_ERR_ALIGNMENT;
     const size_t need = bwd_workspace(p);
-    if (!workspace || workspace_bytes < need) return GDN_ERR_WORKSPACE;
+    if (need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
     const size_t rows = static_cast<size_t>(p->B) * p->D, all = rows * p->T * e;
     const size_t chunks = (static_cast<size_t>(p->T) + kRecurEvery - 1) / kRecurEvery;
     const Span in[] = {Span(dy, strided_bytes(p->B, p->T, p->D, p->dy_stride_b, p->dy_stride_t, e)),

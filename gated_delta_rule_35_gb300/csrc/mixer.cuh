@@ -170,6 +170,12 @@ __device__ __forceinline__ void copy4_async(void *smem, const void *g) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
                      static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(g) : "memory");
 }
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *smem, const void *g) {
+    static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "cp.async");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(g), "n"(BYTES) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");

@@ -337,8 +337,8 @@ def conv_bwd(dy, x, weight, bias=None, state=None, act: str = "silu", d_final_st
 
     dy [B,T,C] in x's dtype, strided, is the gradient of y, ``d_final_state`` [B,W-1,C] in
     x's dtype that of the returned state (None: zeros); the other inputs as given to
-    conv_fwd. ``d_state=d_final_state`` writes in place. ``workspace``
-    (conv_bwd_workspace_bytes) and the gradients may be passed to reuse buffers."""
+    conv_fwd. ``workspace`` (conv_bwd_workspace_bytes) and the gradients may be passed to reuse
+    buffers."""
     return _conv_bwd(x, dy, weight, bias, state, act, d_final_state, lengths, workspace, dx, d_weight, d_bias,
                      d_state, stream=stream)
 

@@ -483,8 +483,8 @@ GDN_API gdn_status gdn_group_norm(const gdn_group_norm_problem *p, const void *x
  *    tokens, written, not added to: fp32, taken in an order that depends on the sizes
  *    alone. Their blocks' parts pass through the workspace, which two calls that may
  *    overlap on the GPU (two captured graphs among them) cannot share. The
- *    *_workspace_bytes functions depend on the sizes and the dtype alone and give SIZE_MAX
- *    for an invalid problem.
+ *    *_workspace_bytes functions depend on the sizes and the dtype alone; they give 0 for T = 0
+ *    (the workspace may be NULL then) and SIZE_MAX for an invalid problem.
  * ------------------------------------------------------------------------- */
 
 /* Gated linear recurrence: every channel is a state of its own with a decay and an input
@@ -585,7 +585,7 @@ GDN_API gdn_status gdn_layer_norm_bwd(const gdn_layer_norm_problem *p, const voi
  * d_state_in is the gradient of the window state, laid out like it.
  *  - x, weight, bias, state_in and lengths as in the forward pass. dy strided; dx [B,T,C],
  *    d_state_out and d_state_in (each or NULL) [B,W-1,C] in `dtype`; d_weight [C,W],
- *    d_bias [C] (or NULL) fp32. d_state_in may be d_state_out itself.
+ *    d_bias [C] (or NULL) fp32.
  *  - The forward pass's limits. T = 0: d_state_in = d_state_out, d_weight = d_bias = 0. */
 typedef struct {
     int32_t B, T, C, W;

@@ -129,7 +129,7 @@ def test_norm_bwd_refusals(kw, status):
     *[({n: fake(CONV_BWD.index(n)) + 1}, ALIGNMENT) for n in ("dy", "x", "lengths")],
     *[({n: fake(CONV_BWD.index(n)) + 8}, ALIGNMENT) for n in CONV_BWD if n not in ("dy", "x", "lengths")],
     *[({o: fake(CONV_BWD.index(n))}, INVALID) for o in ("dx", "d_weight", "d_bias", "d_state_in", "workspace")
-      for n in CONV_BWD if n != o and (o, n) != ("d_state_in", "d_state_out")],
+      for n in CONV_BWD if n != o],
     (dict(d_state_in=fake(CONV_BWD.index("d_state_out")) + 16), INVALID),
 ])
 def test_conv_bwd_refusals(kw, status):

@@ -377,9 +377,7 @@ def test_conv_bwd(size, W, dtype):
             want["d_state"] = None
         checked(dict(dx=dx, d_weight=dw, d_bias=db, d_state=ds), want, bound, dict(dx=dtype, d_state=dtype))
         untouched(dx, want["dx"], FILL)
-        # outputs of its own, the window's gradient in place
-        d = None if dlast is None else dlast.clone()
-        again = gdn.conv_bwd(dy, x, w, b, st, act, d, n, d_state=d if state else None)
+        again = gdn.conv_bwd(dy, x, w, b, st, act, dlast, n)       # outputs of its own
         live = ~torch.from_numpy(np.isnan(want["dx"])).cuda()
         assert torch.equal(again[0][live], dx[live]) and (again[0][~live] == 0).all()
         for a, c in zip(again[1:], (dw, db, ds)):
