@@ -10,20 +10,21 @@ namespace gdn {
 constexpr int kColumnLanes = 32, kColumnRows = 32;
 
 // part [rows, cols] -> first[0 .. split), second[0 .. cols - split); either may be NULL. A
-// thread adds every kColumnRows-th row of one column, then those sums are added in order.
+// thread adds every blockDim.y-th row of one column, then those sums are added in order.
+// Launched while the kernel before it still runs, whose end it waits for.
 static __global__ void __launch_bounds__(kColumnLanes * kColumnRows)
     gdn_column_sums_kernel(const float *part, int rows, int64_t cols, int64_t split, float *first, float *second) {
     __shared__ float sums[kColumnRows][kColumnLanes];
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kColumnLanes + threadIdx.x;
+    ptx::griddep_wait();
     float s = 0.f;
     if (c < cols)
-#pragma unroll 4
-        for (int r = threadIdx.y; r < rows; r += kColumnRows) s += part[r * cols + c];
+#pragma unroll 8
+        for (int r = threadIdx.y; r < rows; r += blockDim.y) s += part[r * cols + c];
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y != 0 || c >= cols) return;
-#pragma unroll
-    for (int r = 1; r < kColumnRows; ++r) s += sums[r][threadIdx.x];
+    for (int r = 1; r < blockDim.y; ++r) s += sums[r][threadIdx.x];
     if (c < split) {
         if (first) first[c] = s;
     } else if (second) {
@@ -31,12 +32,21 @@ static __global__ void __launch_bounds__(kColumnLanes * kColumnRows)
     }
 }
 
+// About eight rows to a thread: 64 rows of 40960 columns 12.0 us with two.
 static inline cudaError_t column_sums(const float *part, int rows, int64_t cols, int64_t split, float *first,
                                       float *second, cudaStream_t s) {
-    const unsigned blocks = static_cast<unsigned>((cols + kColumnLanes - 1) / kColumnLanes);
-    gdn_column_sums_kernel<<<blocks, dim3(kColumnLanes, kColumnRows), 0, s>>>(part, rows, cols, split, first,
-                                                                              second);
-    return cudaGetLastError();
+    unsigned y = 1;
+    while (y < kColumnRows && y * 8 < static_cast<unsigned>(rows)) y *= 2;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((cols + kColumnLanes - 1) / kColumnLanes));
+    cfg.blockDim = dim3(kColumnLanes, y);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gdn_column_sums_kernel, part, rows, cols, split, first, second);
 }
 
 }  // namespace gdn

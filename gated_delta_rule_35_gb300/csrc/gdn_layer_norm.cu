@@ -1,27 +1,27 @@
-// Layer norm of every token and its backward pass: gdn_layer_norm and gdn_layer_norm_bwd of
-// include/gdn.h.
+// Layer norm of every token and its backward pass: gdn_layer_norm and gdn_layer_norm_bwd
+// of include/gdn.h.
 //
-// Bound by memory: x read and y written; in the backward pass x and dy read and dx written. A row
-// is held by `lanes` threads (a power of two) in pieces of V channels (16 bytes, or one channel
-// where rows are not whole 16-byte pieces), P to a thread, while its sums are taken:
-//   gdn_layer_norm_kernel      a row from registers: the mean, the squares about it, the output;
-//   gdn_layer_norm_bwd_kernel  blocks that stay for many rows. A thread keeps its channels, so
-//                              the sums over rows that are the gradients of weight and bias
-//                              stay in its registers; the next rows are on their way to shared
-//                              memory meanwhile. Every block leaves a row of partial sums.
-//   the *_wide_* kernels       rows beyond what a block holds: a block to a row that it reads
-//                              again for each sum, the sums over rows apart.
-#include <utility>
-
+// Bound by memory: x read and y written; in the backward pass x and dy read and dx written. Blocks
+// stay for many rows. A row is held by `lanes` threads (a power of two) in pieces of V channels
+// (16 bytes, or one channel where rows are not whole 16-byte pieces), P to a thread, which keeps its
+// channels: weight and bias stay in registers, and so do the sums over rows that are their
+// gradients, of which every block leaves a row of partial sums. The rows of the next turns are on
+// their way to shared memory meanwhile (cp.async, a ring of a thread's own). A turn takes R
+// rows, whose sums over threads share their shuffles and barriers: the mean, then the squares
+// about it; in the backward pass both sums at once. Rows beyond what a block holds go to the
+// *_wide_* kernels, a block to a row that it reads again for each sum.
 #include "columns.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxLanes = 512;     // threads to a row
 constexpr int kWideParts = 64;     // rows of partial sums of the wide kernels
-constexpr int kMaxParts = 152 * 3; // blocks of the backward pass
+constexpr int kMaxParts = 152 * 2; // blocks of the backward pass
+
+// Blocks to an SM. Of the backward pass three would spill: 302 us for 257 on 65536 x 4096 bf16; of
+// the forward pass two leave too few rows on their way: 203 us for 182.
+constexpr int blocks_to_sm(int P, int threads, int tensors) { return threads * P > 512 ? 1 : tensors == 1 ? 3 : 2; }
 
 template <typename E>
 struct LayerNormParams {
@@ -38,7 +38,7 @@ struct LayerNormParams {
 
 __device__ __forceinline__ F2 both(float v) { return pack2(v, v); }
 
-// Channels c.. of a parameter, 1 without any.
+// Channels c.. of a parameter, `other` without any.
 template <int V>
 __device__ __forceinline__ void params(const float *p, int c, float other, F2 (&f)[(V + 1) / 2]) {
     float v[V];
@@ -60,27 +60,53 @@ __device__ __forceinline__ float halves(F2 v) {
     return V == 1 ? a : a + b;
 }
 
-// Sums over the `lanes` threads of a row, of N values at once, for all of them. Two calls in a
-// row take different `buffer`s.
+// Sums of N values over the `lanes` threads of a row, for all of them. Within a warp the values
+// are shared out over the lanes as the sums go on: 6 shuffles for four values, not 20. Calls in a
+// row alternate between two `buffer`s.
 template <int N, int WARPS>
 __device__ __forceinline__ void row_sums(float (&v)[N], int lanes, float (&buffer)[WARPS][N]) {
+    static_assert(N == 1 || N == 2 || N == 4, "values");
+    constexpr uint32_t all = 0xffffffffu;
+    if (lanes < 32) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (o >= lanes) continue;                      // alike for all threads
+        for (int o = 16; o > 0; o >>= 1) {
+            if (o >= lanes) continue;                  // alike for all threads
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(all, v[i], o);
+        }
+        return;
     }
-    if (lanes <= 32) return;
-    const int warp = threadIdx.x / 32, first = warp & ~(lanes / 32 - 1);
-    if (threadIdx.x % 32 == 0)
+    const int lane = threadIdx.x % 32;
+    int o = 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) buffer[warp][i] = v[i];
+    for (int n = N; n > 1; n /= 2, o /= 2) {           // half of the values to each half of the lanes
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float give = upper ? v[i] : v[i + n / 2], keep = upper ? v[i + n / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(all, give, o);
+        }
+    }
+    float s = v[0];
+#pragma unroll
+    for (int q = 16 / N; q > 0; q /= 2) s += __shfl_xor_sync(all, s, q);
+    constexpr int per = 32 / N;                        // lanes that hold a value's sum
+    if (lanes == 32) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(all, s, i * per);
+        return;
+    }
+    const int warp = threadIdx.x / 32, warps = lanes / 32, first = warp & ~(warps - 1);
+    if (lane % per == 0) buffer[warp][lane / per] = s;
     __syncthreads();
+    // value i of warp w at i + N w: a lane takes every 32nd
+    const float *from = &buffer[first][0];
+    const int count = warps * N;
+    s = from[lane & (count - 1)];
+    if (count > 32) s += from[lane + 32];
+    for (int q = N; q < 32 && q < count; q *= 2) s += __shfl_xor_sync(all, s, q);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-    for (int w = 0; w < lanes / 32; ++w)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += buffer[first + w][i];
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(all, s, i);
 }
 
 // A row's sequence and token.
@@ -94,216 +120,284 @@ __device__ __forceinline__ bool is_valid(const LayerNormParams<E> &p, int b, int
     return !p.lengths || t < p.lengths[b];
 }
 
-template <typename E, int V, int P>
-__global__ void __launch_bounds__(kMaxLanes) gdn_layer_norm_kernel(const LayerNormParams<E> p) {
-    __shared__ float buffers[2][kMaxLanes / 32][1];
-    constexpr int N = (V + 1) / 2;
-    const int lanes = p.lanes, lane = threadIdx.x & (lanes - 1);
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
-    bool live = at < p.rows;
-    const int row = live ? static_cast<int>(at) : 0;
-    int b, t;
-    locate(p, row, b, t);
-    live = live && is_valid(p, b, t);
-    const E *x = p.x + b * p.x_sb + t * p.x_st;
-    Piece<E, V> r[P];
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-        const int c = (q * lanes + lane) * V;
-        r[q].zero();
-        if (live && c < p.C) r[q].load_rw(x + c);
-    }
-    const float inv = 1.f / p.C;
-    float mean = 0.f, s[1];
-    if (!p.rms) {
-        F2 sum = both(0.f);
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-            F2 v[N];
-            r[q].widen(v);
-#pragma unroll
-            for (int k = 0; k < N; ++k) sum = add2(sum, v[k]);
-        }
-        s[0] = halves<V>(sum);
-        row_sums(s, lanes, buffers[0]);
-        mean = s[0] * inv;
-    }
-    const F2 minus = both(-mean);
-    F2 sum = both(0.f);
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-        F2 v[N], sq = both(0.f);
-        r[q].widen(v);
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            v[k] = add2(v[k], minus);
-            sq = fma2(v[k], v[k], sq);
-        }
-        if ((q * lanes + lane) * V < p.C) sum = add2(sum, sq);
-    }
-    s[0] = halves<V>(sum);
-    row_sums(s, lanes, buffers[1]);
-    const float rstd = rsqrtf(fmaf(s[0], inv, p.eps));
-    if (!live) return;
-    E *y = p.y + static_cast<int64_t>(row) * p.C;
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-        const int c = (q * lanes + lane) * V;
-        if (c >= p.C) break;
-        F2 v[N], w[N], bias[N];
-        params<V>(p.w, c, 1.f, w);
-        params<V>(p.bias, c, 0.f, bias);
-        r[q].widen(v);
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = fma2(mul2(add2(v[k], minus), both(rstd)), w[k], bias[k]);
-        r[q].round(v);
-        r[q].store(y + c);
-    }
-    if (p.stats && lane == 0) *reinterpret_cast<float2 *>(p.stats + 2LL * row) = make_float2(mean, rstd);
-}
+// The rows of a block and their ring, for TENSORS of them (x, then dy): two rows a turn where three
+// turns of them fit (one: 220 us for 182, 65536 x 4096 bf16), else one.
+template <typename E, int V, int P, int THREADS, int TENSORS>
+struct RowRing {
+    // a piece, or an element: 4 bytes, the least that an asynchronous copy moves
+    using Slot = typename std::conditional<V == 1, float, uint4>::type;
+    static constexpr int N = (V + 1) / 2;
+    static constexpr int row_bytes = THREADS * TENSORS * P * static_cast<int>(sizeof(Slot));
+    static constexpr int R = 6 * row_bytes <= 100 * 1024 ? 2 : 1;
+    static constexpr int stages = 3 * R * row_bytes <= 200 * 1024 ? (R == 2 && TENSORS == 2 ? 2 : 3) : 1;
+    static constexpr int bytes = stages * R * row_bytes;
+    static_assert(bytes >= THREADS * V * 4, "the ring holds a piece of sums of every thread");
 
-// Rows of a thread in the ring: three, or the one that its block's shared memory holds.
-constexpr int row_bytes(int V, int P, int threads) { return threads * 2 * P * (V == 1 ? 4 : 16); }
-constexpr int row_stages(int V, int P, int threads) { return 3 * row_bytes(V, P, threads) <= 200 * 1024 ? 3 : 1; }
+    const LayerNormParams<E> &p;
+    Slot *mine;
+    int lane, lanes, step, turns;
+    int64_t first;
+
+    __device__ __forceinline__ RowRing(const LayerNormParams<E> &p, uint4 *memory)
+        : p(p), mine(reinterpret_cast<Slot *>(memory) + threadIdx.x), lane(threadIdx.x & (p.lanes - 1)),
+          lanes(p.lanes) {
+        const int per_block = THREADS / lanes;
+        step = gridDim.x * per_block;
+        // alike for all threads
+        turns = static_cast<int>((p.rows + static_cast<int64_t>(R) * step - 1) / (static_cast<int64_t>(R) * step));
+        first = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / lanes;
+    }
+    __device__ __forceinline__ int channel(int q) const { return (q * lanes + lane) * V; }
+    // Asks for the rows of turn i; those that there are (-1: none).
+    __device__ __forceinline__ void fetch(int i, int stage, int (&rows)[R]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = first + (static_cast<int64_t>(i) * R + r) * step;
+            int b = 0, t = 0;
+            rows[r] = -1;
+            if (at < p.rows) {
+                locate(p, static_cast<int>(at), b, t);
+                if (is_valid(p, b, t)) rows[r] = static_cast<int>(at);
+            }
+            Slot *to = slot(stage, r, 0, 0);
+#pragma unroll
+            for (int n = 0; n < TENSORS; ++n) {
+                const E *from = n == 0 ? p.x + (b * p.x_sb + t * p.x_st) : p.dy + (b * p.dy_sb + t * p.dy_st);
+#pragma unroll
+                for (int q = 0; q < P; ++q, to += THREADS) {
+                    const int c = channel(q);
+                    if (rows[r] >= 0 && c < p.C) {
+                        if constexpr (V > 1)
+                            copy16_async(to, from + c);
+                        else if constexpr (sizeof(E) == 4)
+                            copy4_async(to, from + c);
+                        else
+                            *to = to_f32(from[c]);
+                    } else {
+                        memset(to, 0, sizeof(Slot));
+                    }
+                }
+            }
+        }
+        copy_commit();
+    }
+    __device__ __forceinline__ Slot *slot(int stage, int r, int n, int q) const {
+        return mine + (((stage * R + r) * TENSORS + n) * P + q) * THREADS;
+    }
+    __device__ __forceinline__ void read(int stage, int r, int n, int q, F2 (&f)[N]) const {
+        if constexpr (V == 1) {
+            f[0] = both(*slot(stage, r, n, q));
+        } else {
+            Piece<E, V> piece;
+            piece.raw = *slot(stage, r, n, q);
+            piece.widen(f);
+        }
+    }
+};
 
 template <typename E, int V, int P, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS * P <= 512 ? 3 : 1)
-    gdn_layer_norm_bwd_kernel(const LayerNormParams<E> p) {
-    constexpr int kStages = row_stages(V, P, THREADS);
-    __shared__ float buffers[2][THREADS / 32][2];
+__global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
+    gdn_layer_norm_kernel(const LayerNormParams<E> p) {
+    using Ring = RowRing<E, V, P, THREADS, 1>;
+    constexpr int N = Ring::N, R = Ring::R, S = Ring::stages;
+    __shared__ float buffers[2][THREADS / 32][R];
     extern __shared__ uint4 ring_memory[];
-    constexpr int N = (V + 1) / 2;
-    using Slot = typename std::conditional<V == 1, float, uint4>::type;    // a piece, or an element's 4 bytes
-    // [stage][x, dy][piece][thread]: a thread fills and reads its own slots
-    Slot *mine = reinterpret_cast<Slot *>(ring_memory) + threadIdx.x;
-    const int lanes = p.lanes, lane = threadIdx.x & (lanes - 1), per_block = THREADS / lanes;
-    const int step = gridDim.x * per_block;
-    const int turns = (p.rows + step - 1) / step;      // alike for all threads
+    Ring ring(p, ring_memory);
+    const float inv = 1.f / p.C;
+    // 16 channels' weight and bias stay in registers, more are read for every row
+    constexpr bool KEEP = P * V <= 16;
+    F2 w[KEEP ? P : 1][N], bias[KEEP ? P : 1][N];
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const int c = ring.channel(q) < p.C ? ring.channel(q) : 0;
+            params<V>(p.w, c, 1.f, w[q]);
+            params<V>(p.bias, c, 0.f, bias[q]);
+        }
+    }
+    int rows[S][R];
+#pragma unroll
+    for (int i = 0; i < S; ++i) ring.fetch(i, i, rows[i]);
+    int stage = 0;
+    for (int i = 0; i < ring.turns; ++i) {
+        copy_wait<S - 1>();
+        float mean[R], s[R];
+        F2 sum[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = 0.f;
+            sum[r] = both(0.f);
+        }
+        if (!p.rms) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int q = 0; q < P; ++q) {
+                    F2 v[N];
+                    ring.read(stage, r, 0, q, v);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) sum[r] = add2(sum[r], v[k]);
+                }
+                s[r] = halves<V>(sum[r]);
+                sum[r] = both(0.f);
+            }
+            row_sums(s, ring.lanes, buffers[0]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) mean[r] = s[r] * inv;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                F2 v[N], squares = both(0.f);
+                ring.read(stage, r, 0, q, v);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    v[k] = add2(v[k], both(-mean[r]));
+                    squares = fma2(v[k], v[k], squares);
+                }
+                if (ring.channel(q) < p.C) sum[r] = add2(sum[r], squares);
+            }
+            s[r] = halves<V>(sum[r]);
+        }
+        // without the first sums the buffers alternate from turn to turn
+        row_sums(s, ring.lanes, buffers[p.rms ? i & 1 : 1]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = rows[0][r];
+            if (row < 0) continue;
+            const float rstd = rsqrtf(fmaf(s[r], inv, p.eps));
+            E *y = p.y + static_cast<int64_t>(row) * p.C;
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const int c = ring.channel(q);
+                if (c >= p.C) break;
+                F2 v[N];
+                ring.read(stage, r, 0, q, v);
+                constexpr int one = KEEP ? 1 : 0;
+                if constexpr (!KEEP) {
+                    params<V>(p.w, c, 1.f, w[0]);
+                    params<V>(p.bias, c, 0.f, bias[0]);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    v[k] = fma2(mul2(add2(v[k], both(-mean[r])), both(rstd)), w[q * one][k], bias[q * one][k]);
+                Piece<E, V> piece;
+                piece.round(v);
+                piece.store(y + c);
+            }
+            if (p.stats && ring.lane == 0)
+                *reinterpret_cast<float2 *>(p.stats + 2LL * row) = make_float2(mean[r], rstd);
+        }
+#pragma unroll
+        for (int k = 0; k + 1 < S; ++k)
+#pragma unroll
+            for (int r = 0; r < R; ++r) rows[k][r] = rows[k + 1][r];
+        ring.fetch(i + S, stage, rows[S - 1]);
+        stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+}
+
+template <typename E, int V, int P, int THREADS>
+__global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 2))
+    gdn_layer_norm_bwd_kernel(const LayerNormParams<E> p) {
+    using Ring = RowRing<E, V, P, THREADS, 2>;
+    constexpr int N = Ring::N, R = Ring::R, S = Ring::stages;
+    __shared__ float buffers[2][THREADS / 32][2 * R];
+    extern __shared__ uint4 ring_memory[];
+    Ring ring(p, ring_memory);
     const float inv = 1.f / p.C;
     F2 w[P][N], dw[P][N], db[P][N];
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-        const int c = (q * lanes + lane) * V;
+        const int c = ring.channel(q);
 #pragma unroll
-        for (int k = 0; k < N; ++k) w[q][k] = dw[q][k] = db[q][k] = both(0.f);
-        if (c < p.C) params<V>(p.w, c, 1.f, w[q]);
+        for (int k = 0; k < N; ++k) dw[q][k] = db[q][k] = both(0.f);
+        params<V>(p.w, c < p.C ? c : 0, 1.f, w[q]);
     }
-    // The row of a turn, -1 where there is none; its stats are asked for a turn ahead.
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / lanes;
-    auto row_of = [&](int i, int &b, int &t) {
-        const int64_t at = first + static_cast<int64_t>(i) * step;
-        if (at >= p.rows) return -1;
-        const int row = static_cast<int>(at);
-        locate(p, row, b, t);
-        return is_valid(p, b, t) ? row : -1;
-    };
-    auto fetch = [&](int i, int stage) {
-        int b, t;
-        const int row = i < turns ? row_of(i, b, t) : -1;
-        Slot *to = mine + stage * 2 * P * THREADS;
-        const E *x = p.x + (row < 0 ? 0 : b * p.x_sb + t * p.x_st);
-        const E *dy = p.dy + (row < 0 ? 0 : b * p.dy_sb + t * p.dy_st);
+    int rows[S][R];
+    float2 stats[R], next[R];
+    auto stats_of = [&](const int (&of)[R], float2 (&to)[R]) {
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-            const int c = (q * lanes + lane) * V;
-            Slot *tx = to + q * THREADS, *tdy = to + (P + q) * THREADS;
-            if (row >= 0 && c < p.C) {
-                if constexpr (V > 1) {
-                    copy16_async(tx, x + c);
-                    copy16_async(tdy, dy + c);
-                } else if constexpr (sizeof(E) == 4) {
-                    copy4_async(tx, x + c);
-                    copy4_async(tdy, dy + c);
-                } else {
-                    *tx = to_f32(x[c]);
-                    *tdy = to_f32(dy[c]);
-                }
-            } else {
-                memset(tx, 0, sizeof(Slot));
-                memset(tdy, 0, sizeof(Slot));
-            }
-        }
-        copy_commit();
-        return row;
+        for (int r = 0; r < R; ++r)
+            to[r] = of[r] < 0 ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(p.stats_in + 2LL * of[r]);
     };
-    auto stats_of = [&](int row) {
-        return row < 0 ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(p.stats_in + 2LL * row);
-    };
-    auto widen = [&](const Slot *at, F2 (&f)[N]) {
-        if constexpr (V == 1) {
-            f[0] = both(*at);
-        } else {
-            Piece<E, V> r;
-            r.raw = *at;
-            r.widen(f);
-        }
-    };
-    int rows[kStages];
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) rows[i] = fetch(i, i);
-    float2 stats = stats_of(rows[0]);
+    for (int i = 0; i < S; ++i) ring.fetch(i, i, rows[i]);
+    stats_of(rows[0], stats);
     int stage = 0;
-    for (int i = 0; i < turns; ++i) {
-        const int row = rows[0];
-        float2 next;
-        if constexpr (kStages > 1) next = stats_of(rows[1]);
-        copy_wait<kStages - 1>();
-        const Slot *from = mine + stage * 2 * P * THREADS;
-        const F2 minus = both(-stats.x), rstd = both(stats.y);
-        F2 s1 = both(0.f), s2 = both(0.f);
+    for (int i = 0; i < ring.turns; ++i) {
+        if constexpr (S > 1) stats_of(rows[1], next);      // asked for a turn ahead
+        copy_wait<S - 1>();
+        float s[2 * R];
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-            F2 x[N], dy[N];
-            widen(from + q * THREADS, x);
-            widen(from + (P + q) * THREADS, dy);
+        for (int r = 0; r < R; ++r) {
+            const F2 minus = both(-stats[r].x), rstd = both(stats[r].y);
+            F2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const F2 xhat = mul2(add2(x[k], minus), rstd), v = mul2(dy[k], w[q][k]);
-                db[q][k] = add2(db[q][k], dy[k]);
-                dw[q][k] = fma2(dy[k], xhat, dw[q][k]);
-                s1 = add2(s1, v);
-                s2 = fma2(v, xhat, s2);
+            for (int q = 0; q < P; ++q) {
+                F2 x[N], dy[N];
+                ring.read(stage, r, 0, q, x);
+                ring.read(stage, r, 1, q, dy);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const F2 xhat = mul2(add2(x[k], minus), rstd), v = mul2(dy[k], w[q][k]);
+                    db[q][k] = add2(db[q][k], dy[k]);
+                    dw[q][k] = fma2(dy[k], xhat, dw[q][k]);
+                    s1 = add2(s1, v);
+                    s2 = fma2(v, xhat, s2);
+                }
             }
+            s[2 * r] = halves<V>(s1);
+            s[2 * r + 1] = halves<V>(s2);
         }
-        float s[2] = {halves<V>(s1), halves<V>(s2)};
-        row_sums(s, lanes, buffers[i & 1]);
-        const F2 c1 = both(p.rms ? 0.f : -s[0] * inv), c2 = both(-s[1] * inv);
-        if (row >= 0) {
+        row_sums(s, ring.lanes, buffers[i & 1]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = rows[0][r];
+            if (row < 0) continue;
+            const F2 minus = both(-stats[r].x), rstd = both(stats[r].y);
+            const F2 c1 = both(p.rms ? 0.f : -s[2 * r] * inv), c2 = both(-s[2 * r + 1] * inv);
             E *dx = p.dx + static_cast<int64_t>(row) * p.C;
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-                const int c = (q * lanes + lane) * V;
+                const int c = ring.channel(q);
                 if (c >= p.C) break;
                 F2 x[N], dy[N];
-                widen(from + q * THREADS, x);
-                widen(from + (P + q) * THREADS, dy);
+                ring.read(stage, r, 0, q, x);
+                ring.read(stage, r, 1, q, dy);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
                     const F2 xhat = mul2(add2(x[k], minus), rstd);
-                    x[k] = mul2(rstd, fma2(xhat, c2, add2(mul2(dy[k], w[q][k]), c1)));
+                    x[k] = mul2(rstd, fma2(xhat, c2, fma2(dy[k], w[q][k], c1)));
                 }
-                Piece<E, V> r;
-                r.round(x);
-                r.store(dx + c);
+                Piece<E, V> piece;
+                piece.round(x);
+                piece.store(dx + c);
             }
         }
 #pragma unroll
-        for (int k = 0; k + 1 < kStages; ++k) rows[k] = rows[k + 1];
-        rows[kStages - 1] = fetch(i + kStages, stage);
-        if constexpr (kStages == 1) next = stats_of(rows[0]);
-        stats = next;
-        stage = stage == kStages - 1 ? 0 : stage + 1;
+        for (int k = 0; k + 1 < S; ++k)
+#pragma unroll
+            for (int r = 0; r < R; ++r) rows[k][r] = rows[k + 1][r];
+        ring.fetch(i + S, stage, rows[S - 1]);
+        if constexpr (S == 1) stats_of(rows[0], next);
+#pragma unroll
+        for (int r = 0; r < R; ++r) stats[r] = next[r];
+        stage = stage == S - 1 ? 0 : stage + 1;
     }
     copy_wait<0>();
     if (!p.part) return;
     // Rows that the block held at once are added up through the ring's memory, in order.
-    float *sums = reinterpret_cast<float *>(ring_memory);          // [thread][value]
+    const int lanes = ring.lanes, per_block = THREADS / lanes;
+    float *sums = reinterpret_cast<float *>(ring_memory);          // [value][thread]
     float *part = p.part + blockIdx.x * 2LL * p.C;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
         for (int q = 0; q < P; ++q) {
-            const int c = (q * lanes + lane) * V;
+            const int c = ring.channel(q);
             float f[2 * N];
 #pragma unroll
             for (int k = 0; k < N; ++k) unpack2(which ? db[q][k] : dw[q][k], f[2 * k], f[2 * k + 1]);
@@ -451,76 +545,64 @@ void flatten(LayerNormParams<E> &p) {
     p.B = 1;
 }
 
-// Threads to a row of `pieces`, a power of two, with P pieces to a thread at most.
-int lanes_for(int pieces, int P) {
-    int lanes = 1;
-    while (lanes < kMaxLanes && lanes * P < pieces) lanes *= 2;
-    return lanes;
+// Blocks that stay: as many as an SM holds at once (its shared memory and registers), or rows.
+template <typename E, int V, int P, int THREADS, int TENSORS>
+cudaError_t launch_rows(LayerNormParams<E> &p, int &blocks, cudaStream_t s) {
+    using Ring = RowRing<E, V, P, THREADS, TENSORS>;
+    p.lanes = 1;
+    while (p.lanes * P < p.C / V) p.lanes *= 2;
+    const int per_block = THREADS / p.lanes, sm = blocks_to_sm(P, THREADS, TENSORS);
+    const int64_t all = (static_cast<int64_t>(p.rows) + per_block - 1) / per_block;
+    blocks = static_cast<int>(all < 152 * sm ? all : 152 * sm);
+    auto kernel = TENSORS == 1 ? gdn_layer_norm_kernel<E, V, P, THREADS> : gdn_layer_norm_bwd_kernel<E, V, P, THREADS>;
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Ring::bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, THREADS, Ring::bytes, s>>>(p);
+    return cudaGetLastError();
 }
 
-template <typename E, int V, int P>
-cudaError_t launch_fwd(LayerNormParams<E> &p, cudaStream_t s) {
-    const int threads = p.lanes > kThreads ? p.lanes : kThreads, per_block = threads / p.lanes;
-    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.rows) + per_block - 1) / per_block);
-    gdn_layer_norm_kernel<E, V, P><<<blocks, threads, 0, s>>>(p);
-    return cudaGetLastError();
+// By the pieces of a row: a block of 256 threads with up to two 16-byte pieces (eight channels) to a
+// thread, then of 512 with what its registers hold. `held`: whether they hold a row.
+template <typename E, int V, int TENSORS>
+cudaError_t by_pieces(LayerNormParams<E> &p, int &blocks, bool &held, cudaStream_t s) {
+    const int pieces = p.C / V;
+    held = true;
+    if (pieces <= 256) return launch_rows<E, V, 1, 256, TENSORS>(p, blocks, s);
+    if (pieces <= 512) return launch_rows<E, V, 2, 256, TENSORS>(p, blocks, s);
+    if constexpr (V == 1) {
+        if (pieces <= 1024) return launch_rows<E, V, 4, 256, TENSORS>(p, blocks, s);
+        if (pieces <= 2048) return launch_rows<E, V, 8, 256, TENSORS>(p, blocks, s);
+        if (pieces <= 8192) return launch_rows<E, V, 16, 512, TENSORS>(p, blocks, s);
+    } else {
+        if (pieces <= 1024) return launch_rows<E, V, 2, 512, TENSORS>(p, blocks, s);
+        if (pieces <= 2048) return launch_rows<E, V, 4, 512, TENSORS>(p, blocks, s);
+        if constexpr (V <= 4)
+            if (pieces <= 4096) return launch_rows<E, V, 8, 512, TENSORS>(p, blocks, s);
+    }
+    held = false;
+    return cudaSuccess;
 }
 
 template <typename E, int V>
 cudaError_t fwd(LayerNormParams<E> &p, cudaStream_t s) {
-    constexpr int most = V == 1 ? 16 : 8;      // pieces to a thread: at most 64 registers as fp32
-    const int pieces = p.C / V;
-    p.lanes = lanes_for(pieces, most);
-    // few rows: more threads to each, so that every SM has work
-    while (p.lanes < kMaxLanes && p.lanes < pieces && static_cast<int64_t>(p.rows) * p.lanes < 152 * 4 * kThreads)
-        p.lanes *= 2;
-    const int per = (pieces + p.lanes - 1) / p.lanes;
-    if (per <= 1) return launch_fwd<E, V, 1>(p, s);
-    if (per <= 2) return launch_fwd<E, V, 2>(p, s);
-    if (per <= 4) return launch_fwd<E, V, 4>(p, s);
-    if (per <= 8) return launch_fwd<E, V, 8>(p, s);
-    if constexpr (V == 1)
-        if (per <= 16) return launch_fwd<E, V, 16>(p, s);
-    const unsigned blocks = static_cast<unsigned>(p.rows < 152 * 8 ? p.rows : 152 * 8);
+    int blocks;
+    bool held;
+    const cudaError_t err = by_pieces<E, V, 1>(p, blocks, held, s);
+    if (held) return err;
+    blocks = p.rows < 152 * 8 ? p.rows : 152 * 8;
     gdn_layer_norm_wide_kernel<E><<<blocks, kThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-template <typename E, int V, int P, int THREADS>
-cudaError_t launch_bwd(LayerNormParams<E> &p, int &parts, cudaStream_t s) {
-    p.lanes = lanes_for(p.C / V, P);
-    const int per_block = THREADS / p.lanes, most = THREADS * P <= 512 ? kMaxParts : 152;
-    const int64_t blocks = (static_cast<int64_t>(p.rows) + per_block - 1) / per_block;
-    parts = static_cast<int>(blocks < most ? blocks : most);
-    constexpr int bytes = row_stages(V, P, THREADS) * row_bytes(V, P, THREADS);
-    static_assert(bytes >= THREADS * V * 4, "the ring holds a piece of sums of every thread");
-    auto kernel = gdn_layer_norm_bwd_kernel<E, V, P, THREADS>;
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    kernel<<<parts, THREADS, bytes, s>>>(p);
-    return cudaGetLastError();
-}
-
-// The pieces that a thread's registers hold, sums over rows among them, and beyond.
 template <typename E, int V>
 cudaError_t bwd(LayerNormParams<E> &p, int &parts, cudaStream_t s) {
-    const int pieces = p.C / V;
-    if (pieces <= 256) return launch_bwd<E, V, 1, 256>(p, parts, s);
-    if (pieces <= 512) return launch_bwd<E, V, 2, 256>(p, parts, s);
-    if constexpr (V == 1) {
-        if (pieces <= 1024) return launch_bwd<E, V, 4, 256>(p, parts, s);
-        if (pieces <= 2048) return launch_bwd<E, V, 8, 256>(p, parts, s);
-        if (pieces <= 8192) return launch_bwd<E, V, 16, 512>(p, parts, s);
-    } else {
-        if (pieces <= 1024) return launch_bwd<E, V, 2, 512>(p, parts, s);
-        if (pieces <= 2048) return launch_bwd<E, V, 4, 512>(p, parts, s);
-        if constexpr (V <= 4)
-            if (pieces <= 4096) return launch_bwd<E, V, 8, 512>(p, parts, s);
-    }
-    const unsigned blocks = static_cast<unsigned>(p.rows < 152 * 8 ? p.rows : 152 * 8);
+    bool held;
+    cudaError_t err = by_pieces<E, V, 2>(p, parts, held, s);
+    if (held) return err;
+    const int blocks = p.rows < 152 * 8 ? p.rows : 152 * 8;
     gdn_layer_norm_wide_dx_kernel<E><<<blocks, kThreads, 0, s>>>(p);
-    cudaError_t err = cudaGetLastError();
+    err = cudaGetLastError();
     if (err != cudaSuccess || !p.part) return err;
     parts = p.rows < kWideParts ? p.rows : kWideParts;
     gdn_layer_norm_wide_dw_kernel<E><<<dim3((p.C + kThreads - 1) / kThreads, parts), kThreads, 0, s>>>(p);
