@@ -38,7 +38,7 @@ template <typename E, int FORM>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_kernel(const RecurParams<E> p) {
     __shared__ Exchange<kMaxWarps> ex;
     extern __shared__ uint4 ring[];
-    const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.pairs != 0 : true;
+    const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.D % 2 == 0 : true;
     const int scaling = scaling_of<FORM>(p);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int ranks = p.ranks, rank = blockIdx.x % ranks, c0 = blockIdx.x / ranks * kRecurChannels;
@@ -48,17 +48,26 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_kernel(const Recu
     const int n = valid_tokens(p.lengths, b, p.T);
     const int tile = warps * kRecurEvery * ranks;          // of the cluster
     const int tiles = (n + tile - 1) / tile, first = (rank * warps + warp) * kRecurEvery;
-    constexpr int rows = Rows<E>::bytes / sizeof(E);
-    const int slot = (gated ? 3 : 2) * rows;
-    E *mine = reinterpret_cast<E *>(ring) + warp * kStages * slot;
+    using Tile = Rows<E, (FORM >= 0)>;
+    const int slot = (gated ? 3 : 2) * Tile::bytes;
+    unsigned char *mine = reinterpret_cast<unsigned char *>(ring) + warp * kStages * slot;
+    struct Inputs {
+        Tile x, decay, gate;
+    };
+    auto inputs = [&](int i) {
+        unsigned char *at = mine + i % kStages * slot;
+        const int t = i * tile + first;
+        return Inputs{Tile(at, p.x + b * p.x_sb, p.x_st, t, c0),
+                      Tile(at + Tile::bytes, p.decay + b * p.a_sb, p.a_st, t, c0),
+                      Tile(at + 2 * Tile::bytes, gated ? p.gate + b * p.g_sb : nullptr, p.g_st, t, c0)};
+    };
     auto fill = [&](int i) {
         if (i < tiles) {
-            E *to = mine + i % kStages * slot;
-            const int t = i * tile + first;
-            fill_rows(to, p.x + b * p.x_sb, p.x_st, t, n, c0, D, p.fill, 0.f);
-            // behind the sequence a is 1
-            fill_rows(to + rows, p.decay + b * p.a_sb, p.a_st, t, n, c0, D, p.fill, rated ? -INFINITY : INFINITY);
-            if (gated) fill_rows(to + 2 * rows, p.gate + b * p.g_sb, p.g_st, t, n, c0, D, p.fill, 0.f);
+            const Inputs in = inputs(i);
+            const int left = n - (i * tile + first), width = min(kRecurChannels, D - c0);
+            in.x.fill(left, width, p.x_span, 0.f);
+            in.decay.fill(left, width, p.a_span, rated ? -INFINITY : INFINITY);    // behind the sequence a is 1
+            if (gated) in.gate.fill(left, width, p.g_span, 0.f);
         }
         copy_commit();
     };
@@ -70,14 +79,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_kernel(const Recu
     for (int i = 0; i < tiles; ++i) {
         copy_wait<kStages - 1>();
         __syncwarp();
-        const E *from = mine + i % kStages * slot + 2 * lane;
+        const Inputs in = inputs(i);
         F2 a[kRecurEvery], u[kRecurEvery];
         Through through = {both(1.f), both(0.f)};
 #pragma unroll
         for (int j = 0; j < kRecurEvery; ++j) {
-            const E *at = from + j * kRecurChannels;
-            token2(pair_of(at), pair_of(at + rows), gated ? pair_of(at + 2 * rows) : both(0.f), t_scale, gated,
-                   rated, scaling, a[j], u[j]);
+            token2(in.x.pair(j, lane), in.decay.pair(j, lane), gated ? in.gate.pair(j, lane) : both(0.f), t_scale,
+                   gated, rated, scaling, a[j], u[j]);
             through.h = fma2(a[j], through.h, u[j]);
             through.a = mul2(a[j], through.a);
         }
@@ -192,9 +200,10 @@ cudaError_t launch(RecurParams<E> &p, cudaStream_t s, std::integer_sequence<int,
     }
     using Kernel = void (*)(RecurParams<E>);
     static constexpr Kernel table[] = {gdn_recur_kernel<E, kAnyForm>, gdn_recur_kernel<E, FORMS>...};
-    recur_alignment(p);
-    const int warps = recur_shape(p, sizeof(E) == 2 ? kMaxWarps : kMaxWarps / 2, 2 * 152);
-    return recur_launch(recur_kernel<E>(table, p), p, warps, warps * kStages * (p.gate ? 3 : 2) * Rows<E>::bytes, s);
+    recur_rows(p);
+    const int slot = kStages * (p.gate ? 3 : 2) * recur_row_bytes(p);
+    const int warps = recur_shape<E, Exchange<kMaxWarps>>(p, kMaxWarps, slot);
+    return recur_launch(recur_kernel<E>(table, p), p, warps, warps * slot, s);
 }
 
 }  // namespace

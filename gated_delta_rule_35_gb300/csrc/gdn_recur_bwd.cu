@@ -22,7 +22,7 @@ template <typename E, int FORM>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const RecurParams<E> p) {
     __shared__ Exchange<kMaxWarps> ex;
     extern __shared__ uint4 ring[];
-    const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.pairs != 0 : true;
+    const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.D % 2 == 0 : true;
     const int scaling = scaling_of<FORM>(p);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int ranks = p.ranks, rank = blockIdx.x % ranks, c0 = blockIdx.x / ranks * kRecurChannels;
@@ -32,18 +32,28 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const 
     const int n = valid_tokens(p.lengths, b, p.T);
     const int tile = warps * kRecurEvery * ranks;          // of the cluster
     const int tiles = (n + tile - 1) / tile, first = (rank * warps + warp) * kRecurEvery;
-    constexpr int rows = Rows<E>::bytes / sizeof(E);
-    const int slot = (gated ? 4 : 3) * rows;
-    E *mine = reinterpret_cast<E *>(ring) + warp * kStages * slot;
-    auto fill = [&](int i) {                               // i-th from the last
+    using Tile = Rows<E, (FORM >= 0)>;
+    const int slot = (gated ? 4 : 3) * Tile::bytes;
+    unsigned char *mine = reinterpret_cast<unsigned char *>(ring) + warp * kStages * slot;
+    struct Inputs {
+        Tile x, decay, dy, gate;
+    };
+    auto inputs = [&](int i) {                             // i-th from the last
+        unsigned char *at = mine + i % kStages * slot;
+        const int t = (tiles - 1 - i) * tile + first;
+        return Inputs{Tile(at, p.x + b * p.x_sb, p.x_st, t, c0),
+                      Tile(at + Tile::bytes, p.decay + b * p.a_sb, p.a_st, t, c0),
+                      Tile(at + 2 * Tile::bytes, p.dy + b * p.dy_sb, p.dy_st, t, c0),
+                      Tile(at + 3 * Tile::bytes, gated ? p.gate + b * p.g_sb : nullptr, p.g_st, t, c0)};
+    };
+    auto fill = [&](int i) {
         if (i < tiles) {
-            E *to = mine + i % kStages * slot;
-            const int t = (tiles - 1 - i) * tile + first;
-            fill_rows(to, p.x + b * p.x_sb, p.x_st, t, n, c0, D, p.fill, 0.f);
-            // behind the sequence a is 1
-            fill_rows(to + rows, p.decay + b * p.a_sb, p.a_st, t, n, c0, D, p.fill, rated ? -INFINITY : INFINITY);
-            fill_rows(to + 2 * rows, p.dy + b * p.dy_sb, p.dy_st, t, n, c0, D, p.fill, 0.f);
-            if (gated) fill_rows(to + 3 * rows, p.gate + b * p.g_sb, p.g_st, t, n, c0, D, p.fill, 0.f);
+            const Inputs in = inputs(i);
+            const int left = n - ((tiles - 1 - i) * tile + first), width = min(kRecurChannels, D - c0);
+            in.x.fill(left, width, p.x_span, 0.f);
+            in.decay.fill(left, width, p.a_span, rated ? -INFINITY : INFINITY);    // behind the sequence a is 1
+            in.dy.fill(left, width, p.dy_span, 0.f);
+            if (gated) in.gate.fill(left, width, p.g_span, 0.f);
         }
         copy_commit();
     };
@@ -61,41 +71,39 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const 
         if (n > t) h = load_pair(p.states + (b * chunks + t / kRecurEvery) * D, c, D, pairs);
         copy_wait<kStages - 1>();
         __syncwarp();
-        const E *from = mine + i % kStages * slot + 2 * lane;
+        const Inputs in = inputs(i);
         F2 lam[kRecurEvery];                               // first the decay factors
         Through through = {both(1.f), both(0.f)};
 #pragma unroll
         for (int j = kRecurEvery - 1; j >= 0; --j) {
-            const E *at = from + j * kRecurChannels;
-            lam[j] = sigmoid2(pair_of(at + rows));
+            lam[j] = sigmoid2(in.decay.pair(j, lane));
             if (rated) lam[j] = decay_factor2(mul2(lam[j], t_scale));
-            through.h = mul2(lam[j], add2(pair_of(at + 2 * rows), through.h));
+            through.h = mul2(lam[j], add2(in.dy.pair(j, lane), through.h));
             through.a = mul2(lam[j], through.a);
         }
         F2 next = scan.step(i, through);
 #pragma unroll
         for (int j = kRecurEvery - 1; j >= 0; --j) {
             const F2 a = lam[j];
-            lam[j] = add2(pair_of(from + j * kRecurChannels + 2 * rows), next);
+            lam[j] = add2(in.dy.pair(j, lane), next);
             next = mul2(a, lam[j]);
         }
         int64_t out = (b * p.T + t) * D + c;
 #pragma unroll
         for (int j = 0; j < kRecurEvery; ++j) {
-            const E *at = from + j * kRecurChannels;
             F2 s, s_n, a, a_n, inverse;
-            sigmoids2(pair_of(at + rows), s, s_n);
+            sigmoids2(in.decay.pair(j, lane), s, s_n);
             if (rated) {
                 decay_factor2(mul2(s, t_scale), a, a_n);
             } else {
                 a = s;
                 a_n = s_n;
             }
-            const F2 m = input_factor2(a, a_n, scaling, inverse), x = pair_of(at);
+            const F2 m = input_factor2(a, a_n, scaling, inverse), x = in.x.pair(j, lane);
             F2 qx = x, dx = mul2(m, lam[j]), d_gate;
             if (gated) {
                 F2 q, q_n;
-                sigmoids2(pair_of(at + 3 * rows), q, q_n);
+                sigmoids2(in.gate.pair(j, lane), q, q_n);
                 qx = mul2(q, x);
                 d_gate = mul2(mul2(dx, qx), q_n);
                 dx = mul2(dx, q);
@@ -141,10 +149,10 @@ template <typename E, int... FORMS>
 cudaError_t launch(RecurParams<E> &p, float *d_rate, cudaStream_t s, std::integer_sequence<int, FORMS...>) {
     using Kernel = void (*)(RecurParams<E>);
     static constexpr Kernel table[] = {gdn_recur_bwd_kernel<E, kAnyForm>, gdn_recur_bwd_kernel<E, FORMS>...};
-    recur_alignment(p);
-    const int warps = recur_shape(p, sizeof(E) == 2 ? kMaxWarps : kMaxWarps / 2, 2 * 152);
-    const cudaError_t err = recur_launch(recur_kernel<E>(table, p), p, warps,
-                                         warps * kStages * (p.gate ? 4 : 3) * Rows<E>::bytes, s);
+    recur_rows(p);
+    const int slot = kStages * (p.gate ? 4 : 3) * recur_row_bytes(p);
+    const int warps = recur_shape<E, Exchange<kMaxWarps>>(p, kMaxWarps, slot);
+    const cudaError_t err = recur_launch(recur_kernel<E>(table, p), p, warps, warps * slot, s);
     if (err != cudaSuccess || !d_rate) return err;
     return column_sums(p.d_rate_part, p.B * p.ranks, p.D, p.D, d_rate, nullptr, s);
 }

@@ -13,6 +13,7 @@
 #pragma once
 
 #include "columns.cuh"
+#include "rows.cuh"
 
 namespace gdn {
 
@@ -28,10 +29,10 @@ struct RecurParams {
     E *y, *dx, *d_decay, *d_gate;
     float *h_final, *states, *d_rate_part, *dh0;
     int64_t x_sb, x_st, a_sb, a_st, g_sb, g_st, dy_sb, dy_st;
+    RowSpan x_span, a_span, g_span, dy_span;
     int B, T, D, scaling;
-    // fill: bytes of a copy to shared memory (16, 4 or, element by element, 2);
-    // pairs: whether the outputs' channel pairs are aligned
-    int fill, pairs, ranks;     // ranks: blocks to a cluster
+    int whole;     // every input's rows are aligned 16-byte pieces
+    int ranks;     // blocks to a cluster
 };
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -93,7 +94,7 @@ __device__ __forceinline__ void decay_factor2(F2 t, F2 &a, F2 &n) {
 }
 
 // The form of a problem: what its kernels know when they are compiled. kAnyForm's kernels ask the
-// problem instead, and take outputs of an odd number of channels.
+// problem instead, and take rows that are not whole, aligned 16-byte pieces.
 constexpr int kForms = 12, kAnyForm = -1;
 constexpr int recur_form(bool gated, bool rated, int scaling) { return scaling * 4 + rated * 2 + gated; }
 
@@ -118,7 +119,7 @@ __device__ __forceinline__ F2 input_factor2(F2 a, F2 n, int scaling, F2 &inverse
     return scaling == GDN_RECUR_COMPLEMENT ? n : both(1.f);
 }
 
-// Two channels of a row in shared or global memory.
+// Two channels of a row in shared memory.
 __device__ __forceinline__ F2 pair_of(const __nv_bfloat16 *p) {
     const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
     return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -149,53 +150,70 @@ __device__ __forceinline__ void store_pair(S *at, F2 v, bool there, bool second,
     }
 }
 
-// A warp's tile of one tensor: kRecurEvery rows of kRecurChannels values.
-template <typename E>
+// A warp's tile of one tensor: kRecurEvery rows of kRecurChannels values. WHOLE rows are copied in
+// 16-byte pieces; others value by value in fp32, and in bf16, whose values are less than an
+// asynchronous copy moves, as the aligned pieces that they touch.
+template <typename E, bool WHOLE>
 struct Rows {
-    static constexpr int bytes = kRecurEvery * kRecurChannels * sizeof(E);
-};
+    static constexpr bool SHIFTED = !WHOLE && sizeof(E) == 2;
+    static constexpr int pitch = kRecurChannels * sizeof(E) + (SHIFTED ? 16 : 0);
+    static constexpr int bytes = kRecurEvery * pitch;
+    unsigned char *at;
+    const E *from;         // channel c0 of the tile's first token
+    int64_t stride;
 
-// Copies rows t .. t + 15 (those below n), channels c0 .. c0 + 63 (those below D), of a sequence to
-// `to`, asynchronously where the alignment allows. Rows behind the sequence take `other`,
-// written for the pair of channels that the lane will read.
-template <typename E>
-__device__ __forceinline__ void fill_rows(E *to, const E *from, int64_t stride, int t, int n, int c0, int D, int fill,
-                                          float other) {
-    const int lane = threadIdx.x % 32;
-    from += t * stride + c0;
-    const int rows = min(kRecurEvery, n - t);
-    if (fill == 16) {
-        constexpr int V = 16 / sizeof(E), per_row = kRecurChannels / V, step = 32 / per_row;
-        const int c = lane % per_row * V;
-        int row = lane / per_row;
-        from += row * stride + c;
-        to += row * kRecurChannels + c;
-        if (c0 + c < D) {
+    __device__ __forceinline__ Rows(unsigned char *at, const E *sequence, int64_t stride, int t, int c0)
+        : at(at), from(sequence + t * stride + c0), stride(stride) {}
+
+    __device__ __forceinline__ E *row(int j) const {
+        unsigned char *r = at + j * pitch;
+        if constexpr (SHIFTED)      // by the low bits of the row's address
+            r += (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(from)) +
+                  static_cast<uint32_t>(stride * static_cast<int>(sizeof(E))) * j) & 15;
+        return reinterpret_cast<E *>(r);
+    }
+    // Channels 2 lane and 2 lane + 1 of token j; what is there in place of channels that the row does
+    // not have is of no use.
+    __device__ __forceinline__ F2 pair(int j, int lane) const {
+        const E *v = row(j) + 2 * lane;
+        if constexpr (!SHIFTED) return pair_of(v);
+        return pack2(to_f32(v[0]), to_f32(v[1]));
+    }
+    // Copies the first `rows` rows' values, `width` of the kRecurChannels; the others, behind the
+    // sequence, take `other`, written for the pair of channels that the lane will read.
+    __device__ __forceinline__ void fill(int rows, int width, const RowSpan &span, float other) const {
+        const int lane = threadIdx.x % 32;
+        rows = min(rows, kRecurEvery);
+        if constexpr (WHOLE) {
+            constexpr int V = 16 / sizeof(E), per_row = kRecurChannels / V, step = 32 / per_row;
+            const int c = lane % per_row * V, first = lane / per_row;
+            if (c < width) {
+                const E *f = from + first * stride + c;
+                E *to = reinterpret_cast<E *>(at) + first * kRecurChannels + c;
 #pragma unroll
-            for (; row < kRecurEvery; row += step) {
-                if (row < rows) copy16_async(to, from);
-                from += step * stride;
-                to += step * kRecurChannels;
+                for (int k = 0; k < kRecurEvery / step; ++k) {
+                    if (first + k * step < rows) copy16_async(to, f);
+                    f += step * stride;
+                    to += step * kRecurChannels;
+                }
             }
-        }
-        to -= row * kRecurChannels + c;
-    } else if (fill == 4) {
-        constexpr int V = 4 / sizeof(E);
-        for (int row = 0; row < rows; ++row)
+        } else if constexpr (!SHIFTED) {
+            const E *f = from + lane;
+            E *to = reinterpret_cast<E *>(at) + lane;
+            for (int j = 0; j < rows; ++j, f += stride, to += kRecurChannels)
 #pragma unroll
-            for (int c = lane * V; c < kRecurChannels; c += 32 * V)
-                if (c0 + c < D) copy4_async(to + row * kRecurChannels + c, from + row * stride + c);
-    } else {
-#pragma unroll 4
-        for (int row = 0; row < rows; ++row)
-            for (int c = lane; c < kRecurChannels; c += 32)
-                if (c0 + c < D) to[row * kRecurChannels + c] = from[row * stride + c];
+                for (int c = 0; c < kRecurChannels; c += 32)
+                    if (c + lane < width) copy4_async(to + c, f + c);
+        } else {
+            const RowCopy<E> copy(span, from, stride, rows, width);          // 9 pieces to a row, two rows at once
+            for (int j = lane / 16; j < rows; j += 2) copy(at + j * pitch, from + j * stride, width, lane % 16);
+        }
+        for (int j = max(rows, 0); j < kRecurEvery; ++j) {
+            E *v = row(j) + 2 * lane;
+            v[0] = v[1] = from_f32<E>(other);
+        }
     }
-    for (int row = max(rows, 0); row < kRecurEvery; ++row) {
-        E *at = to + row * kRecurChannels + 2 * lane;
-        at[0] = at[1] = from_f32<E>(other);
-    }
-}
+};
 
 // (A, H) of two channels.
 struct Through {
@@ -317,29 +335,30 @@ inline bool aligned_rows(const void *p, int B, int T, int64_t sb, int64_t st, si
     return is_aligned(p, a) && (B == 1 || sb * e % a == 0) && (T == 1 || st * e % a == 0);
 }
 
-// Copies of 16 bytes where every input's rows are whole pieces of them, else of 4, else elements.
 template <typename E>
-void recur_alignment(RecurParams<E> &p) {
+void recur_rows(RecurParams<E> &p) {
     constexpr size_t e = sizeof(E);
-    auto all = [&](size_t a) {
-        return p.D * e % a == 0 && aligned_rows(p.x, p.B, p.T, p.x_sb, p.x_st, e, a) &&
-               aligned_rows(p.decay, p.B, p.T, p.a_sb, p.a_st, e, a) &&
-               (!p.gate || aligned_rows(p.gate, p.B, p.T, p.g_sb, p.g_st, e, a)) &&
-               (!p.dy || aligned_rows(p.dy, p.B, p.T, p.dy_sb, p.dy_st, e, a));
-    };
-    p.fill = all(16) ? 16 : all(4) ? 4 : static_cast<int>(e);
-    p.pairs = p.D % 2 == 0;
+    p.whole = p.D * e % 16 == 0 && aligned_rows(p.x, p.B, p.T, p.x_sb, p.x_st, e, 16) &&
+              aligned_rows(p.decay, p.B, p.T, p.a_sb, p.a_st, e, 16) &&
+              (!p.gate || aligned_rows(p.gate, p.B, p.T, p.g_sb, p.g_st, e, 16)) &&
+              (!p.dy || aligned_rows(p.dy, p.B, p.T, p.dy_sb, p.dy_st, e, 16));
+    p.x_span = row_span(p.x, p.B, p.T, p.D, p.x_sb, p.x_st, e);
+    p.a_span = row_span(p.decay, p.B, p.T, p.D, p.a_sb, p.a_st, e);
+    p.g_span = row_span(p.gate, p.B, p.T, p.D, p.g_sb, p.g_st, e);
+    p.dy_span = row_span(p.dy, p.B, p.T, p.D, p.dy_sb, p.dy_st, e);
 }
 
-// Warps to a block: as many as a sequence's tokens fill, up to `most`. Blocks to a cluster: as
-// many as leave the GPU's `places` for blocks filled once, and have tokens.
-template <typename E>
-int recur_shape(RecurParams<E> &p, int most, int places) {
+// Warps to a block: as many as a sequence's tokens fill, up to `most` and to what lets two blocks,
+// with `slot` bytes to a warp's ring, share an SM. Blocks to a cluster: as many as leave the GPU's
+// places for two blocks to an SM filled once, and have tokens.
+template <typename E, typename X>
+int recur_shape(RecurParams<E> &p, int most, int slot) {
+    const int fit = (228 * 1024 / 2 - 1024 - static_cast<int>(sizeof(X))) / slot;
     int warps = 1;
-    while (warps < most && static_cast<int64_t>(warps) * kRecurEvery < p.T) ++warps;
+    while (warps < most && warps < fit && static_cast<int64_t>(warps) * kRecurEvery < p.T) ++warps;
     const int64_t blocks = static_cast<int64_t>(p.B) * ((p.D + kRecurChannels - 1) / kRecurChannels);
     p.ranks = 1;
-    while (p.ranks < kMaxRanks && blocks * p.ranks * 2 <= places &&
+    while (p.ranks < kMaxRanks && blocks * p.ranks * 2 <= 2 * 152 &&
            p.T > static_cast<int64_t>(p.ranks) * warps * kRecurEvery)
         p.ranks *= 2;
     return warps;
@@ -365,10 +384,14 @@ cudaError_t recur_launch(void (*kernel)(RecurParams<E>), const RecurParams<E> &p
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Bytes of a warp's ring slot for one tensor.
+template <typename E>
+int recur_row_bytes(const RecurParams<E> &p) { return p.whole ? Rows<E, true>::bytes : Rows<E, false>::bytes; }
+
 // The kernel of a problem's form, of a table that begins with kAnyForm's.
 template <typename E, typename K>
 K recur_kernel(const K (&table)[kForms + 1], const RecurParams<E> &p) {
-    return table[p.pairs ? 1 + recur_form(p.gate, p.rate, p.scaling) : 0];
+    return table[p.whole ? 1 + recur_form(p.gate, p.rate, p.scaling) : 0];
 }
 
 }  // namespace gdn
