@@ -11,8 +11,15 @@
 // about it; in the backward pass both sums at once. Rows beyond what a block holds go to the
 // *_wide_* kernels, a block to a row that it reads again for each sum.
 #include "columns.cuh"
+#include "rows.cuh"
 
 namespace gdn {
+
+// The pairs' operations on single values (beside them: inner scopes would hide the pairs').
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+
 namespace {
 
 constexpr int kThreads = 256;
@@ -21,7 +28,9 @@ constexpr int kMaxParts = 152 * 2; // blocks of the backward pass
 
 // Blocks to an SM. Of the backward pass three would spill: 302 us for 257 on 65536 x 4096 bf16; of
 // the forward pass two leave too few rows on their way: 203 us for 182.
-constexpr int blocks_to_sm(int P, int threads, int tensors) { return threads * P > 512 ? 1 : tensors == 1 ? 3 : 2; }
+constexpr int blocks_to_sm(int P, int threads, int tensors) {
+    return threads > 256 ? 1 : tensors == 1 && P < 16 ? 3 : 2;
+}
 
 template <typename E>
 struct LayerNormParams {
@@ -31,34 +40,52 @@ struct LayerNormParams {
     E *y, *dx;
     float *stats, *part;
     int64_t x_sb, x_st, dy_sb, dy_st;
+    RowSpan x_span, dy_span;
     int rows, B, T, C, lanes;
     bool rms;
     float eps;
 };
 
-__device__ __forceinline__ F2 both(float v) { return pack2(v, v); }
-
-// Channels c.. of a parameter, `other` without any.
+// What the arithmetic below takes: pairs of channels, or single ones where V is 1.
 template <int V>
-__device__ __forceinline__ void params(const float *p, int c, float other, F2 (&f)[(V + 1) / 2]) {
-    float v[V];
-    if (p) {
-        load_f32<V>(p + c, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = other;
+struct Lanes {
+    static constexpr int N = (V + 1) / 2;
+    using T = typename std::conditional<V == 1, float, F2>::type;
+    static __device__ __forceinline__ T both(float v) {
+        if constexpr (V == 1) return v; else return pack2(v, v);
     }
+    static __device__ __forceinline__ float sum(T v) {
+        if constexpr (V == 1) {
+            return v;
+        } else {
+            float a, b;
+            unpack2(v, a, b);
+            return a + b;
+        }
+    }
+    static __device__ __forceinline__ void values(const T (&f)[N], float (&v)[V]) {
+        if constexpr (V == 1) {
+            v[0] = f[0];
+        } else {
 #pragma unroll
-    for (int i = 0; i < (V + 1) / 2; ++i) f[i] = pack2(v[2 * i], v[V == 1 ? 0 : 2 * i + 1]);
-}
-
-// The halves' sum of a piece's pairs; a single value is in both halves.
-template <int V>
-__device__ __forceinline__ float halves(F2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    return V == 1 ? a : a + b;
-}
+            for (int k = 0; k < N; ++k) unpack2(f[k], v[2 * k], v[2 * k + 1]);
+        }
+    }
+    // Channels c.. of a parameter, `other` without any.
+    static __device__ __forceinline__ void params(const float *p, int c, float other, T (&f)[N]) {
+        float v[V];
+        if (p) {
+            load_f32<V>(p + c, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = other;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (V == 1) f[i] = v[i]; else f[i] = pack2(v[2 * i], v[2 * i + 1]);
+        }
+    }
+};
 
 // Sums of N values over the `lanes` threads of a row, for all of them. Within a warp the values
 // are shared out over the lanes as the sums go on: 6 shuffles for four values, not 20. Calls in a
@@ -121,35 +148,48 @@ __device__ __forceinline__ bool is_valid(const LayerNormParams<E> &p, int b, int
 }
 
 // The rows of a block and their ring, for TENSORS of them (x, then dy): two rows a turn where three
-// turns of them fit (one: 220 us for 182, 65536 x 4096 bf16), else one.
+// turns of them fit (one: 220 us for 182, 65536 x 4096 bf16), else one. A thread fills and reads
+// slots of its own; in bf16 rows that are not whole pieces, whose elements are less than an
+// asynchronous copy moves, the threads of a row copy the aligned pieces that it touches.
+constexpr int kMinLanes = 8;
 template <typename E, int V, int P, int THREADS, int TENSORS>
 struct RowRing {
-    // a piece, or an element: 4 bytes, the least that an asynchronous copy moves
+    static constexpr bool SHARED = V == 1 && sizeof(E) == 2;
+    // a piece, or an element of fp32
     using Slot = typename std::conditional<V == 1, float, uint4>::type;
-    static constexpr int N = (V + 1) / 2;
-    static constexpr int row_bytes = THREADS * TENSORS * P * static_cast<int>(sizeof(Slot));
+    using L = Lanes<V>;
+    using T = typename L::T;
+    static constexpr int N = L::N;
+    static constexpr int row_bytes =
+        TENSORS * (SHARED ? THREADS * P * 2 + THREADS / kMinLanes * 16 : THREADS * P * static_cast<int>(sizeof(Slot)));
     static constexpr int R = 6 * row_bytes <= 100 * 1024 ? 2 : 1;
     static constexpr int stages = 3 * R * row_bytes <= 200 * 1024 ? (R == 2 && TENSORS == 2 ? 2 : 3) : 1;
-    static constexpr int bytes = stages * R * row_bytes;
-    static_assert(bytes >= THREADS * V * 4, "the ring holds a piece of sums of every thread");
+    static constexpr int ring = stages * R * row_bytes, sums = THREADS * V * 4;
+    static constexpr int bytes = ring > sums ? ring : sums;        // sums: of a piece of every thread
 
     const LayerNormParams<E> &p;
-    Slot *mine;
+    unsigned char *memory;
     int lane, lanes, step, turns;
     int64_t first;
 
-    __device__ __forceinline__ RowRing(const LayerNormParams<E> &p, uint4 *memory)
-        : p(p), mine(reinterpret_cast<Slot *>(memory) + threadIdx.x), lane(threadIdx.x & (p.lanes - 1)),
-          lanes(p.lanes) {
+    __device__ __forceinline__ RowRing(const LayerNormParams<E> &p, uint4 *at)
+        : p(p), memory(reinterpret_cast<unsigned char *>(at)), lane(threadIdx.x & (p.lanes - 1)), lanes(p.lanes) {
         const int per_block = THREADS / lanes;
+        memory += SHARED ? threadIdx.x / lanes * (lanes * P * 2 + 16) : threadIdx.x * static_cast<int>(sizeof(Slot));
         step = gridDim.x * per_block;
         // alike for all threads
         turns = static_cast<int>((p.rows + static_cast<int64_t>(R) * step - 1) / (static_cast<int64_t>(R) * step));
         first = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / lanes;
     }
     __device__ __forceinline__ int channel(int q) const { return (q * lanes + lane) * V; }
+    __device__ __forceinline__ unsigned char *slot(int stage, int r, int n) const {
+        return memory + ((stage * R + r) * TENSORS + n) * (row_bytes / TENSORS);
+    }
+    __device__ __forceinline__ const E *source(int n, int b, int t) const {
+        return n == 0 ? p.x + (b * p.x_sb + t * p.x_st) : p.dy + (b * p.dy_sb + t * p.dy_st);
+    }
     // Asks for the rows of turn i; those that there are (-1: none).
-    __device__ __forceinline__ void fetch(int i, int stage, int (&rows)[R]) {
+    __device__ __forceinline__ void fetch(int i, int stage, int (&rows)[R]) const {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t at = first + (static_cast<int64_t>(i) * R + r) * step;
@@ -159,38 +199,79 @@ struct RowRing {
                 locate(p, static_cast<int>(at), b, t);
                 if (is_valid(p, b, t)) rows[r] = static_cast<int>(at);
             }
-            Slot *to = slot(stage, r, 0, 0);
 #pragma unroll
             for (int n = 0; n < TENSORS; ++n) {
-                const E *from = n == 0 ? p.x + (b * p.x_sb + t * p.x_st) : p.dy + (b * p.dy_sb + t * p.dy_st);
+                const E *from = source(n, b, t);
+                if constexpr (SHARED) {
+                    if (rows[r] < 0) continue;
+                    const RowCopy<E> copy(n == 0 ? p.x_span : p.dy_span, from, 0, 1, p.C);
 #pragma unroll
-                for (int q = 0; q < P; ++q, to += THREADS) {
-                    const int c = channel(q);
-                    if (rows[r] >= 0 && c < p.C) {
-                        if constexpr (V > 1)
-                            copy16_async(to, from + c);
-                        else if constexpr (sizeof(E) == 4)
-                            copy4_async(to, from + c);
-                        else
-                            *to = to_f32(from[c]);
-                    } else {
-                        memset(to, 0, sizeof(Slot));
+                    for (int k = 0; k <= P / 8; ++k) copy(slot(stage, r, n), from, p.C, k * lanes + lane);
+                } else {
+                    Slot *to = reinterpret_cast<Slot *>(slot(stage, r, n));
+#pragma unroll
+                    for (int q = 0; q < P; ++q, to += THREADS) {
+                        const int c = channel(q);
+                        if (rows[r] >= 0 && c < p.C) {
+                            if constexpr (V > 1)
+                                copy16_async(to, from + c);
+                            else
+                                copy4_async(to, from + c);
+                        } else {
+                            memset(to, 0, sizeof(Slot));
+                        }
                     }
                 }
             }
         }
         copy_commit();
     }
-    __device__ __forceinline__ Slot *slot(int stage, int r, int n, int q) const {
-        return mine + (((stage * R + r) * TENSORS + n) * P + q) * THREADS;
+    // Behind the wait for a turn's rows, and before they are filled anew: of rows that threads fill
+    // together. Between the two come the sums over threads, with the barrier that many lanes take.
+    __device__ __forceinline__ void arrived() const {
+        if (!SHARED) return;
+        if (lanes > 32) __syncthreads(); else __syncwarp();
     }
-    __device__ __forceinline__ void read(int stage, int r, int n, int q, F2 (&f)[N]) const {
+    __device__ __forceinline__ void done() const {
+        if (SHARED) __syncwarp();
+    }
+    // Single values are read once, pieces where they are needed.
+    struct Row {
+        T kept[V == 1 ? P : 1];
+    };
+    __device__ __forceinline__ void open(int stage, int r, int n, int row, Row &of) const {
         if constexpr (V == 1) {
-            f[0] = both(*slot(stage, r, n, q));
+            const E *v = nullptr;
+            if constexpr (SHARED) {
+                int b = 0, t = 0;
+                if (row >= 0) locate(p, row, b, t);
+                v = row_in_copy<E>(slot(stage, r, n), source(n, b, t));
+            }
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                if constexpr (SHARED)
+                    of.kept[q] = row >= 0 && channel(q) < p.C ? to_f32(v[channel(q)]) : 0.f;
+                else
+                    of.kept[q] = reinterpret_cast<const Slot *>(slot(stage, r, n))[q * THREADS];
+            }
+        }
+    }
+    __device__ __forceinline__ void read(const Row &of, int stage, int r, int n, int q, T (&f)[N]) const {
+        if constexpr (V == 1) {
+            f[0] = of.kept[q];
         } else {
             Piece<E, V> piece;
-            piece.raw = *slot(stage, r, n, q);
+            piece.raw = reinterpret_cast<const Slot *>(slot(stage, r, n))[q * THREADS];
             piece.widen(f);
+        }
+    }
+    static __device__ __forceinline__ void write(E *at, const T (&f)[N]) {
+        if constexpr (V == 1) {
+            *at = from_f32<E>(f[0]);
+        } else {
+            Piece<E, V> piece;
+            piece.round(f);
+            piece.store(at);
         }
     }
 };
@@ -199,6 +280,8 @@ template <typename E, int V, int P, int THREADS>
 __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
     gdn_layer_norm_kernel(const LayerNormParams<E> p) {
     using Ring = RowRing<E, V, P, THREADS, 1>;
+    using L = typename Ring::L;
+    using T = typename Ring::T;
     constexpr int N = Ring::N, R = Ring::R, S = Ring::stages;
     __shared__ float buffers[2][THREADS / 32][R];
     extern __shared__ uint4 ring_memory[];
@@ -206,13 +289,13 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
     const float inv = 1.f / p.C;
     // 16 channels' weight and bias stay in registers, more are read for every row
     constexpr bool KEEP = P * V <= 16;
-    F2 w[KEEP ? P : 1][N], bias[KEEP ? P : 1][N];
+    T w[KEEP ? P : 1][N], bias[KEEP ? P : 1][N];
     if constexpr (KEEP) {
 #pragma unroll
         for (int q = 0; q < P; ++q) {
             const int c = ring.channel(q) < p.C ? ring.channel(q) : 0;
-            params<V>(p.w, c, 1.f, w[q]);
-            params<V>(p.bias, c, 0.f, bias[q]);
+            L::params(p.w, c, 1.f, w[q]);
+            L::params(p.bias, c, 0.f, bias[q]);
         }
     }
     int rows[S][R];
@@ -221,25 +304,29 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
     int stage = 0;
     for (int i = 0; i < ring.turns; ++i) {
         copy_wait<S - 1>();
+        ring.arrived();
+        typename Ring::Row xs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) ring.open(stage, r, 0, rows[0][r], xs[r]);
         float mean[R], s[R];
-        F2 sum[R];
+        T sum[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             mean[r] = 0.f;
-            sum[r] = both(0.f);
+            sum[r] = L::both(0.f);
         }
         if (!p.rms) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
 #pragma unroll
                 for (int q = 0; q < P; ++q) {
-                    F2 v[N];
-                    ring.read(stage, r, 0, q, v);
+                    T v[N];
+                    ring.read(xs[r], stage, r, 0, q, v);
 #pragma unroll
                     for (int k = 0; k < N; ++k) sum[r] = add2(sum[r], v[k]);
                 }
-                s[r] = halves<V>(sum[r]);
-                sum[r] = both(0.f);
+                s[r] = L::sum(sum[r]);
+                sum[r] = L::both(0.f);
             }
             row_sums(s, ring.lanes, buffers[0]);
 #pragma unroll
@@ -249,16 +336,16 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
         for (int r = 0; r < R; ++r) {
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-                F2 v[N], squares = both(0.f);
-                ring.read(stage, r, 0, q, v);
+                T v[N], squares = L::both(0.f);
+                ring.read(xs[r], stage, r, 0, q, v);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    v[k] = add2(v[k], both(-mean[r]));
+                    v[k] = add2(v[k], L::both(-mean[r]));
                     squares = fma2(v[k], v[k], squares);
                 }
                 if (ring.channel(q) < p.C) sum[r] = add2(sum[r], squares);
             }
-            s[r] = halves<V>(sum[r]);
+            s[r] = L::sum(sum[r]);
         }
         // without the first sums the buffers alternate from turn to turn
         row_sums(s, ring.lanes, buffers[p.rms ? i & 1 : 1]);
@@ -272,19 +359,17 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
             for (int q = 0; q < P; ++q) {
                 const int c = ring.channel(q);
                 if (c >= p.C) break;
-                F2 v[N];
-                ring.read(stage, r, 0, q, v);
+                T v[N];
+                ring.read(xs[r], stage, r, 0, q, v);
                 constexpr int one = KEEP ? 1 : 0;
                 if constexpr (!KEEP) {
-                    params<V>(p.w, c, 1.f, w[0]);
-                    params<V>(p.bias, c, 0.f, bias[0]);
+                    L::params(p.w, c, 1.f, w[0]);
+                    L::params(p.bias, c, 0.f, bias[0]);
                 }
 #pragma unroll
                 for (int k = 0; k < N; ++k)
-                    v[k] = fma2(mul2(add2(v[k], both(-mean[r])), both(rstd)), w[q * one][k], bias[q * one][k]);
-                Piece<E, V> piece;
-                piece.round(v);
-                piece.store(y + c);
+                    v[k] = fma2(mul2(add2(v[k], L::both(-mean[r])), L::both(rstd)), w[q * one][k], bias[q * one][k]);
+                Ring::write(y + c, v);
             }
             if (p.stats && ring.lane == 0)
                 *reinterpret_cast<float2 *>(p.stats + 2LL * row) = make_float2(mean[r], rstd);
@@ -293,6 +378,7 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
         for (int k = 0; k + 1 < S; ++k)
 #pragma unroll
             for (int r = 0; r < R; ++r) rows[k][r] = rows[k + 1][r];
+        ring.done();
         ring.fetch(i + S, stage, rows[S - 1]);
         stage = stage == S - 1 ? 0 : stage + 1;
     }
@@ -303,18 +389,20 @@ template <typename E, int V, int P, int THREADS>
 __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 2))
     gdn_layer_norm_bwd_kernel(const LayerNormParams<E> p) {
     using Ring = RowRing<E, V, P, THREADS, 2>;
+    using L = typename Ring::L;
+    using T = typename Ring::T;
     constexpr int N = Ring::N, R = Ring::R, S = Ring::stages;
     __shared__ float buffers[2][THREADS / 32][2 * R];
     extern __shared__ uint4 ring_memory[];
     Ring ring(p, ring_memory);
     const float inv = 1.f / p.C;
-    F2 w[P][N], dw[P][N], db[P][N];
+    T w[P][N], dw[P][N], db[P][N];
 #pragma unroll
     for (int q = 0; q < P; ++q) {
         const int c = ring.channel(q);
 #pragma unroll
-        for (int k = 0; k < N; ++k) dw[q][k] = db[q][k] = both(0.f);
-        params<V>(p.w, c < p.C ? c : 0, 1.f, w[q]);
+        for (int k = 0; k < N; ++k) dw[q][k] = db[q][k] = L::both(0.f);
+        L::params(p.w, c < p.C ? c : 0, 1.f, w[q]);
     }
     int rows[S][R];
     float2 stats[R], next[R];
@@ -330,57 +418,63 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 2))
     for (int i = 0; i < ring.turns; ++i) {
         if constexpr (S > 1) stats_of(rows[1], next);      // asked for a turn ahead
         copy_wait<S - 1>();
+        ring.arrived();
+        typename Ring::Row xs[R], dys[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            ring.open(stage, r, 0, rows[0][r], xs[r]);
+            ring.open(stage, r, 1, rows[0][r], dys[r]);
+        }
         float s[2 * R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const F2 minus = both(-stats[r].x), rstd = both(stats[r].y);
-            F2 s1 = both(0.f), s2 = both(0.f);
+            const T minus = L::both(-stats[r].x), rstd = L::both(stats[r].y);
+            T s1 = L::both(0.f), s2 = L::both(0.f);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-                F2 x[N], dy[N];
-                ring.read(stage, r, 0, q, x);
-                ring.read(stage, r, 1, q, dy);
+                T x[N], dy[N];
+                ring.read(xs[r], stage, r, 0, q, x);
+                ring.read(dys[r], stage, r, 1, q, dy);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const F2 xhat = mul2(add2(x[k], minus), rstd), v = mul2(dy[k], w[q][k]);
+                    const T xhat = mul2(add2(x[k], minus), rstd), v = mul2(dy[k], w[q][k]);
                     db[q][k] = add2(db[q][k], dy[k]);
                     dw[q][k] = fma2(dy[k], xhat, dw[q][k]);
                     s1 = add2(s1, v);
                     s2 = fma2(v, xhat, s2);
                 }
             }
-            s[2 * r] = halves<V>(s1);
-            s[2 * r + 1] = halves<V>(s2);
+            s[2 * r] = L::sum(s1);
+            s[2 * r + 1] = L::sum(s2);
         }
         row_sums(s, ring.lanes, buffers[i & 1]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = rows[0][r];
             if (row < 0) continue;
-            const F2 minus = both(-stats[r].x), rstd = both(stats[r].y);
-            const F2 c1 = both(p.rms ? 0.f : -s[2 * r] * inv), c2 = both(-s[2 * r + 1] * inv);
+            const T minus = L::both(-stats[r].x), rstd = L::both(stats[r].y);
+            const T c1 = L::both(p.rms ? 0.f : -s[2 * r] * inv), c2 = L::both(-s[2 * r + 1] * inv);
             E *dx = p.dx + static_cast<int64_t>(row) * p.C;
 #pragma unroll
             for (int q = 0; q < P; ++q) {
                 const int c = ring.channel(q);
                 if (c >= p.C) break;
-                F2 x[N], dy[N];
-                ring.read(stage, r, 0, q, x);
-                ring.read(stage, r, 1, q, dy);
+                T x[N], dy[N];
+                ring.read(xs[r], stage, r, 0, q, x);
+                ring.read(dys[r], stage, r, 1, q, dy);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const F2 xhat = mul2(add2(x[k], minus), rstd);
+                    const T xhat = mul2(add2(x[k], minus), rstd);
                     x[k] = mul2(rstd, fma2(xhat, c2, fma2(dy[k], w[q][k], c1)));
                 }
-                Piece<E, V> piece;
-                piece.round(x);
-                piece.store(dx + c);
+                Ring::write(dx + c, x);
             }
         }
 #pragma unroll
         for (int k = 0; k + 1 < S; ++k)
 #pragma unroll
             for (int r = 0; r < R; ++r) rows[k][r] = rows[k + 1][r];
+        ring.done();
         ring.fetch(i + S, stage, rows[S - 1]);
         if constexpr (S == 1) stats_of(rows[0], next);
 #pragma unroll
@@ -398,9 +492,8 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 2))
 #pragma unroll
         for (int q = 0; q < P; ++q) {
             const int c = ring.channel(q);
-            float f[2 * N];
-#pragma unroll
-            for (int k = 0; k < N; ++k) unpack2(which ? db[q][k] : dw[q][k], f[2 * k], f[2 * k + 1]);
+            float f[V];
+            if (which) L::values(db[q], f); else L::values(dw[q], f);
             if (per_block > 1) {
                 __syncthreads();
 #pragma unroll
@@ -530,6 +623,7 @@ LayerNormParams<E> params(const gdn_layer_norm_problem *p, const void *x, const 
     a.B = p->B; a.T = p->T; a.C = p->C;
     a.rms = (p->flags & GDN_LAYER_NORM_RMS) != 0;
     a.eps = p->eps;
+    a.x_span = row_span(x, p->B, p->T, p->C, a.x_sb, a.x_st, sizeof(E));
     return a;
 }
 
@@ -549,7 +643,7 @@ void flatten(LayerNormParams<E> &p) {
 template <typename E, int V, int P, int THREADS, int TENSORS>
 cudaError_t launch_rows(LayerNormParams<E> &p, int &blocks, cudaStream_t s) {
     using Ring = RowRing<E, V, P, THREADS, TENSORS>;
-    p.lanes = 1;
+    p.lanes = V == 1 ? kMinLanes : 1;
     while (p.lanes * P < p.C / V) p.lanes *= 2;
     const int per_block = THREADS / p.lanes, sm = blocks_to_sm(P, THREADS, TENSORS);
     const int64_t all = (static_cast<int64_t>(p.rows) + per_block - 1) / per_block;
@@ -562,19 +656,18 @@ cudaError_t launch_rows(LayerNormParams<E> &p, int &blocks, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// By the pieces of a row: a block of 256 threads with up to two 16-byte pieces (eight channels) to a
-// thread, then of 512 with what its registers hold. `held`: whether they hold a row.
+// By the pieces of a row: a block of 256 threads with two pieces (8 or 16 single channels) to a thread,
+// then of 512 with what its registers hold. `held`: whether they hold a row.
 template <typename E, int V, int TENSORS>
 cudaError_t by_pieces(LayerNormParams<E> &p, int &blocks, bool &held, cudaStream_t s) {
     const int pieces = p.C / V;
     held = true;
-    if (pieces <= 256) return launch_rows<E, V, 1, 256, TENSORS>(p, blocks, s);
-    if (pieces <= 512) return launch_rows<E, V, 2, 256, TENSORS>(p, blocks, s);
     if constexpr (V == 1) {
-        if (pieces <= 1024) return launch_rows<E, V, 4, 256, TENSORS>(p, blocks, s);
         if (pieces <= 2048) return launch_rows<E, V, 8, 256, TENSORS>(p, blocks, s);
+        if (pieces <= 4096) return launch_rows<E, V, 16, 256, TENSORS>(p, blocks, s);
         if (pieces <= 8192) return launch_rows<E, V, 16, 512, TENSORS>(p, blocks, s);
     } else {
+        if (pieces <= 512) return launch_rows<E, V, 2, 256, TENSORS>(p, blocks, s);
         if (pieces <= 1024) return launch_rows<E, V, 2, 512, TENSORS>(p, blocks, s);
         if (pieces <= 2048) return launch_rows<E, V, 4, 512, TENSORS>(p, blocks, s);
         if constexpr (V <= 4)
@@ -696,6 +789,7 @@ GDN_API gdn_status gdn_layer_norm_bwd(const gdn_layer_norm_problem *p, const voi
         using E = decltype(tag);
         LayerNormParams<E> a = params<E>(p, x, lengths);
         a.dy = static_cast<const E *>(dy);
+        a.dy_span = row_span(dy, p->B, p->T, p->C, a.dy_sb, a.dy_st, e);
         a.stats_in = stats;
         a.w = weight;
         a.dx = static_cast<E *>(dx);
