@@ -10,6 +10,12 @@
 // rows, whose sums over threads share their shuffles and barriers: the mean, then the squares
 // about it; in the backward pass both sums at once. Rows beyond what a block holds go to the
 // *_wide_* kernels, a block to a row that it reads again for each sum.
+//
+// 65536 x 4096 bf16: 180 us, 5.97 TB/s (89% of a plain copy's 6.68), the gradients 254 us, 6.35 TB/s
+// (95%), 6 us of them the sums over the blocks' rows. A block to a row with every value read three
+// times took 434 and 2189 us; a part of a warp to a row, weight and bias read for each, 246. fp32
+// 32768 x 4096: 177 and 266 us; rows of 1003: bf16 62 and 88, fp32 68 and 105 (element by element
+// with 4 elements to a thread, 256 threads to a row: 284 and 142 the norm).
 #include "columns.cuh"
 #include "rows.cuh"
 

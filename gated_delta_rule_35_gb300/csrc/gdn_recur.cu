@@ -1,8 +1,16 @@
 // The gated linear recurrence: gdn_recur_fwd of include/gdn.h.
 //
-// Bound by memory: one read of x, decay and gate and one write of y; instructions (about 30 to a
-// value) and their special functions come close to it. recur.cuh describes the tiles; a few
-// tokens go to a kernel of their own, a thread to four channels of a sequence.
+// One read of x, decay and gate and one write of y, 8 bytes a value in bf16, against 34 instructions
+// a value, five of them special functions. recur.cuh describes the tiles; a few tokens go to a
+// kernel of their own, a thread to four channels of a sequence.
+//
+// B4 T2048 D4096 bf16, states kept: 59 us, 4.66 TB/s (70% of a plain copy's 6.68); 45 us with the
+// arithmetic left out and 4 less without the exchange. 256 blocks on 152 SMs load 84% of their
+// places, and where there are two the schedulers issue in 70% of the cycles. T32768 D2048, one
+// sequence in clusters of 8: 145 us, 3.70 TB/s; 100 without the exchange, whose barrier of the
+// cluster takes 1.4 us for every 1024 tokens. fp32 B4 T2048 D4096 93 us, 5.8 TB/s. Rows that are not
+// whole pieces (D4097): 140 us in bf16, 224 in fp32. Tiles of 8 tokens to a warp with three times
+// the warps took 66 to 76 us for 64, one with a ring of one tile 64.
 #include <utility>
 
 #include "recur.cuh"

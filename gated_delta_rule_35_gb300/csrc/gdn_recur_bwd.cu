@@ -6,8 +6,14 @@
 // anew from the state that the forward pass kept for them:
 //   dx = lam m q,  dgate = lam m q (1 - q) x,  dlog = lam (a h_before + q x dm/dlog a)
 //   ddecay = -dlog rate s (1 - s) (or dlog (1 - a)),  drate = -sum dlog s
-// with dm/dlog a = -a^2 / m for the root, -a for the complement. Bound by memory: four tensors
-// read and three written, the states a thirtieth of that.
+// with dm/dlog a = -a^2 / m for the root, -a for the complement. Four tensors read and three
+// written, the states a thirtieth of that: 14 bytes a value in bf16, against 67 instructions; the
+// factors are computed twice, since lam needs those of later tokens and registers hold one array.
+//
+// B4 T2048 D4096 bf16: 121 us, 3.96 TB/s (59% of a plain copy's 6.68); T32768 D2048 244 us, 3.93 TB/s;
+// fp32 B4 T2048 D4096 164 us, 5.8 TB/s. Ten to twelve warps of 166 registers to an SM issue in 56% of
+// the cycles. 128 registers and 16 warps with a ring of one tile: 126 us for 132 then, but 281 for
+// 263 on T32768.
 #include <utility>
 
 #include "recur.cuh"

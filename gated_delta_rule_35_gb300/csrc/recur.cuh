@@ -9,7 +9,10 @@
 //   across warps     each warp passes the block's state through the (A, H) of the warps before it;
 //   across blocks    with few channels a cluster of blocks takes consecutive tiles and every
 //                    block passes the state through the others' (A, H) first.
-// So every input is read once and every output written once, whatever the length.
+// So every input is read once and every output written once, whatever the length. A thread to a
+// channel over all tokens, in their order, took 2198 us for 59 (B4 T2048 D4096 bf16, 16384 channels)
+// and 34 ms for 145 us (T32768 D2048); lanes of four channels and 8 tokens would shuffle between
+// halves of a warp.
 #pragma once
 
 #include "columns.cuh"
