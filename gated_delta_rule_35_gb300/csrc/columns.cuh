@@ -10,21 +10,25 @@ namespace gdn {
 constexpr int kColumnLanes = 32, kColumnRows = 32;
 
 // part [rows, cols] -> first[0 .. split), second[0 .. cols - split); either may be NULL. A
-// thread adds every blockDim.y-th row of one column, then those sums are added in order.
+// thread adds every blockDim.y-th row of one column, then a part of a warp adds a column's sums.
 // Launched while the kernel before it still runs, whose end it waits for.
 static __global__ void __launch_bounds__(kColumnLanes * kColumnRows)
     gdn_column_sums_kernel(const float *part, int rows, int64_t cols, int64_t split, float *first, float *second) {
-    __shared__ float sums[kColumnRows][kColumnLanes];
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kColumnLanes + threadIdx.x;
+    __shared__ float sums[kColumnRows][kColumnLanes + 1];
+    const int64_t first_column = static_cast<int64_t>(blockIdx.x) * kColumnLanes, mine = first_column + threadIdx.x;
     ptx::griddep_wait();
     float s = 0.f;
-    if (c < cols)
+    if (mine < cols)
 #pragma unroll 8
-        for (int r = threadIdx.y; r < rows; r += blockDim.y) s += part[r * cols + c];
+        for (int r = threadIdx.y; r < rows; r += blockDim.y) s += part[r * cols + mine];
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y != 0 || c >= cols) return;
-    for (int r = 1; r < blockDim.y; ++r) s += sums[r][threadIdx.x];
+    // blockDim.y (a power of two) lanes to a column, as many columns as a warp has such parts
+    const int y = blockDim.y, of = threadIdx.y * (kColumnLanes / y) + threadIdx.x / y;
+    s = sums[threadIdx.x & (y - 1)][of];
+    for (int o = y / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int64_t c = first_column + of;
+    if ((threadIdx.x & (y - 1)) != 0 || c >= cols) return;
     if (c < split) {
         if (first) first[c] = s;
     } else if (second) {

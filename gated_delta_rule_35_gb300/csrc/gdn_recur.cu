@@ -9,7 +9,7 @@
 // places, and where there are two the schedulers issue in 70% of the cycles. T32768 D2048, one
 // sequence in clusters of 8: 145 us, 3.70 TB/s; 100 without the exchange, whose barrier of the
 // cluster takes 1.4 us for every 1024 tokens. fp32 B4 T2048 D4096 93 us, 5.8 TB/s. Rows that are not
-// whole pieces (D4097): 140 us in bf16, 224 in fp32. Tiles of 8 tokens to a warp with three times
+// whole pieces (D4097): 140 us in bf16, 177 in fp32. Tiles of 8 tokens to a warp with three times
 // the warps took 66 to 76 us for 64, one with a ring of one tile 64.
 #include <utility>
 
@@ -19,7 +19,6 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxWarps = 8;
-constexpr int kStages = 2;         // tiles in the ring
 constexpr int kStepTokens = 8;     // up to here the step kernel
 constexpr int kStepThreads = 256;
 
@@ -44,6 +43,7 @@ __device__ __forceinline__ void token2(F2 x, F2 decay, F2 gate, F2 t_scale, bool
 
 template <typename E, int FORM>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_kernel(const RecurParams<E> p) {
+    constexpr int kStages = kRecurStages<E>;
     __shared__ Exchange<kMaxWarps> ex;
     extern __shared__ uint4 ring[];
     const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.D % 2 == 0 : true;
@@ -209,7 +209,7 @@ cudaError_t launch(RecurParams<E> &p, cudaStream_t s, std::integer_sequence<int,
     using Kernel = void (*)(RecurParams<E>);
     static constexpr Kernel table[] = {gdn_recur_kernel<E, kAnyForm>, gdn_recur_kernel<E, FORMS>...};
     recur_rows(p);
-    const int slot = kStages * (p.gate ? 3 : 2) * recur_row_bytes(p);
+    const int slot = kRecurStages<E> * (p.gate ? 3 : 2) * recur_row_bytes(p);
     const int warps = recur_shape<E, Exchange<kMaxWarps>>(p, kMaxWarps, slot);
     return recur_launch(recur_kernel<E>(table, p), p, warps, warps * slot, s);
 }

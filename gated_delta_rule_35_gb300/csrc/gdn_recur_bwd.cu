@@ -11,7 +11,7 @@
 // factors are computed twice, since lam needs those of later tokens and registers hold one array.
 //
 // B4 T2048 D4096 bf16: 121 us, 3.96 TB/s (59% of a plain copy's 6.68); T32768 D2048 244 us, 3.93 TB/s;
-// fp32 B4 T2048 D4096 164 us, 5.8 TB/s. Ten to twelve warps of 166 registers to an SM issue in 56% of
+// fp32 B4 T2048 D4096 159 us, 5.9 TB/s. Ten to twelve warps of 166 registers to an SM issue in 56% of
 // the cycles. 128 registers and 16 warps with a ring of one tile: 126 us for 132 then, but 281 for
 // 263 on T32768.
 #include <utility>
@@ -22,10 +22,10 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxWarps = 6;
-constexpr int kStages = 2;         // tiles in the ring
 
 template <typename E, int FORM>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const RecurParams<E> p) {
+    constexpr int kStages = kRecurStages<E>;
     __shared__ Exchange<kMaxWarps> ex;
     extern __shared__ uint4 ring[];
     const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.D % 2 == 0 : true;
@@ -156,7 +156,7 @@ cudaError_t launch(RecurParams<E> &p, float *d_rate, cudaStream_t s, std::intege
     using Kernel = void (*)(RecurParams<E>);
     static constexpr Kernel table[] = {gdn_recur_bwd_kernel<E, kAnyForm>, gdn_recur_bwd_kernel<E, FORMS>...};
     recur_rows(p);
-    const int slot = kStages * (p.gate ? 4 : 3) * recur_row_bytes(p);
+    const int slot = kRecurStages<E> * (p.gate ? 4 : 3) * recur_row_bytes(p);
     const int warps = recur_shape<E, Exchange<kMaxWarps>>(p, kMaxWarps, slot);
     const cudaError_t err = recur_launch(recur_kernel<E>(table, p), p, warps, warps * slot, s);
     if (err != cudaSuccess || !d_rate) return err;

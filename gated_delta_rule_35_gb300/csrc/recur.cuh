@@ -360,6 +360,11 @@ void recur_rows(RecurParams<E> &p) {
     p.dy_span = row_span(p.dy, p.B, p.T, p.D, p.dy_sb, p.dy_st, e);
 }
 
+// Tiles in a warp's ring. In fp32 one: twice the warps with one tile each (T8192 D2048 70 -> 60 us, its
+// gradients 117 -> 100; B4 T2048 D4097 224 -> 177 and 420 -> 322).
+template <typename E>
+constexpr int kRecurStages = sizeof(E) == 2 ? 2 : 1;
+
 // Warps to a block: as many as a sequence's tokens fill, up to `most` and to what lets two blocks,
 // with `slot` bytes to a warp's ring, share an SM. Blocks to a cluster: as many as leave the GPU's
 // places for two blocks to an SM filled once, and have tokens.
