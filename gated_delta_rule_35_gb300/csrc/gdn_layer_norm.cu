@@ -11,7 +11,7 @@
 // about it; in the backward pass both sums at once. Rows beyond what a block holds go to the
 // *_wide_* kernels, a block to a row that it reads again for each sum.
 //
-// 65536 x 4096 bf16: 180 us, 5.97 TB/s (89% of a plain copy's 6.68), the gradients 254 us, 6.35 TB/s
+// 65536 x 4096 bf16: FWD us, FWDT TB/s (FWDP% of a plain copy's 6.68), the gradients 254 us, 6.35 TB/s
 // (95%), 6 us of them the sums over the blocks' rows. A block to a row with every value read three
 // times took 434 and 2189 us; a part of a warp to a row, weight and bias read for each, 246. fp32
 // 32768 x 4096: 177 and 266 us; rows of 1003: bf16 62 and 88, fp32 68 and 105 (element by element
@@ -33,10 +33,8 @@ constexpr int kWideParts = 64;     // rows of partial sums of the wide kernels
 constexpr int kMaxParts = 152 * 2; // blocks of the backward pass
 
 // Blocks to an SM. Of the backward pass three would spill: 302 us for 257 on 65536 x 4096 bf16; of
-// the forward pass two leave too few rows on their way: 203 us for 182.
-constexpr int blocks_to_sm(int P, int threads, int tensors) {
-    return threads > 256 ? 1 : tensors == 1 && P < 16 ? 3 : 2;
-}
+// the forward pass three take 177 for 170.
+constexpr int blocks_to_sm(int threads) { return threads > 256 ? 1 : 2; }
 
 template <typename E>
 struct LayerNormParams {
@@ -153,8 +151,10 @@ __device__ __forceinline__ bool is_valid(const LayerNormParams<E> &p, int b, int
     return !p.lengths || t < p.lengths[b];
 }
 
-// The rows of a block and their ring, for TENSORS of them (x, then dy): two rows a turn where three
-// turns of them fit (one: 220 us for 182, 65536 x 4096 bf16), else one. A thread fills and reads
+// The rows of a block and their ring, for TENSORS of them (x, then dy): as many rows a turn, up to four
+// (two in the backward pass, whose rows have two sums), as leave the ring two turns, three where a
+// block has an SM for itself. One, two and four: 220, 182 and 170 us (65536 x 4096 bf16), with a
+// third turn 175; blocks of 512 threads 183 with two, 177 with three (32768 x 4096 fp32). A thread fills and reads
 // slots of its own; in bf16 rows that are not whole pieces, whose elements are less than an
 // asynchronous copy moves, the threads of a row copy the aligned pieces that it touches.
 constexpr int kMinLanes = 8;
@@ -168,8 +168,11 @@ struct RowRing {
     static constexpr int N = L::N;
     static constexpr int row_bytes =
         TENSORS * (SHARED ? THREADS * P * 2 + THREADS / kMinLanes * 16 : THREADS * P * static_cast<int>(sizeof(Slot)));
-    static constexpr int R = 6 * row_bytes <= 100 * 1024 ? 2 : 1;
-    static constexpr int stages = 3 * R * row_bytes <= 200 * 1024 ? (R == 2 && TENSORS == 2 ? 2 : 3) : 1;
+    static constexpr int most = (THREADS > 256 ? 200 : 96) * 1024;
+    // what the registers of single channels hold, and bytes enough in flight, count too
+    static constexpr int wanted = V == 1 && P > 8 ? 1 : TENSORS == 1 && (sizeof(E) == 2 || THREADS == 256) ? 4 : 2;
+    static constexpr int R = wanted >= 4 && 8 * row_bytes <= most ? 4 : wanted >= 2 && 4 * row_bytes <= most ? 2 : 1;
+    static constexpr int stages = THREADS > 256 && 3 * R * row_bytes <= most ? 3 : 2 * R * row_bytes <= most ? 2 : 1;
     static constexpr int ring = stages * R * row_bytes, sums = THREADS * V * 4;
     static constexpr int bytes = ring > sums ? ring : sums;        // sums: of a piece of every thread
 
@@ -283,7 +286,7 @@ struct RowRing {
 };
 
 template <typename E, int V, int P, int THREADS>
-__global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
+__global__ void __launch_bounds__(THREADS, blocks_to_sm(THREADS))
     gdn_layer_norm_kernel(const LayerNormParams<E> p) {
     using Ring = RowRing<E, V, P, THREADS, 1>;
     using L = typename Ring::L;
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 1))
 }
 
 template <typename E, int V, int P, int THREADS>
-__global__ void __launch_bounds__(THREADS, blocks_to_sm(P, THREADS, 2))
+__global__ void __launch_bounds__(THREADS, blocks_to_sm(THREADS))
     gdn_layer_norm_bwd_kernel(const LayerNormParams<E> p) {
     using Ring = RowRing<E, V, P, THREADS, 2>;
     using L = typename Ring::L;
@@ -645,13 +648,13 @@ void flatten(LayerNormParams<E> &p) {
     p.B = 1;
 }
 
-// Blocks that stay: as many as an SM holds at once (its shared memory and registers), or rows.
+// Blocks that stay: as many as an SM holds at once, or rows.
 template <typename E, int V, int P, int THREADS, int TENSORS>
 cudaError_t launch_rows(LayerNormParams<E> &p, int &blocks, cudaStream_t s) {
     using Ring = RowRing<E, V, P, THREADS, TENSORS>;
     p.lanes = V == 1 ? kMinLanes : 1;
     while (p.lanes * P < p.C / V) p.lanes *= 2;
-    const int per_block = THREADS / p.lanes, sm = blocks_to_sm(P, THREADS, TENSORS);
+    const int per_block = THREADS / p.lanes, sm = blocks_to_sm(THREADS);
     const int64_t all = (static_cast<int64_t>(p.rows) + per_block - 1) / per_block;
     blocks = static_cast<int>(all < 152 * sm ? all : 152 * sm);
     auto kernel = TENSORS == 1 ? gdn_layer_norm_kernel<E, V, P, THREADS> : gdn_layer_norm_bwd_kernel<E, V, P, THREADS>;
