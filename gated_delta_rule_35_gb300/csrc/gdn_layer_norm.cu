@@ -2,8 +2,9 @@
 // of include/gdn.h.
 //
 // Bound by memory: x read and y written; in the backward pass x and dy read and dx written. Blocks
-// stay for many rows. A row is held by `lanes` threads (a power of two) in pieces of V channels
-// (16 bytes, or one channel where rows are not whole 16-byte pieces), P to a thread, which keeps its
+// stay for many rows. A row is held by `lanes` threads (a power of two up to a warp, or whole
+// warps) in pieces of V channels (16 bytes, or one channel where rows are not whole 16-byte
+// pieces), P to a thread, which keeps its
 // channels: weight and bias stay in registers, and so do the sums over rows that are their
 // gradients, of which every block leaves a row of partial sums. The rows of the next turns are on
 // their way to shared memory meanwhile (cp.async, a ring of a thread's own). A turn takes R
@@ -11,11 +12,12 @@
 // about it; in the backward pass both sums at once. Rows beyond what a block holds go to the
 // *_wide_* kernels, a block to a row that it reads again for each sum.
 //
-// 65536 x 4096 bf16: FWD us, FWDT TB/s (FWDP% of a plain copy's 6.68), the gradients 254 us, 6.35 TB/s
+// 65536 x 4096 bf16: 166 us, 6.47 TB/s (97% of a plain copy's 6.68), the gradients 254 us, 6.35 TB/s
 // (95%), 6 us of them the sums over the blocks' rows. A block to a row with every value read three
 // times took 434 and 2189 us; a part of a warp to a row, weight and bias read for each, 246. fp32
-// 32768 x 4096: 177 and 266 us; rows of 1003: bf16 62 and 88, fp32 68 and 105 (element by element
-// with 4 elements to a thread, 256 threads to a row: 284 and 142 the norm).
+// 32768 x 4096: 177 and 251 us; 65536 x 2560 bf16 130 and 191 (154 and 227 with a power of two of
+// threads to a row); rows of 1003: bf16 60 and 83, fp32 66 and 104 (element by element with 4 elements
+// to a thread: 284 and 142 the norm).
 #include "columns.cuh"
 #include "rows.cuh"
 
@@ -91,12 +93,13 @@ struct Lanes {
     }
 };
 
-// Sums of N values over the `lanes` threads of a row, for all of them. Within a warp the values
+// Sums of N values over the `lanes` threads of a row, whose first warp is `first_warp` where they are
+// whole warps, for all of them. Within a warp the values
 // are shared out over the lanes as the sums go on: 6 shuffles for four values, not 20. Calls in a
 // row alternate between two `buffer`s.
 template <int N, int WARPS>
-__device__ __forceinline__ void row_sums(float (&v)[N], int lanes, float (&buffer)[WARPS][N]) {
-    static_assert(N == 1 || N == 2 || N == 4, "values");
+__device__ __forceinline__ void row_sums(float (&v)[N], int lanes, int first_warp, float (&buffer)[WARPS][N]) {
+    static_assert((N == 1 || N == 2 || N == 4) && WARPS * N <= 64, "values");
     constexpr uint32_t all = 0xffffffffu;
     if (lanes < 32) {
 #pragma unroll
@@ -127,15 +130,22 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int lanes, float (&buffe
         for (int i = 0; i < N; ++i) v[i] = __shfl_sync(all, s, i * per);
         return;
     }
-    const int warp = threadIdx.x / 32, warps = lanes / 32, first = warp & ~(warps - 1);
-    if (lane % per == 0) buffer[warp][lane / per] = s;
+    if (lane % per == 0) buffer[threadIdx.x / 32][lane / per] = s;
     __syncthreads();
-    // value i of warp w at i + N w: a lane takes every 32nd
-    const float *from = &buffer[first][0];
-    const int count = warps * N;
-    s = from[lane & (count - 1)];
-    if (count > 32) s += from[lane + 32];
-    for (int q = N; q < 32 && q < count; q *= 2) s += __shfl_xor_sync(all, s, q);
+    // value i of warp w at i + N w: a lane takes every 32nd, the same value of each (16 warps at most);
+    // a power of two of them without bounds: 169 us for 179 (65536 x 4096 bf16)
+    const float *from = &buffer[first_warp][0];
+    const int count = lanes / 32 * N;
+    if ((count & (count - 1)) == 0) {
+        s = from[lane & (count - 1)];
+        if (count > 32) s += from[lane + 32];
+        for (int q = N; q < 32 && q < count; q *= 2) s += __shfl_xor_sync(all, s, q);
+    } else {
+        s = lane < count ? from[lane] : 0.f;
+        if (lane + 32 < count) s += from[lane + 32];
+#pragma unroll
+        for (int q = N; q < 32; q *= 2) s += __shfl_xor_sync(all, s, q);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = __shfl_sync(all, s, i);
 }
@@ -178,12 +188,13 @@ struct RowRing {
 
     const LayerNormParams<E> &p;
     unsigned char *memory;
-    int lane, lanes, step, turns;
+    int lane, lanes, first_warp, step, turns;
     int64_t first;
 
     __device__ __forceinline__ RowRing(const LayerNormParams<E> &p, uint4 *at)
-        : p(p), memory(reinterpret_cast<unsigned char *>(at)), lane(threadIdx.x & (p.lanes - 1)), lanes(p.lanes) {
-        const int per_block = THREADS / lanes;
+        : p(p), memory(reinterpret_cast<unsigned char *>(at)), lane(threadIdx.x % p.lanes), lanes(p.lanes) {
+        const int per_block = blockDim.x / lanes;
+        first_warp = threadIdx.x / lanes * (lanes / 32);
         memory += SHARED ? threadIdx.x / lanes * (lanes * P * 2 + 16) : threadIdx.x * static_cast<int>(sizeof(Slot));
         step = gridDim.x * per_block;
         // alike for all threads
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(THREADS))
                 s[r] = L::sum(sum[r]);
                 sum[r] = L::both(0.f);
             }
-            row_sums(s, ring.lanes, buffers[0]);
+            row_sums(s, ring.lanes, ring.first_warp, buffers[0]);
 #pragma unroll
             for (int r = 0; r < R; ++r) mean[r] = s[r] * inv;
         }
@@ -357,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(THREADS))
             s[r] = L::sum(sum[r]);
         }
         // without the first sums the buffers alternate from turn to turn
-        row_sums(s, ring.lanes, buffers[p.rms ? i & 1 : 1]);
+        row_sums(s, ring.lanes, ring.first_warp, buffers[p.rms ? i & 1 : 1]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = rows[0][r];
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(THREADS))
             s[2 * r] = L::sum(s1);
             s[2 * r + 1] = L::sum(s2);
         }
-        row_sums(s, ring.lanes, buffers[i & 1]);
+        row_sums(s, ring.lanes, ring.first_warp, buffers[i & 1]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = rows[0][r];
@@ -493,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, blocks_to_sm(THREADS))
     copy_wait<0>();
     if (!p.part) return;
     // Rows that the block held at once are added up through the ring's memory, in order.
-    const int lanes = ring.lanes, per_block = THREADS / lanes;
+    const int lanes = ring.lanes, per_block = blockDim.x / lanes;
     float *sums = reinterpret_cast<float *>(ring_memory);          // [value][thread]
     float *part = p.part + blockIdx.x * 2LL * p.C;
 #pragma unroll
@@ -652,8 +663,10 @@ void flatten(LayerNormParams<E> &p) {
 template <typename E, int V, int P, int THREADS, int TENSORS>
 cudaError_t launch_rows(LayerNormParams<E> &p, int &blocks, cudaStream_t s) {
     using Ring = RowRing<E, V, P, THREADS, TENSORS>;
+    const int threads = (p.C / V + P - 1) / P;         // that a row needs
     p.lanes = V == 1 ? kMinLanes : 1;
-    while (p.lanes * P < p.C / V) p.lanes *= 2;
+    while (p.lanes < 32 && p.lanes < threads) p.lanes *= 2;
+    if (threads > 32) p.lanes = (threads + 31) / 32 * 32;
     const int per_block = THREADS / p.lanes, sm = blocks_to_sm(THREADS);
     const int64_t all = (static_cast<int64_t>(p.rows) + per_block - 1) / per_block;
     blocks = static_cast<int>(all < 152 * sm ? all : 152 * sm);
@@ -661,7 +674,7 @@ cudaError_t launch_rows(LayerNormParams<E> &p, int &blocks, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, Ring::bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks, THREADS, Ring::bytes, s>>>(p);
+    kernel<<<blocks, per_block * p.lanes, Ring::bytes, s>>>(p);
     return cudaGetLastError();
 }
 
