@@ -24,7 +24,8 @@ static __global__ void __launch_bounds__(kColumnLanes * kColumnRows)
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     // blockDim.y (a power of two) lanes to a column, as many columns as a warp has such parts
-    const int y = blockDim.y, of = threadIdx.y * (kColumnLanes / y) + threadIdx.x / y;
+    const int y = blockDim.y, shift = __ffs(y) - 1;
+    const int of = threadIdx.y * (kColumnLanes >> shift) + (threadIdx.x >> shift);
     s = sums[threadIdx.x & (y - 1)][of];
     for (int o = y / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
     const int64_t c = first_column + of;

@@ -26,7 +26,7 @@ constexpr int kThreads = 128;
 constexpr int kChannels = 4;    // of a thread
 constexpr int kUnroll = 4;      // tokens per turn
 constexpr int kStages = 3;      // turns in the ring
-constexpr int kMinRun = 8;
+constexpr int kMinRun = 8, kMinPieces = 8;
 static_assert(kMinRun >= kUnroll && kUnroll >= 3, "W - 1");
 
 template <typename E>
@@ -373,7 +373,7 @@ struct Shape {
 Shape shape(const gdn_conv_bwd_problem *p) {
     const int64_t cv = (p->C + kChannels - 1) / kChannels;
     Shape s;
-    s.pieces = 8;
+    s.pieces = kMinPieces;
     while (s.pieces < 32 && s.pieces < cv) s.pieces *= 2;
     s.groups = static_cast<int>((cv + s.pieces - 1) / s.pieces);
     const int per_block = kThreads / s.pieces;
@@ -402,15 +402,18 @@ cudaError_t launch(const gdn_conv_bwd_problem *pr, ConvBwdParams<E> &p, float *d
     p.runs_of_one = cut.runs_of_one;
     p.runs = cut.runs;
     if (cut.blocks * cut.groups > INT32_MAX) return cudaErrorInvalidValue;
-    const int ring = kStages * kUnroll * 2 * token_bytes<E, !WHOLE && sizeof(E) == 2>(cut.pieces);
-    constexpr int sums = kChannels * (W + 1) * kThreads * 4;
-    const int bytes = ring > sums ? ring : sums;
+    constexpr auto shared_bytes = [](int pieces) {
+        const int ring = kStages * kUnroll * 2 * token_bytes<E, !WHOLE && sizeof(E) == 2>(pieces);
+        const int sums = kChannels * (W + 1) * kThreads * 4;
+        return ring > sums ? ring : sums;
+    };
     auto kernel = pr->act == GDN_ACT_SILU ? gdn_conv_bwd_kernel<E, W, WHOLE, true>
                                           : gdn_conv_bwd_kernel<E, W, WHOLE, false>;
+    // one bound for all calls: a call of another size on another thread must not lower it
     cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes(kMinPieces));
     if (err != cudaSuccess) return err;
-    kernel<<<static_cast<unsigned>(cut.blocks * cut.groups), kThreads, bytes, s>>>(p);
+    kernel<<<static_cast<unsigned>(cut.blocks * cut.groups), kThreads, shared_bytes(cut.pieces), s>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     const int64_t taps = static_cast<int64_t>(pr->C) * W;

@@ -365,12 +365,14 @@ void recur_rows(RecurParams<E> &p) {
 template <typename E>
 constexpr int kRecurStages = sizeof(E) == 2 ? 2 : 1;
 
+constexpr int kBlockShared = 228 * 1024 / 2 - 1024;    // of one of two blocks to an SM
+
 // Warps to a block: as many as a sequence's tokens fill, up to `most` and to what lets two blocks,
 // with `slot` bytes to a warp's ring, share an SM. Blocks to a cluster: as many as leave the GPU's
 // places for two blocks to an SM filled once, and have tokens.
 template <typename E, typename X>
 int recur_shape(RecurParams<E> &p, int most, int slot) {
-    const int fit = (228 * 1024 / 2 - 1024 - static_cast<int>(sizeof(X))) / slot;
+    const int fit = (kBlockShared - static_cast<int>(sizeof(X))) / slot;
     int warps = 1;
     while (warps < most && warps < fit && static_cast<int64_t>(warps) * kRecurEvery < p.T) ++warps;
     const int64_t blocks = static_cast<int64_t>(p.B) * ((p.D + kRecurChannels - 1) / kRecurChannels);
@@ -384,8 +386,9 @@ int recur_shape(RecurParams<E> &p, int most, int slot) {
 template <typename E>
 cudaError_t recur_launch(void (*kernel)(RecurParams<E>), const RecurParams<E> &p, int warps, int bytes,
                          cudaStream_t s) {
+    // one bound for all calls: a call of another size on another thread must not lower it
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockShared);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((p.D + kRecurChannels - 1) / kRecurChannels) * p.ranks, p.B);

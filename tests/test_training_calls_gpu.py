@@ -268,6 +268,33 @@ def test_two_threads():
     assert not failed, failed
 
 
+def test_two_threads_on_one_kernel():
+    """Calls of other sizes on the same kernels, whose blocks take other amounts of shared memory."""
+    work = [calls(BF16, 72, T, seed=913) for T in (20, 700)] + [calls(BF16, D, 40, seed=914) for D in (33, 257)]
+    want = [[c() for c in w] for w in work]
+    torch.cuda.synchronize()
+    failed = []
+
+    def go(k):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(40):
+                with torch.cuda.stream(s):
+                    got = [c() for c in work[k]]
+                s.synchronize()
+                for a, b in zip(got, want[k]):
+                    same(a, b)
+        except Exception as e:       # noqa: BLE001 (reported below)
+            failed.append(e)
+
+    threads = [threading.Thread(target=go, args=(k,)) for k in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+
+
 def test_workspaces_are_checked():
     x = torch.randn(2, 40, 64, device="cuda")
     w, st, stats = torch.ones(64, 4, device="cuda"), torch.zeros(2, 3, 64, device="cuda"), torch.ones(2, 40, 2, device="cuda")
