@@ -9,7 +9,7 @@
 // places, and where there are two the schedulers issue in 70% of the cycles. T32768 D2048, one
 // sequence in clusters of 8: 145 us, 3.70 TB/s; 100 without the exchange, whose barrier of the
 // cluster takes 1.4 us for every 1024 tokens. fp32 B4 T2048 D4096 93 us, 5.8 TB/s. Rows that are not
-// whole pieces (D4097): 140 us in bf16, 177 in fp32. Tiles of 8 tokens to a warp with three times
+// whole pieces (D4097): 123 us in bf16, 163 in fp32. Tiles of 8 tokens to a warp with three times
 // the warps took 66 to 76 us for 64, one with a ring of one tile 64.
 #include <utility>
 
@@ -46,8 +46,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_kernel(const Recu
     constexpr int kStages = kRecurStages<E>;
     __shared__ Exchange<kMaxWarps> ex;
     extern __shared__ uint4 ring[];
-    const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.D % 2 == 0 : true;
-    const int scaling = scaling_of<FORM>(p);
+    constexpr bool gated = Form<FORM>::gated, rated = Form<FORM>::rated, whole = Form<FORM>::whole;
+    constexpr int scaling = Form<FORM>::scaling;
+    const bool pairs = whole || p.D % 2 == 0;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int ranks = p.ranks, rank = blockIdx.x % ranks, c0 = blockIdx.x / ranks * kRecurChannels;
     const int c = c0 + 2 * lane, D = p.D;
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_kernel(const Recu
     const int n = valid_tokens(p.lengths, b, p.T);
     const int tile = warps * kRecurEvery * ranks;          // of the cluster
     const int tiles = (n + tile - 1) / tile, first = (rank * warps + warp) * kRecurEvery;
-    using Tile = Rows<E, (FORM >= 0)>;
+    using Tile = Rows<E, whole>;
     const int slot = (gated ? 3 : 2) * Tile::bytes;
     unsigned char *mine = reinterpret_cast<unsigned char *>(ring) + warp * kStages * slot;
     struct Inputs {
@@ -207,7 +208,7 @@ cudaError_t launch(RecurParams<E> &p, cudaStream_t s, std::integer_sequence<int,
         return p.rate ? launch_step<E, false, true>(p, s) : launch_step<E, false, false>(p, s);
     }
     using Kernel = void (*)(RecurParams<E>);
-    static constexpr Kernel table[] = {gdn_recur_kernel<E, kAnyForm>, gdn_recur_kernel<E, FORMS>...};
+    static constexpr Kernel table[] = {gdn_recur_kernel<E, FORMS>...};
     recur_rows(p);
     const int slot = kRecurStages<E> * (p.gate ? 3 : 2) * recur_row_bytes(p);
     const int warps = recur_shape<E, Exchange<kMaxWarps>>(p, kMaxWarps, slot);

@@ -11,7 +11,7 @@
 // factors are computed twice, since lam needs those of later tokens and registers hold one array.
 //
 // B4 T2048 D4096 bf16: 121 us, 3.96 TB/s (59% of a plain copy's 6.68); T32768 D2048 244 us, 3.93 TB/s;
-// fp32 B4 T2048 D4096 159 us, 5.9 TB/s. Ten to twelve warps of 166 registers to an SM issue in 56% of
+// fp32 B4 T2048 D4096 161 us, 5.8 TB/s; D4097 243 us in bf16, 295 in fp32. Ten to twelve warps of 166 registers to an SM issue in 56% of
 // the cycles. 128 registers and 16 warps with a ring of one tile: 126 us for 132 then, but 281 for
 // 263 on T32768.
 #include <utility>
@@ -28,8 +28,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const 
     constexpr int kStages = kRecurStages<E>;
     __shared__ Exchange<kMaxWarps> ex;
     extern __shared__ uint4 ring[];
-    const bool gated = is_gated<FORM>(p), rated = is_rated<FORM>(p), pairs = FORM < 0 ? p.D % 2 == 0 : true;
-    const int scaling = scaling_of<FORM>(p);
+    constexpr bool gated = Form<FORM>::gated, rated = Form<FORM>::rated, whole = Form<FORM>::whole;
+    constexpr int scaling = Form<FORM>::scaling;
+    const bool pairs = whole || p.D % 2 == 0;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     const int ranks = p.ranks, rank = blockIdx.x % ranks, c0 = blockIdx.x / ranks * kRecurChannels;
     const int c = c0 + 2 * lane, D = p.D;
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const 
     const int n = valid_tokens(p.lengths, b, p.T);
     const int tile = warps * kRecurEvery * ranks;          // of the cluster
     const int tiles = (n + tile - 1) / tile, first = (rank * warps + warp) * kRecurEvery;
-    using Tile = Rows<E, (FORM >= 0)>;
+    using Tile = Rows<E, whole>;
     const int slot = (gated ? 4 : 3) * Tile::bytes;
     unsigned char *mine = reinterpret_cast<unsigned char *>(ring) + warp * kStages * slot;
     struct Inputs {
@@ -154,7 +155,7 @@ size_t bwd_workspace(const gdn_recur_problem *p) {
 template <typename E, int... FORMS>
 cudaError_t launch(RecurParams<E> &p, float *d_rate, cudaStream_t s, std::integer_sequence<int, FORMS...>) {
     using Kernel = void (*)(RecurParams<E>);
-    static constexpr Kernel table[] = {gdn_recur_bwd_kernel<E, kAnyForm>, gdn_recur_bwd_kernel<E, FORMS>...};
+    static constexpr Kernel table[] = {gdn_recur_bwd_kernel<E, FORMS>...};
     recur_rows(p);
     const int slot = kRecurStages<E> * (p.gate ? 4 : 3) * recur_row_bytes(p);
     const int warps = recur_shape<E, Exchange<kMaxWarps>>(p, kMaxWarps, slot);
