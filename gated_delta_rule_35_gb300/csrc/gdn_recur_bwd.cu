@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const 
                 inner = fma2(qx, both(-1.f), h);
             const F2 dlog = mul2(mul2(lam[j], a), inner);
             h = fma2(a, h, mul2(m, qx));
-            if (rated) d_rate = fma2(dlog, s, d_rate);
             const bool there = j < left;
+            // s is not quite 0 behind the sequence, and what h ends with need not be finite
+            if (rated && there) d_rate = fma2(dlog, s, d_rate);
             store_pair(p.dx + out, dx, there, second, pairs);
             if (gated) store_pair(p.d_gate + out, d_gate, there, second, pairs);
             store_pair(p.d_decay + out, mul2(dlog, rated ? mul2(minus_rate, mul2(s, s_n)) : a_n), there, second,

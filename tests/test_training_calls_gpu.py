@@ -413,6 +413,29 @@ def test_nan_stays_where_it_belongs(dtype, D):
     but(other, cdb, clean[5][2])
 
 
+# What a sequence ends with need not be finite for its gradients to be: its last input, whose factor
+# is 1, reaches none of them but its gate's.
+@pytest.mark.parametrize("D", [72, 65])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_last_input_that_is_not_finite(value, dtype, D):
+    B, T = 3, 150
+    i = recur_inputs(B, T, D, dtype, 965, scaling="none")
+    i["lengths"] = torch.tensor([150, 20, 97], dtype=torch.int32, device="cuda")
+    dy = draw(gen(966), (B, T, D), dtype)
+
+    def gradients():
+        _, _, states = gdn.recur_fwd(**i, output_states=True)
+        return gdn.recur_bwd(dy, states=states, **{n: v for n, v in i.items() if n != "h0"})
+
+    clean = gradients()
+    for b, n in enumerate(i["lengths"].tolist()):
+        i["x"][b, n - 1] = value
+    dx, d_decay, _, d_rate, d_state = gradients()
+    for got, want in zip((dx, d_decay, d_rate, d_state), (clean[0], clean[1], clean[3], clean[4])):
+        assert torch.isfinite(want).all() and torch.equal(got, want)
+
+
 def test_beyond_32_bits():
     """Tensors of more than 2^31 values: the last sequence as if it were alone."""
     B, T, D = 5, 65536, 8192
