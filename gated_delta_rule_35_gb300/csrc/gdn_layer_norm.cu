@@ -16,7 +16,7 @@
 // (95%), 6 us of them the sums over the blocks' rows. A block to a row with every value read three
 // times took 434 and 2189 us; a part of a warp to a row, weight and bias read for each, 246. fp32
 // 32768 x 4096: 177 and 251 us; 65536 x 2560 bf16 130 and 191 (154 and 227 with a power of two of
-// threads to a row); rows of 1003: bf16 60 and 83, fp32 66 and 104 (element by element with 4 elements
+// threads to a row); rows of 1003: bf16 60 and 85, fp32 64 and 101 (element by element with 4 elements
 // to a thread: 284 and 142 the norm).
 #include "columns.cuh"
 #include "rows.cuh"
@@ -179,8 +179,11 @@ struct RowRing {
     static constexpr int row_bytes =
         TENSORS * (SHARED ? THREADS * P * 2 + THREADS / kMinLanes * 16 : THREADS * P * static_cast<int>(sizeof(Slot)));
     static constexpr int most = (THREADS > 256 ? 200 : 96) * 1024;
-    // what the registers of single channels hold, and bytes enough in flight, count too
-    static constexpr int wanted = V == 1 && P > 8 ? 1 : TENSORS == 1 && (sizeof(E) == 2 || THREADS == 256) ? 4 : 2;
+    // what the registers of single channels hold, and bytes enough in flight, count too: rows of 4097 with
+    // one, two and four to a turn 398, 328 and 483 us in bf16, 368 and 316 in fp32 (32768 of them)
+    static constexpr int wanted = V == 1 && P > 8                                     ? 3 - TENSORS
+                                  : TENSORS == 1 && (sizeof(E) == 2 || THREADS == 256) ? 4
+                                                                                       : 2;
     static constexpr int R = wanted >= 4 && 8 * row_bytes <= most ? 4 : wanted >= 2 && 4 * row_bytes <= most ? 2 : 1;
     static constexpr int stages = THREADS > 256 && 3 * R * row_bytes <= most ? 3 : 2 * R * row_bytes <= most ? 2 : 1;
     static constexpr int ring = stages * R * row_bytes, sums = THREADS * V * 4;
@@ -210,6 +213,12 @@ struct RowRing {
     }
     // Asks for the rows of turn i; those that there are (-1: none).
     __device__ __forceinline__ void fetch(int i, int stage, int (&rows)[R]) const {
+        if (i >= turns) {          // 1 x 2048 took 8.9 us for 6.8 with such turns' slots cleared
+#pragma unroll
+            for (int r = 0; r < R; ++r) rows[r] = -1;
+            copy_commit();
+            return;
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t at = first + (static_cast<int64_t>(i) * R + r) * step;
