@@ -104,7 +104,7 @@ __device__ __forceinline__ F2 through_act(F2 dy, F2 v, int act) {
     // the product in range
     float a, b;
     unpack2(mul2(v, both(-kLog2e)), a, b);
-    const F2 e = pack2(exp2_ftz(fminf(a, 126.f)), exp2_ftz(fminf(b, 126.f)));
+    const F2 e = pack2(exp2_ftz(min_nan(a, 126.f)), exp2_ftz(min_nan(b, 126.f)));
     unpack2(add2(e, both(1.f)), a, b);
     const F2 s = pack2(rcp_ftz(a), rcp_ftz(b));
     return mul2(mul2(dy, s), mul2(e, s));

@@ -58,6 +58,18 @@ __device__ __forceinline__ float rcp_ftz(float v) {
     return r;
 }
 
+// The larger and the smaller of two values, NaN where one of them is (fmaxf and fminf give the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // 1 / (1 + exp(-v)). Far below 0 the exponential is inf and the quotient 0: what is lost

@@ -1,0 +1,93 @@
+"""Gradients at the edges of their ranges on the GPU against their fp64 forms: values that are not
+finite."""
+import pytest
+import torch
+
+import gated_delta_rule_35_gb300 as gdn
+from oracle import training as ref
+from tests.mixer_bounds import check
+from tests.test_mixer_gpu import draw, f64, gen
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+# ------------------------------------------------------------------- NaN goes on
+def is_nan_in(t, at):
+    """NaN exactly where `at` says so."""
+    return torch.equal(torch.isnan(t), at)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu", "none"])
+@pytest.mark.parametrize("C", [72, 65])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_conv_bwd_gives_nan_on(dtype, C, act):
+    """A value before the activation that is NaN makes NaN of the gradients it enters, as the forward
+    pass does of its output; without an activation no gradient but the weights' reads the input."""
+    B, T, W, b, t, c = 2, 40, 4, 1, 17, 5
+    g = gen(1000)
+    x, dy, state = draw(g, (B, T, C), dtype), draw(g, (B, T, C), dtype), draw(g, (B, W - 1, C), dtype)
+    weight, bias = torch.randn(C, W, generator=g).cuda(), torch.randn(C, generator=g).cuda()
+    clean = gdn.conv_bwd(dy, x, weight, bias, state, act)
+    through = act != "none"
+
+    def gradients(**changed):
+        got = gdn.conv_bwd(dy, **{**dict(x=x, weight=weight, bias=bias, state=state, act=act), **changed})
+        y = gdn.conv_fwd(changed.get("x", x), changed.get("weight", weight), changed.get("bias", bias), state,
+                         act=act)[0]
+        return got, torch.isnan(y)
+
+    def only(got, *at):
+        for v, want, where in zip(got, clean, at):
+            assert is_nan_in(v, where)
+            assert torch.equal(v[~where], want[~where])
+
+    nowhere = [torch.zeros_like(v, dtype=torch.bool) for v in clean]
+    # an input: the values before the activation of W tokens, the gradients of W - 1 more before them
+    bad = x.clone()
+    bad[b, t, c] = float("nan")
+    got, y = gradients(x=bad)
+    dx, dw, db, ds = (v.clone() for v in nowhere)
+    assert y.any() and y[b, t:t + W, c].all()
+    dx[b, t - W + 1:t + W, c] = through
+    dw[c] = True
+    db[c] = through
+    only(got, dx, dw, db, ds)
+    # a weight: every value of its channel
+    bad = weight.clone()
+    bad[c, 2] = float("nan")
+    got, y = gradients(weight=bad)
+    assert y[..., c].all()
+    if through:
+        dx, dw, db, ds = (v.clone() for v in nowhere)
+        dx[..., c] = dw[c] = db[c] = ds[..., c] = True
+        only(got, dx, dw, db, ds)
+    # a bias
+    bad = bias.clone()
+    bad[c] = float("nan")
+    got, y = gradients(bias=bad)
+    dx, dw, db, ds = (v.clone() for v in nowhere)
+    assert y[..., c].all()
+    dx[..., c] = dw[c] = db[c] = ds[..., c] = through
+    only(got, dx, dw, db, ds)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_conv_bwd_of_far_values(dtype):
+    """The sigmoid's slope where exp(-v) leaves fp32's range on either side, infinite values among
+    them: 0 but for what lies below the normal range."""
+    B, T, C, W = 1, 24, 16, 2
+    x = torch.zeros(B, T, C, device="cuda", dtype=dtype)
+    far = torch.tensor([60.0, -60.0, 87.0, -87.0, 88.0, -88.0, 126.0, -126.0, 200.0, -200.0, 1e30, -1e30, 3e38,
+                        -3e38, float("inf"), -float("inf")], device="cuda")
+    dy = draw(gen(1010), (B, T, C), dtype)
+    dx, dw, db = gdn.conv_bwd(dy, x, torch.ones(C, W, device="cuda"), far, act="sigmoid")[:3]
+    p = dy.double() * torch.exp(-far.abs().double())           # s (1 - s), whose larger factor is 1 but for 2^-86
+    # a sigmoid and its complement are off by 19 + 6 |v| roundings, products and 24 additions by fewer
+    # than 40; exp(-88) is below the normal range, where each factor is off by tiny
+    bound = (19 + 6 * 88 + 40) * ref.U * p.abs() + 2 * ref.TINY * dy.double().abs()
+    two = lambda v: torch.cat([v[:, :-1] + v[:, 1:], v[:, -1:]], 1)
+    check(dx, f64(two(p)), f64(two(bound)), dtype)
+    check(db, f64(p.sum((0, 1))), f64(bound.sum((0, 1))), F32)
+    assert (dw == 0).all()
