@@ -68,6 +68,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const 
     for (int i = 0; i < kStages; ++i) fill(i);
     const F2 rate = rated ? load_pair(p.rate, c, D, pairs) : both(0.f), t_scale = mul2(rate, both(-kLog2e));
     const F2 minus_rate = mul2(rate, both(-1.f));
+    float rate0, rate1;
+    unpack2(rate, rate0, rate1);
+    const F2 floors = rated ? pack2(root_floor(rate0), root_floor(rate1)) : both(root_floor(1.f));
     F2 d_rate = both(0.f);
     const int64_t chunks = (static_cast<int64_t>(p.T) + kRecurEvery - 1) / kRecurEvery;
     Scan<true, kMaxWarps> scan(ex, ranks, rank,
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) gdn_recur_bwd_kernel(const 
                 a = s;
                 a_n = s_n;
             }
-            const F2 m = input_factor2(a, a_n, scaling, inverse), x = in.x.pair(j, lane);
+            const F2 m = input_factor2(a, a_n, scaling, floors, inverse), x = in.x.pair(j, lane);
             F2 qx = x, dx = mul2(m, lam[j]), d_gate;
             if (gated) {
                 F2 q, q_n;

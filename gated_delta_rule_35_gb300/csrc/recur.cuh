@@ -110,17 +110,23 @@ constexpr int recur_form(bool gated, bool rated, int scaling, bool whole) {
 }
 
 // The input's factor m of a and n = 1 - a, and its reciprocal where it is a root; where 1 - a^2 is
-// below the normal range m is below 2^-63 and the reciprocal 2^63.
-__device__ __forceinline__ F2 input_factor2(F2 a, F2 n, int scaling, F2 &inverse) {
+// below the normal range m is below 2^-63 and the reciprocal 2^63. `floors` are root_floor's of the channels.
+__device__ __forceinline__ F2 input_factor2(F2 a, F2 n, int scaling, F2 floors, F2 &inverse) {
     if (scaling == GDN_RECUR_ROOT) {
-        constexpr float tiny = 1.17549435e-38f;
         const F2 v = fma2(n, a, n);                    // 1 - a^2
-        float v0, v1;
+        float v0, v1, f0, f1;
         unpack2(v, v0, v1);
-        inverse = pack2(rsqrt_ftz(fmaxf(v0, tiny)), rsqrt_ftz(fmaxf(v1, tiny)));
+        unpack2(floors, f0, f1);
+        inverse = pack2(rsqrt_ftz(fmaxf(v0, f0)), rsqrt_ftz(fmaxf(v1, f1)));
         return mul2(v, inverse);
     }
     return scaling == GDN_RECUR_COMPLEMENT ? n : both(1.f);
+}
+// The smallest 1 - a^2 whose root a reciprocal is taken of: the normal range's end. In a channel whose rate is
+// 0, or below that range, m is 0 for every token and has no gradient: infinity, so that the reciprocal is 0.
+__device__ __forceinline__ float root_floor(float rate) {
+    constexpr float tiny = 1.17549435e-38f;
+    return rate < tiny ? INFINITY : tiny;
 }
 
 // Two channels of a row in shared memory.

@@ -1,5 +1,5 @@
 """Gradients at the edges of their ranges on the GPU against their fp64 forms: values that are not
-finite."""
+finite, rates of 0."""
 import pytest
 import torch
 
@@ -7,10 +7,12 @@ import gated_delta_rule_35_gb300 as gdn
 from oracle import training as ref
 from tests.mixer_bounds import check
 from tests.test_mixer_gpu import draw, f64, gen
+from tests.test_training_gpu import checked, recur_bwd_ref, recur_inputs, recur_ref
 
 pytestmark = pytest.mark.gpu
 
 F32, BF16 = torch.float32, torch.bfloat16
+GRADIENTS = ("dx", "d_decay", "d_gate", "d_rate", "d_state")
 
 
 # ------------------------------------------------------------------- NaN goes on
@@ -91,3 +93,53 @@ def test_conv_bwd_of_far_values(dtype):
     check(dx, f64(two(p)), f64(two(bound)), dtype)
     check(db, f64(p.sum((0, 1))), f64(bound.sum((0, 1))), F32)
     assert (dw == 0).all()
+
+
+# ---------------------------------------------------------------------- rates of 0
+@pytest.mark.parametrize("scaling", ["root", "complement", "none"])
+@pytest.mark.parametrize("size", [(2, 5, 72), (2, 50, 72), (3, 150, 65), (1, 2100, 16)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_recur_channels_of_rate_zero(dtype, size, scaling):
+    """A channel whose rate is 0 keeps its state whole; the root's factor m is 0 there and its
+    gradient counts as 0, in the rate's gradient too."""
+    B, T, D = size
+    for gate in (True, False):
+        i = recur_inputs(*size, dtype, 1100, gate=gate, scaling=scaling, lengths=B > 1)
+        i["rate"][::3] = 0.0
+        i["rate"][1::6] = -0.0
+        y, h, states = gdn.recur_fwd(**i, output_states=True)
+        want, bound, _ = recur_ref(i)
+        checked(dict(y=y, h=h, states=states), want, bound, dict(y=dtype))
+        dy, dh = draw(gen(1101), size, dtype), torch.randn(B, D, generator=gen(1102)).cuda()
+        h0 = i.pop("h0")
+        got = gdn.recur_bwd(dy, states=states, d_final_state=dh, **i)
+        i["h0"] = h0
+        want, bound = recur_bwd_ref(dy, i, dh)
+        if scaling == "root":
+            # m's gradient is 0, so the rate's is -sum lam s a h: no larger than its terms
+            size_of = abs(want["d_rate"][::3]).max()
+            assert size_of < 1e6 and abs(got[3][::3]).max() < 2 * size_of
+        checked(dict(zip(GRADIENTS, got)), want, bound, dict(dx=dtype, d_decay=dtype, d_gate=dtype))
+
+
+def test_recur_rates_below_the_normal_range():
+    """They count as 0 for m, as 1 - a^2 does in the forward pass: the state passes whole, x adds
+    nothing to it, and the rate's gradient is that of the decay alone."""
+    B, T, D = 2, 50, 40
+    i = recur_inputs(B, T, D, F32, 1110)
+    i["rate"].copy_(torch.tensor([1e-38, 1e-39, 1e-40, 1e-44, 0.0])[torch.arange(D) % 5])
+    y, h, states = gdn.recur_fwd(**i, output_states=True)
+    assert torch.equal(h, i["h0"]) and torch.equal(y, h[:, None].expand_as(y))
+    dy = draw(gen(1111), (B, T, D), F32)
+    h0 = i.pop("h0")
+    dx, dd, dg, dr, d0 = gdn.recur_bwd(dy, states=states, **i)
+    lam = dy.double().flip(1).cumsum(1).flip(1)
+    s = torch.sigmoid(i["decay"].double())
+    terms = -lam * s * h0.double()[:, None]
+    # lam is off by 60 roundings of its terms, the sigmoid by 7 + 2 |v|, |v| < 6; 100 additions, 2 products
+    size = 60 * ref.U * dy.double().abs().sum(1, keepdim=True) * s * h0.double().abs()[:, None] \
+        + (7 + 12 + 102) * ref.U * terms.abs()
+    check(dr, f64(terms.sum((0, 1))), f64(size.sum((0, 1))), F32)
+    # m is below 2^-62, and its gradient times any of the rates too
+    small = 2.0 ** -55
+    assert abs(dx).max() < small and abs(dd).max() < small and abs(dg).max() < small
