@@ -60,6 +60,12 @@ def _optional(t, name, shape, dtype, index):
     return (0, 0) if t is None else _tokens(t, name, shape, dtype, index)
 
 
+def _given(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} must be given")
+
+
 def _zeros(shape, dtype, x, lengths=None):
     return (torch.empty if lengths is None else torch.zeros)(shape, dtype=dtype, device=x.device)
 
@@ -71,6 +77,7 @@ def _recur_refusal(p):
 
 def _recur_problem(x, decay, rate, gate, scaling, lengths, dy=None):
     """(problem, device index) of the inputs that both passes take."""
+    _given(decay=decay)
     shape, dtype, index = _x(x, "[B,T,D]")
     B, T, D = shape
     p = RecurProblem(*_int32("gdn_recur_fwd", B, T, D), DTYPES[dtype], _scaling(scaling), 0,
@@ -113,9 +120,8 @@ def recur_fwd(x, decay, rate=None, gate=None, scaling: str = "root", h0=None, le
     state in place; ``out`` and ``states`` may be passed to reuse buffers."""
     if not output_states:
         states = None
-    key = ("recur", x.shape, x.stride(), x.dtype, x.get_device(), decay.shape, decay.stride(), decay.dtype,
-           decay.get_device(), _form(rate), _form(gate), scaling, _form(h0), _form(lengths), _form(out),
-           _form(final_state), _form(states))
+    key = ("recur", x.shape, x.stride(), x.dtype, x.get_device(), _form(decay), _form(rate), _form(gate), scaling,
+           _form(h0), _form(lengths), _form(out), _form(final_state), _form(states))
     p, state, kept, index = _plans.get(key) or _keep(key, _recur_plan(
         x, decay, rate, gate, scaling, h0, lengths, out, final_state, states))
     if out is None:
@@ -147,6 +153,7 @@ def recur_bwd_workspace_bytes(B: int, T: int, D: int, dtype=torch.bfloat16) -> i
 
 def _recur_bwd_plan(dy, x, decay, states, rate, gate, scaling, d_final_state, lengths, dx, d_decay, d_gate,
                     d_rate, d_state):
+    _given(dy=dy, states=states)
     p, index = _recur_problem(x, decay, rate, gate, scaling, lengths, dy)
     state, f32 = (x.shape[0], x.shape[2]), torch.float32
     for t, name, form, kind in ((states, "states", _recur_states(x), f32),
@@ -257,6 +264,7 @@ def layer_norm_bwd_workspace_bytes(B: int, T: int, C: int, dtype=torch.bfloat16)
 
 
 def _layer_norm_bwd_plan(dy, x, stats, weight, center, lengths, dx, d_weight, d_bias):
+    _given(dy=dy, stats=stats)
     p, index = _layer_norm_problem(x, weight, 0.0, center, lengths, dy)
     for t, name, form, kind in ((stats, "stats", (*x.shape[:2], 2), torch.float32), (dx, "dx", x.shape, x.dtype),
                                 (d_weight, "d_weight", (x.shape[2],), torch.float32),
@@ -311,6 +319,7 @@ def conv_bwd_workspace_bytes(B: int, T: int, C: int, W: int, dtype=torch.bfloat1
 
 
 def _conv_bwd_plan(dy, x, weight, bias, state, act, d_final_state, lengths, dx, d_weight, d_bias, d_state):
+    _given(dy=dy, weight=weight)
     shape, dtype, index = _x(x)
     B, T, C = shape
     if weight.dim() != 2:
