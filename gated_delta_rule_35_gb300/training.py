@@ -9,7 +9,8 @@ those of include/gdn.h. Inputs marked *strided* may be slices of wider tensors. 
 ([B] int32, on the device) holds the valid tokens of each sequence of a padded batch: rows
 at or past it are not used, add nothing to a gradient, and are not written in the outputs
 (zeros, then, in an output that the call allocates). A backward pass returns gradients; it
-adds to nothing.
+adds to nothing. A buffer for a gradient that the call does not have (of a weight, bias, gate,
+rate or state that is not given) is refused; one whose output_* flag is off is left alone.
 """
 from __future__ import annotations
 
@@ -288,10 +289,8 @@ def layer_norm_bwd(dy, x, stats, weight=None, bias: bool = False, center: bool =
 @_on_stream
 def _layer_norm_bwd(x, dy, stats, weight, bias, center, lengths, workspace, dx, d_weight, d_bias):
     center, C = bool(center), x.shape[-1]
-    if weight is None:
-        d_weight = None
-    if not bias:
-        d_bias = None
+    if d_weight is not None and weight is None or d_bias is not None and not bias:
+        raise ValueError("d_weight and d_bias go with a weight and with bias=True")
     key = ("layer_norm_bwd", x.shape, x.stride(), x.dtype, x.get_device(), _form(dy), _form(stats), _form(weight),
            center, _form(lengths), _form(dx), _form(d_weight), _form(d_bias))
     p, need, index = _plans.get(key) or _keep(key, _layer_norm_bwd_plan(
@@ -354,10 +353,8 @@ def conv_bwd(dy, x, weight, bias=None, state=None, act: str = "silu", d_final_st
 
 @_on_stream
 def _conv_bwd(x, dy, weight, bias, state, act, d_final_state, lengths, workspace, dx, d_weight, d_bias, d_state):
-    if bias is None:
-        d_bias = None
-    if state is None:
-        d_state = None
+    if d_bias is not None and bias is None or d_state is not None and state is None:
+        raise ValueError("d_bias and d_state go with a bias and a state")
     key = ("conv_bwd", x.shape, x.stride(), x.dtype, x.get_device(), _form(dy), _form(weight), _form(bias),
            _form(state), act, _form(d_final_state), _form(lengths), _form(dx), _form(d_weight), _form(d_bias),
            _form(d_state))
