@@ -15,6 +15,8 @@
 // halves of a warp.
 #pragma once
 
+#include <cstddef>
+
 #include "columns.cuh"
 #include "rows.cuh"
 
@@ -225,8 +227,8 @@ struct Rows {
     }
 };
 
-// (A, H) of two channels.
-struct Through {
+// (A, H) of two channels, which a store to another block takes in one piece of 16 bytes.
+struct alignas(16) Through {
     F2 a, h;
 };
 
@@ -244,6 +246,8 @@ struct Exchange {
     Through warps[2][WARPS][32], ranks[2][kMaxRanks][32];
     F2 state[2][32];
 };
+static_assert(sizeof(Through) == 16 && alignof(Exchange<1>) % 16 == 0 && offsetof(Exchange<1>, ranks) % 16 == 0,
+              "16-byte stores to another block");
 
 template <bool REVERSE, int WARPS>
 struct Scan {
