@@ -1,5 +1,5 @@
 """Gradients at the edges of their ranges on the GPU against their fp64 forms: values that are not
-finite, rates of 0."""
+finite, rates of 0, every form of the recurrence's gates."""
 import pytest
 import torch
 
@@ -143,3 +143,26 @@ def test_recur_rates_below_the_normal_range():
     # m is below 2^-62, and its gradient times any of the rates too
     small = 2.0 ** -55
     assert abs(dx).max() < small and abs(dd).max() < small and abs(dg).max() < small
+
+
+# ----------------------------------------------------------------- every form of gates
+@pytest.mark.parametrize("scaling", ["none", "complement", "root"])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("rate", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_recur_every_form(dtype, rate, gate, scaling):
+    """Each form has kernels of its own: for rows of whole pieces (72), for others with an even and an odd
+    number of channels, and for a few tokens."""
+    for k, size in enumerate(((2, 40, 72), (2, 40, 65), (3, 37, 66), (2, 5, 72), (2, 7, 65))):
+        i = recur_inputs(*size, dtype, 1200 + k, rate, gate, scaling, lengths=k % 2 == 1)
+        y, h, states = gdn.recur_fwd(**i, output_states=True)
+        want, bound, _ = recur_ref(i)
+        checked(dict(y=y, h=h, states=states), want, bound, dict(y=dtype))
+        dy = draw(gen(1210 + k), size, dtype)
+        dh = torch.randn(size[0], size[2], generator=gen(1220 + k)).cuda()
+        h0 = i.pop("h0")
+        got = gdn.recur_bwd(dy, states=states, d_final_state=dh, **i)
+        i["h0"] = h0
+        want, bound = recur_bwd_ref(dy, i, dh)
+        checked(dict(zip(GRADIENTS, got)), {n: want[n] for n in GRADIENTS}, bound,
+                dict(dx=dtype, d_decay=dtype, d_gate=dtype))
