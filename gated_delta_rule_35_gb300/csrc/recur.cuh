@@ -369,21 +369,37 @@ constexpr int kRecurStages = sizeof(E) == 2 ? 2 : 1;
 
 constexpr int kBlockShared = 228 * 1024 / 2 - 1024;    // of one of two blocks to an SM
 
+// Whether a kernel may have that many blocks. They fill the GPU's places for two blocks to an SM once; those
+// of a padded batch, whose shorter sequences leave their places early, may go beyond: by a tenth where
+// clusters double, by a third in the gradients in bf16, which wait for arithmetic more than for memory. Time with
+// more blocks over time without (events around the call, L2 flushed, medians of three runs), lengths spread evenly
+// to a mean of 50, 80 and 90% of the longest and all alike:
+//                                            forward               backward
+//   a tenth, B5 T777 D1024 fp32        0.81 0.97 1.03 0.95   0.82 0.99 0.95 1.15
+//   a tenth, B2 T3000 D2560 fp32       0.75 0.94 0.99 1.02   0.76 1.08 1.14 1.07
+//   a tenth, B4 T4000 D1280 bf16       0.76 0.90 0.94 0.95   0.81 1.00 0.96 1.00
+//   a third, B6 T2048 D2048 bf16       0.91 1.14 1.18 1.07   0.77 0.96 1.02 0.97
+//   a third, B6 T2048 D2048 fp32       0.92 1.15 1.21 1.20   0.77 1.03 1.20 1.16
+// and where single blocks became clusters, a tenth beyond the places:
+//   B2 T4096 D5120 fp32                0.97 1.14 1.16 1.14   0.98 1.22 1.27 1.15
+template <typename E>
+bool recur_fits(const RecurParams<E> &p, int64_t blocks) {
+    const int places = 2 * 152;
+    if (!p.lengths) return blocks <= places;
+    if (sizeof(E) == 2 && p.dx) return blocks <= places * 4 / 3;
+    return blocks <= (p.ranks > 1 ? places * 11 / 10 : places);
+}
+
 // Warps to a block: as many as a sequence's tokens fill, up to `most` and to what lets two blocks,
-// with `slot` bytes to a warp's ring, share an SM. Blocks to a cluster: as many as leave the GPU's
-// places for two blocks to an SM filled once, and have tokens; a third more in a padded batch, whose
-// shorter sequences leave their places early. With half of the tokens valid 1.2 to 1.6 times as fast where
-// that doubles the clusters (gradients of B3 T4096 D4096 bf16 154 -> 106 us, fp32 191 -> 137; B5 T777
-// D1000 fp32 35 -> 29); with all of them valid it takes 236 -> 219, 258 -> 302 and 43 -> 48.
+// with `slot` bytes to a warp's ring, share an SM. Blocks to a cluster: as many as fit and have tokens.
 template <typename E, typename X>
 int recur_shape(RecurParams<E> &p, int most, int slot) {
     const int fit = (kBlockShared - static_cast<int>(sizeof(X))) / slot;
     int warps = 1;
     while (warps < most && warps < fit && static_cast<int64_t>(warps) * kRecurEvery < p.T) ++warps;
     const int64_t blocks = static_cast<int64_t>(p.B) * ((p.D + kRecurChannels - 1) / kRecurChannels);
-    const int places = p.lengths ? 2 * 152 * 4 / 3 : 2 * 152;
     p.ranks = 1;
-    while (p.ranks < kMaxRanks && blocks * p.ranks * 2 <= places &&
+    while (p.ranks < kMaxRanks && recur_fits(p, blocks * p.ranks * 2) &&
            p.T > static_cast<int64_t>(p.ranks) * warps * kRecurEvery)
         p.ranks *= 2;
     return warps;
