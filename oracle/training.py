@@ -18,8 +18,12 @@ The bounds, u = 2^-24 fp32's rounding and tiny = 2^-126 the end of its normal ra
   place of the state, so that the bound holds for any order in which the terms are
   added up: a token adds the error of its factor twice (in the state and in a product of
   factors) and 4u M.
-* A sum over tokens or channels takes at most SUMS additions in a row."""
+* A sum over tokens or channels takes at most SUMS additions in a row. `additions` counts those of a sum
+  over tokens; the forms are compared at sizes where it gives no more, and a larger one is
+  bounded with its own count."""
 from __future__ import annotations
+
+import math
 
 import numpy as np
 
@@ -32,6 +36,16 @@ FAR = 150.0
 # What a sigmoid off by tiny makes of sqrt(1 - a^2) <= sqrt(2 rate s), of rate s / sqrt(2 rate s) and of
 # s / sqrt(2 rate s), for rates of 0.002 to 300.
 SMALL = 2.0 ** -58
+
+
+def additions(terms, parts):
+    """Additions in a row of a sum over tokens of which a thread adds `terms` in turn, and which leaves
+    `parts` partial results: these go eight and more to a thread, 32 threads at most to a sum, and on in a
+    tree. `terms` is, for the rate's gradient, a lane's share of a sequence (its tokens over the warps of its
+    cluster, up to a tile, and the warps); for the norm's, a block's share of the rows (of 304 blocks, of 152
+    where one fills an SM, of 64 where a row is more than a block holds) and the rows it holds at once; for the
+    convolution's, a run of 256 tokens at most and the runs of a block."""
+    return math.ceil(terms) + max(8, math.ceil(parts / 32)) + 5
 
 
 def sigmoids(v):

@@ -1,5 +1,5 @@
 """Gradients at the edges of their ranges on the GPU against their fp64 forms: values that are not
-finite, rates of 0, every form of the recurrence's gates."""
+finite, rates of 0, every form of the recurrence's gates, sums of very many terms."""
 import pytest
 import torch
 
@@ -166,3 +166,43 @@ def test_recur_every_form(dtype, rate, gate, scaling):
         want, bound = recur_bwd_ref(dy, i, dh)
         checked(dict(zip(GRADIENTS, got)), {n: want[n] for n in GRADIENTS}, bound,
                 dict(dx=dtype, d_decay=dtype, d_gate=dtype))
+
+
+# -------------------------------------------------------------- sums of very many terms
+def sum_is(got, terms, additions, each):
+    """`terms` (fp64) summed over batch and tokens in fp32, every one of them off by `each` roundings
+    and at most `additions` additions behind it."""
+    total, size = terms.sum((0, 1)), terms.abs().sum((0, 1))
+    check(got, f64(total), f64(size) * (additions + each) * ref.U, F32)
+
+
+def test_layer_norm_sums_behind_the_bounds_of_the_form():
+    """Rows that take a block: each of 304 adds up 900 of them, more than the fp64 form's bound counts."""
+    rows, C = 304 * 900, 1032
+    x = torch.randn(1, rows, C, device="cuda", generator=torch.Generator("cuda").manual_seed(1300))
+    dy = torch.randn(1, rows, C, device="cuda", generator=torch.Generator("cuda").manual_seed(1301))
+    w = torch.rand(C, generator=gen(1302)).cuda()
+    _, stats = gdn.layer_norm(x, w, output_stats=True)
+    _, dw, db = gdn.layer_norm_bwd(dy, x, stats, w, bias=True)
+    additions = ref.additions(rows / 304, 304)
+    assert additions > ref.SUMS
+    xhat = x.double().sub_(stats[..., :1]).mul_(stats[..., 1:])     # two roundings in fp32
+    sum_is(dw, xhat.mul_(dy), additions, 3)
+    del xhat
+    sum_is(db, dy.double(), additions, 0)
+
+
+def test_recur_sums_behind_the_bounds_of_the_form():
+    """Without clusters a lane adds up every sixth tile of 16 tokens. The terms of the rate's gradient by the
+    decay's, d_decay = -dlog rate s (1 - s): the same products but for rate and 1 - s."""
+    B, T, D = 2, 8192, 64 * 77
+    g = torch.Generator("cuda").manual_seed(1310)
+    x, decay, dy = (torch.randn(B, T, D, device="cuda", generator=g) for _ in range(3))
+    rate = (0.05 + torch.rand(D, generator=gen(1311))).cuda()
+    _, _, states = gdn.recur_fwd(x, decay, rate, scaling="none", output_states=True)
+    d_decay, d_rate = gdn.recur_bwd(dy, x, decay, states, rate, scaling="none")[1:4:2]
+    terms = d_decay.double().div_(rate).div_(torch.sigmoid(-decay.double()))
+    additions = ref.additions(T / 6 + 16 + 6, B)
+    assert additions > ref.SUMS
+    # 1 - s off by (12 + 4 |v|) roundings, |v| < 7; its product with s and both with the rate and dlog
+    sum_is(d_rate, terms, additions, 12 + 4 * 7 + 5)
