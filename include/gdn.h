@@ -480,11 +480,13 @@ GDN_API gdn_status gdn_group_norm(const gdn_group_norm_problem *p, const void *x
  *    whatever they hold, and the gradients' rows there are left as they were. Outputs
  *    may not overlap any input.
  *  - Gradients of what the tokens share (rate, weight, bias) are sums over all valid
- *    tokens, written, not added to: fp32, taken in an order that depends on the sizes and
- *    on whether lengths are given. Their blocks' parts pass through the workspace, which
- *    two calls that may overlap on the GPU (two captured graphs among them) cannot share. The
- *    *_workspace_bytes functions depend on the sizes and the dtype alone; they give 0 for T = 0
- *    (the workspace may be NULL then) and SIZE_MAX for an invalid problem.
+ *    tokens, written, not added to: in fp32 throughout, taken in an order that depends on
+ *    the sizes, the dtype, which optional inputs are given (lengths among them) and the
+ *    inputs' strides and alignment; calls alike in all of these give the same bits. Their
+ *    blocks' parts pass through the workspace, which two calls that may overlap on the GPU
+ *    (two captured graphs among them) cannot share. The *_workspace_bytes functions depend
+ *    on the sizes and the dtype alone; they give 0 for T = 0 (the workspace may be NULL
+ *    then) and SIZE_MAX for an invalid problem.
  * ------------------------------------------------------------------------- */
 
 /* Gated linear recurrence: every channel is a state of its own with a decay and an input
