@@ -115,8 +115,8 @@ def recur_fwd(x, decay, rate=None, gate=None, scaling: str = "root", h0=None, le
         h <- a h + m sigmoid(gate) x,  y = h             (m x without a gate)
 
     per token and channel, m by ``scaling``: "root" sqrt(1 - a^2), "complement" 1 - a,
-    "none" 1. x, decay, gate [B,T,D] float32 or bfloat16 (one dtype), strided; rate [D] >=
-    0, h0 and h_final [B,D] float32. ``states`` [B, ceil(T / RECUR_EVERY), D] float32: the
+    "none" 1. x, decay, gate [B,T,D] float32 or bfloat16 (one dtype), strided; rate [D] in
+    0..2^64, h0 and h_final [B,D] float32. ``states`` [B, ceil(T / RECUR_EVERY), D] float32: the
     ones entering every RECUR_EVERY-th token, for recur_bwd. ``final_state=h0`` updates the
     state in place; ``out`` and ``states`` may be passed to reuse buffers."""
     if not output_states:

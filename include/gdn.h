@@ -498,8 +498,10 @@ GDN_API gdn_status gdn_group_norm(const gdn_group_norm_problem *p, const void *x
  * with m = 1 (GDN_RECUR_PLAIN), 1 - a (GDN_RECUR_COMPLEMENT) or sqrt(1 - a^2)
  * (GDN_RECUR_ROOT), and without the sigmoid where gate is NULL.
  *  - x, decay, gate (or NULL) [B,T,D] in `dtype`, each strided; y [B,T,D] in `dtype`; rate
- *    [D] (or NULL) fp32, finite and >= 0 (m of GDN_RECUR_ROOT has no gradient at rate 0:
+ *    [D] (or NULL) fp32, from 0 to 2^64 (m of GDN_RECUR_ROOT has no gradient at rate 0:
  *    taken as 0 there, and for rates below 2^-126); h0, h_final [B,D] fp32.
+ *  - A state that is not finite leaves the later ones of its sequence and channel so, infinite
+ *    or NaN. In the gradients a sigmoid(decay) below 2^-126 counts as that.
  *  - states [B, ceil(T / GDN_RECUR_EVERY), D] fp32 or NULL: state k of a sequence is the one
  *    entering its token k GDN_RECUR_EVERY, written where that token is valid. The backward
  *    pass starts from them.

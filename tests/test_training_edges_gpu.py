@@ -145,6 +145,32 @@ def test_recur_rates_below_the_normal_range():
     assert abs(dx).max() < small and abs(dd).max() < small and abs(dg).max() < small
 
 
+@pytest.mark.parametrize("size", [(2, 6, 24), (2, 70, 24), (2, 45, 33)])
+def test_recur_the_largest_rates(size):
+    """2^64: decays far below 0 on both sides of where their sigmoid counts as 0 or as 2^-126, which moves m
+    by 2^-30 at most (sqrt(2^65 2^-126)) and 1 - a by 2^-62; the tokens behind a sequence pass its state whole."""
+    B, T, D = size
+    i = recur_inputs(*size, F32, 1120, lengths=True)
+    i["rate"].fill_(2.0 ** 64)
+    far = torch.tensor([-float("inf"), -200.0, -100.0, -88.0, -87.0, -80.0, -60.0, -30.0, 0.0, 90.0])
+    inside = torch.isfinite(i["x"])
+    decay = far[torch.randint(0, 10, size, generator=gen(1121))].cuda()
+    i["decay"] = torch.where(inside, decay, torch.full_like(decay, float("nan")))
+    y, h, states = gdn.recur_fwd(**i, output_states=True)
+    want, bound, _ = recur_ref(i)
+    off = 2.0 ** -30 * float(i["x"].nan_to_num(0.0).abs().sum(1).max())
+    checked(dict(y=y, h=h, states=states), want, {k: v + off for k, v in bound.items()}, {})
+    i["decay"] = torch.where(inside, torch.full_like(decay, -float("inf")), i["decay"])
+    y, h, states = gdn.recur_fwd(**i, output_states=True)
+    assert torch.equal(h, i["h0"])
+    dy, dh = torch.zeros_like(y), torch.randn(B, D, generator=gen(1122)).cuda()
+    dx, dd, dg, _, d0 = gdn.recur_bwd(dy, states=states, d_final_state=dh,
+                                      **{k: v for k, v in i.items() if k != "h0"})
+    assert torch.equal(d0, dh)
+    for v in (dx, dd, dg):
+        assert abs(v).max() <= 2.0 ** -24
+
+
 # ----------------------------------------------------------------- every form of gates
 @pytest.mark.parametrize("scaling", ["none", "complement", "root"])
 @pytest.mark.parametrize("gate", [False, True])
