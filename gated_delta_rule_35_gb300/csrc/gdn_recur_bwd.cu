@@ -7,13 +7,13 @@
 //   dx = lam m q,  dgate = lam m q (1 - q) x,  dlog = lam (a h_before + q x dm/dlog a)
 //   ddecay = -dlog rate s (1 - s) (or dlog (1 - a)),  drate = -sum dlog s
 // with dm/dlog a = -a^2 / m for the root, -a for the complement. Four tensors read and three
-// written, the states a thirtieth of that: 14 bytes a value in bf16, against 67 instructions; the
+// written, and a quarter byte of states: 14 bytes a value in bf16, against 67 instructions; the
 // factors are computed twice, since lam needs those of later tokens and registers hold one array.
 //
 // B4 T2048 D4096 bf16: 123 us, 3.89 TB/s (58% of a plain copy's 6.68); T32768 D2048 248 us, 3.85 TB/s;
 // fp32 B4 T2048 D4096 161 us, 5.8 TB/s; D4097 243 us in bf16, 295 in fp32. Ten to twelve warps of 166
-// registers to an SM issue in 56% of the cycles. 128 registers and 16 warps with a ring of one tile: 126 us for 132 then, but 281 for
-// 263 on T32768.
+// registers to an SM issue in 56% of the cycles. 128 registers and 16 warps with a ring of one
+// tile: 126 us for 132 then, but 281 for 263 on T32768.
 #include <utility>
 
 #include "recur.cuh"

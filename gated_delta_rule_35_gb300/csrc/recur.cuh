@@ -65,10 +65,11 @@ __device__ __forceinline__ void sigmoids2(F2 v, F2 &s, F2 &n) {
 
 // a = 2^t and n = 1 - a for t <= 0, both to a few roundings of themselves: with t = k + f, k
 // whole and |f| <= 1/2, a = 2^k + 2^k p and n = (1 - 2^k) - 2^k p, where p = 2^f - 1 is a
-// polynomial in f without a constant term (off by 2.1e-8 of itself at most), so that n keeps its
-// bits where a is next to 1. Below 2^-126 a is 2^-126. The scale comes from the rounded k's bits:
-// by the exponential's instruction, of which a token takes four already, 65 us for 62 (B4 T2048
-// D4096 bf16).
+// polynomial in f without a constant term, so that n keeps its bits where a is next to 1. Of degree
+// 6, the one whose largest error relative to 2^f - 1 is least there, found by Lawson's iteration (least
+// squares, the weights multiplied by the errors each time) and rounded to fp32: off by 2.2e-8 of itself
+// at most. Below 2^-126 a is 2^-126. The scale comes from the rounded k's bits: by the exponential's
+// instruction, of which a token takes four already, 65 us for 62 (B4 T2048 D4096 bf16).
 __device__ __forceinline__ F2 decay_scale2(F2 t, F2 &p) {
     constexpr float shift = 12582912.f;                // 1.5 2^23: rounds to whole numbers
     float k0, k1;
