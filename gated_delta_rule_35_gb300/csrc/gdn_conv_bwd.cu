@@ -11,11 +11,11 @@
 // one (fp32), or the threads of a run copy the aligned 16-byte pieces that their part of a row touches
 // (bf16, whose elements are less than an asynchronous copy moves).
 //
-// B8 T8192 C8192 W4 SiLU bf16: 554 us, 5.82 TB/s (87% of a plain copy's 6.68; the FMA pipe 57%, issue
+// B8 T8192 C8192 W4 SiLU bf16: 555 us, 5.81 TB/s (87% of a plain copy's 6.68; the FMA pipe 57%, issue
 // 60%, four blocks of 126 registers to an SM); 11 us of it are the sums over the 64 blocks of runs.
-// B4 T4096 C4096 bf16 93 us, fp32 140, C4097 202 and 184. A thread to a channel over all tokens:
-// 5161 us. Three blocks of 256 threads (80 registers) would spill: 844 us; eight tokens to a turn
-// 598.
+// B4 T4096 C4096 bf16 90 us (two rounds of blocks, the second two thirds full), fp32 136, C4097 195
+// and 181. A thread to a channel over all tokens: 5161 us. Three blocks of 256 threads (80 registers)
+// would spill: 844 us; eight tokens to a turn 598.
 #include "columns.cuh"
 #include "rows.cuh"
 

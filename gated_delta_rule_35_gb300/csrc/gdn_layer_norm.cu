@@ -14,9 +14,9 @@
 // 65536 x 4096 bf16: 165 us, 6.53 TB/s (98% of a plain copy's 6.68), the gradients 252 us, 6.41 TB/s
 // (96%), 6 us of them the sums over the blocks' rows. A block to a row with every value read three
 // times took 434 and 2189 us; a part of a warp to a row, weight and bias read for each, 246. fp32
-// 32768 x 4096: 177 and 251 us; 65536 x 2560 bf16 130 and 191 (154 and 227 with a power of two of
-// threads to a row); rows of 1003: bf16 60 and 85, fp32 64 and 101 (element by element with 4 elements
-// to a thread: 284 and 142 the norm).
+// 32768 x 4096: 177 and 251 us; 65536 x 2560 bf16 137 and 195 (154 and 227 with a power of two of
+// threads to a row); rows of 1003: bf16 60 and 85, fp32 64 and 101 (4 single channels to a thread, read one by
+// one: 284 and 142 the norm).
 #include "columns.cuh"
 #include "rows.cuh"
 

@@ -9,7 +9,7 @@
 // places, and where there are two the schedulers issue in 70% of the cycles. T32768 D2048, one
 // sequence in clusters of 8: 145 us, 3.70 TB/s; 100 without the exchange, whose barrier of the
 // cluster takes 1.4 us for every 1024 tokens. fp32 B4 T2048 D4096 93 us, 5.8 TB/s. Rows that are not
-// whole pieces (D4097): 123 us in bf16, 163 in fp32. Tiles of 8 tokens to a warp with three times
+// whole pieces (D4097): 123 us in bf16, 164 in fp32. Tiles of 8 tokens to a warp with three times
 // the warps took 66 to 76 us for 64, one with a ring of one tile 64.
 #include <utility>
 

@@ -10,10 +10,10 @@
 // written, and a quarter byte of states: 14 bytes a value in bf16, against 67 instructions; the
 // factors are computed twice, since lam needs those of later tokens and registers hold one array.
 //
-// B4 T2048 D4096 bf16: 123 us, 3.89 TB/s (58% of a plain copy's 6.68); T32768 D2048 248 us, 3.85 TB/s;
-// fp32 B4 T2048 D4096 161 us, 5.8 TB/s; D4097 243 us in bf16, 295 in fp32. Ten to twelve warps of 166
-// registers to an SM issue in 56% of the cycles. 128 registers and 16 warps with a ring of one
-// tile: 126 us for 132 then, but 281 for 263 on T32768.
+// B4 T2048 D4096 bf16: 122 us, 3.92 TB/s (59% of a plain copy's 6.68); T32768 D2048 247 us, 3.87 TB/s;
+// fp32 B4 T2048 D4096 159 us, 5.9 TB/s; D4097 243 us in bf16, 293 in fp32. Nine to twelve warps of
+// 168 registers to an SM issue in 57% of the cycles, 256 blocks on 304 places. 128 registers and 16
+// warps with a ring of one tile: 126 us for 132 then, but 281 for 263 on T32768.
 #include <utility>
 
 #include "recur.cuh"

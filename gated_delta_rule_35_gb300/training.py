@@ -9,8 +9,9 @@ those of include/gdn.h. Inputs marked *strided* may be slices of wider tensors. 
 ([B] int32, on the device) holds the valid tokens of each sequence of a padded batch: rows
 at or past it are not used, add nothing to a gradient, and are not written in the outputs
 (zeros, then, in an output that the call allocates). A backward pass returns gradients; it
-adds to nothing. A buffer for a gradient that the call does not have (of a weight, bias, gate,
-rate or state that is not given) is refused; one whose output_* flag is off is left alone.
+adds to nothing. Autograd records none of these calls: outputs do not require gradients. A
+buffer for a gradient that the call does not have (of a weight, bias, gate, rate or state
+that is not given) is refused; one whose output_* flag is off is left alone.
 """
 from __future__ import annotations
 
